@@ -7,13 +7,16 @@ is missing the call raises instead of falling back to any other code.
 """
 from . import workloads  # noqa: F401  (seeded input generators; no GPU needed)
 
-__all__ = ["forward", "kda_forward", "backward", "decode_step", "forward_workspace_bytes",
-           "backward_workspace_bytes", "library", "CkdaError", "workloads"]
+_BINDING = ("forward", "kda_forward", "backward", "decode_step", "forward_workspace_bytes",
+            "backward_workspace_bytes", "gdr_forward", "gdr_decode_step",
+            "gdr_forward_workspace_bytes", "qk_norm_rotary", "qk_norm_rotary_backward", "rotary",
+            "rotary_frequencies", "library", "CkdaError")
+
+__all__ = [*_BINDING, "workloads"]
 
 
 def __getattr__(name):
-    if name in ("forward", "kda_forward", "backward", "decode_step", "forward_workspace_bytes",
-                "backward_workspace_bytes", "library", "CkdaError"):
+    if name in _BINDING:
         from . import _lib
         return getattr(_lib, name)
     raise AttributeError(name)

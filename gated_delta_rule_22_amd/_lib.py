@@ -9,6 +9,7 @@ call fails, an exception is raised.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -63,6 +64,24 @@ def library() -> ctypes.CDLL:
         lib.ckda_backward_ex.restype = ci
         lib.ckda_decode_step.argtypes = [vp] * 7 + [ci] * 5 + [vp]
         lib.ckda_decode_step.restype = ci
+        ll, fl = ctypes.c_longlong, ctypes.c_float
+        lib.gdr_forward_workspace_bytes.argtypes = [ci] * 8
+        lib.gdr_forward_workspace_bytes.restype = sz
+        lib.gdr_forward.argtypes = [vp] * 7 + [ci] * 8 + [vp, vp, vp, sz, vp]
+        lib.gdr_forward.restype = ci
+        lib.gdr_decode_step.argtypes = [vp] * 7 + [ci, vp] + [ci] * 6 + [vp]
+        lib.gdr_decode_step.restype = ci
+        lib.qk_norm_rotary.argtypes = ([vp] * 6 + [ci] * 5 + [ll] * 2 + [ci] * 2 + [fl] * 3
+                                       + [ci, vp, vp, ll, ll, vp])
+        lib.qk_norm_rotary.restype = ci
+        lib.qk_norm_rotary_backward_workspace_bytes.argtypes = [ci] * 2
+        lib.qk_norm_rotary_backward_workspace_bytes.restype = sz
+        lib.qk_norm_rotary_backward.argtypes = ([vp] * 8 + [ci] * 5 + [ll] * 4 + [ci] * 2
+                                                + [fl] * 3 + [ci, vp, vp, ll, ll]
+                                                + [vp] * 3 + [sz, vp])
+        lib.qk_norm_rotary_backward.restype = ci
+        lib.ckda_rotary.argtypes = ([vp] * 3 + [ci] * 4 + [ll, ci, fl, ci, ci, vp, ll, vp])
+        lib.ckda_rotary.restype = ci
         _lib = lib
     return _lib
 
@@ -260,4 +279,301 @@ def decode_step(q, k, v, g, beta, S, *, out=None):
     st = library().ckda_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S),
                                     _ptr(o), N, H, dk, dv, code, _stream(q.device))
     _check(st, "ckda_decode_step")
+    return o
+
+
+# ------------------------------------------------------------------ gated delta rule
+
+def gdr_forward_workspace_bytes(B, T, Hk, Hv, dk, dv, N, dtype) -> int:
+    code = dtype if isinstance(dtype, int) else (CKDA_BF16 if dtype == torch.bfloat16 else CKDA_F32)
+    return int(library().gdr_forward_workspace_bytes(B, T, Hk, Hv, dk, dv, N, code))
+
+
+def _gdr_sizes(q, k, v, g, beta, cu_seqlens):
+    """Checks the inputs shared by the forward and the backward; their sizes."""
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q, k and v must have 4 dimensions [B, T, heads, channels]")
+    B, T, Hk, dk = q.shape
+    Hv, dv = v.shape[-2:]
+    for t, n in ((q, "q"), (k, "k"), (v, "v")):
+        _need(t, n, q.dtype)
+    _need(k, "k", shape=(B, T, Hk, dk))
+    _need(v, "v", shape=(B, T, Hv, dv))
+    _need(g, "g", torch.float32, (B, T, Hv))
+    _need(beta, "beta", torch.float32, (B, T, Hv))
+    if cu_seqlens is None:
+        return B, T, Hk, Hv, dk, dv, B
+    _need(cu_seqlens, "cu_seqlens", torch.int32)
+    return B, T, Hk, Hv, dk, dv, cu_seqlens.numel() - 1
+
+
+def _same_device(dev, *tensors):
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"all tensors must be on {dev}, got one on {t.device}")
+
+
+def gdr_forward(q, k, v, g, beta, S0=None, cu_seqlens=None, *, out=None, final_state=None,
+                workspace=None, output_final_state=True):
+    """Gated delta rule over a batch of sequences: one log-gate ``g`` per token
+    and head, value heads sharing query/key heads in groups.  Returns
+    ``(o, S_T)``, ``o`` in the type of ``q`` (``S_T`` is None when
+    ``output_final_state`` is False).  See ``gdr_forward`` in include/ckda.h for
+    shapes; ``final_state`` may be ``S0`` itself."""
+    code = _dtype_code(q)
+    B, T, Hk, Hv, dk, dv, N = _gdr_sizes(q, k, v, g, beta, cu_seqlens)
+    if S0 is not None:
+        _need(S0, "S0", torch.float32, (N, Hv, dk, dv))
+    dev = q.device
+    o = out if out is not None else torch.empty((B, T, Hv, dv), dtype=q.dtype, device=dev)
+    _need(o, "out", q.dtype, (B, T, Hv, dv))
+    S_T = None
+    if output_final_state:
+        S_T = final_state if final_state is not None else torch.empty(
+            (N, Hv, dk, dv), dtype=torch.float32, device=dev)
+        _need(S_T, "final_state", torch.float32, (N, Hv, dk, dv))
+    ws_bytes = gdr_forward_workspace_bytes(B, T, Hk, Hv, dk, dv, N, code)
+    if workspace is None or workspace.numel() * workspace.element_size() < ws_bytes:
+        workspace = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=dev)
+    _same_device(dev, k, v, g, beta, S0, cu_seqlens, o, S_T, workspace)
+    with torch.cuda.device(dev):
+        st = library().gdr_forward(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S0),
+                                   _ptr(cu_seqlens), B, T, Hk, Hv, dk, dv, N, code, _ptr(o),
+                                   _ptr(S_T), _ptr(workspace), ws_bytes, _stream(dev))
+    _check(st, "gdr_forward")
+    return o, S_T
+
+
+def gdr_decode_step(q, k, v, g, beta, S, slots=None, *, out=None):
+    """One token of the gated delta rule for N rows; row n's state is
+    ``S[slots[n]]`` (``S[n]`` without ``slots``), updated in place.  Rows whose
+    slot is outside the pool, or named by an earlier row, are padding: their
+    ``o`` is zero.  Returns o ``[N, Hv, dv]`` in the type of ``q``."""
+    if q.dim() != 3 or v.dim() != 3 or S.dim() != 4:
+        raise ValueError("q, k and v must have 3 dimensions [N, heads, channels], S 4")
+    N, Hk, dk = q.shape
+    Hv, dv = v.shape[-2:]
+    code = _dtype_code(q)
+    for t, n in ((q, "q"), (k, "k"), (v, "v")):
+        _need(t, n, q.dtype)
+    _need(k, "k", shape=(N, Hk, dk))
+    _need(v, "v", shape=(N, Hv, dv))
+    _need(g, "g", torch.float32, (N, Hv))
+    _need(beta, "beta", torch.float32, (N, Hv))
+    pool = S.shape[0]
+    _need(S, "S", torch.float32, (pool, Hv, dk, dv))
+    if slots is not None:
+        _need(slots, "slots", torch.int32, (N,))
+    dev = q.device
+    o = out if out is not None else torch.empty((N, Hv, dv), dtype=q.dtype, device=dev)
+    _need(o, "out", q.dtype, (N, Hv, dv))
+    _same_device(dev, k, v, g, beta, S, slots, o)
+    with torch.cuda.device(dev):
+        st = library().gdr_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S),
+                                       _ptr(slots), pool, _ptr(o), N, Hk, Hv, dk, dv, code,
+                                       _stream(dev))
+    _check(st, "gdr_decode_step")
+    return o
+
+
+# ------------------------------------------------------------------ norm and rotation
+
+_NORMS = {"none": 0, "l2": 1, "rms": 2}              # CKDA_NORM_* in include/ckda.h
+_LAYOUTS = {"half": 0, "interleaved": 1}             # CKDA_ROTARY_*
+
+
+def rotary_frequencies(rotary_dim, base=10000.0, *, scaling=None, factor=1.0,
+                       original_length=None, beta_fast=32.0, beta_slow=1.0, device=None):
+    """Angles per position of the ``rotary_dim / 2`` pairs (fp64, radians), and
+    the scale of the rotated channels that goes with them.
+
+    ``scaling`` stretches the context ``factor``-fold: ``"linear"`` divides all
+    angles; ``"base"`` raises the base so that the slowest pair turns ``factor``
+    times slower and the fastest one is unchanged; ``"ramp"`` divides the angles
+    of pairs that turn less than ``beta_slow`` times within ``original_length``
+    positions, keeps those that turn more than ``beta_fast`` times, blends in
+    between, and scales by ``0.1 ln(factor) + 1``."""
+    if rotary_dim < 2 or rotary_dim % 2:
+        raise ValueError("rotary_dim must be even and positive")
+    if factor < 1.0 or base <= 1.0:
+        raise ValueError("factor must be at least 1 and base above 1")
+    i = torch.arange(0, rotary_dim, 2, dtype=torch.float64)
+    scale = 1.0
+    if scaling == "base":
+        if rotary_dim < 4:
+            raise ValueError("scaling='base' needs rotary_dim of at least 4")
+        base = base * factor ** (rotary_dim / (rotary_dim - 2))
+    freqs = base ** (-i / rotary_dim)
+    if scaling == "linear":
+        freqs = freqs / factor
+    elif scaling == "ramp":
+        if original_length is None or original_length < 1 or not beta_fast > beta_slow > 0:
+            raise ValueError("scaling='ramp' needs original_length and beta_fast > beta_slow > 0")
+        # index of the pair that turns n times within the original length
+        def pair(n):
+            return (rotary_dim * math.log(original_length / (n * 2 * math.pi))
+                    / (2 * math.log(base)))
+        lo = max(math.floor(pair(beta_fast)), 0)
+        hi = min(math.ceil(pair(beta_slow)), rotary_dim - 1)
+        ramp = ((i / 2 - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+        freqs = freqs / factor * ramp + freqs * (1 - ramp)
+        scale = 0.1 * math.log(factor) + 1.0
+    elif scaling not in (None, "base"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    return freqs.to(device), scale
+
+
+def _rows(t, name, dtype=None, lead=None, d=None):
+    """Rows [..., heads, d] whose heads are dense and whose tokens are one
+    distance apart; (heads, tokens, distance in elements)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dim() < 3:
+        raise ValueError(f"{name} must have at least 3 dimensions [..., heads, channels]")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if lead is not None and tuple(t.shape[:-2]) != tuple(lead):
+        raise ValueError(f"{name} must have leading dimensions {tuple(lead)}, got {tuple(t.shape)}")
+    if d is not None and t.shape[-1] != d:
+        raise ValueError(f"{name} must have {d} channels, got {t.shape[-1]}")
+    heads, width = t.shape[-2:]
+    tokens = t.shape[:-2].numel()
+    if t.numel() == 0:
+        return heads, tokens, heads * width
+    if (width > 1 and t.stride(-1) != 1) or (heads > 1 and t.stride(-2) != width):
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    ld = None
+    span = 1                            # tokens that the dimensions so far cover
+    for n, s in zip(reversed(t.shape[:-2]), reversed(t.stride()[:-2])):
+        if n == 1:
+            continue
+        if ld is None:
+            ld = s
+        elif s != ld * span:
+            raise ValueError(f"{name}: tokens must be evenly spaced")
+        span *= n
+    ld = heads * width if ld is None else ld
+    if ld < heads * width:
+        raise ValueError(f"{name}: tokens must not overlap")
+    return heads, tokens, ld
+
+
+def _angles(positions, freqs, lead, d):
+    if freqs is None:
+        return 0, None
+    if positions is None:
+        raise ValueError("positions are needed with freqs")
+    _need(positions, "positions", torch.int32, lead)
+    _need(freqs, "freqs", torch.float64)
+    if freqs.dim() != 1 or not 0 < 2 * freqs.numel() <= d:
+        raise ValueError(f"freqs must have 1 to {d // 2} entries, got {tuple(freqs.shape)}")
+    return 2 * freqs.numel(), positions
+
+
+def _choice(table, value, name):
+    if value not in table:
+        raise ValueError(f"{name} must be one of {sorted(table)}, got {value!r}")
+    return table[value]
+
+
+def qk_norm_rotary(q, k, positions=None, freqs=None, *, norm="rms", q_weight=None, k_weight=None,
+                   eps=1e-6, layout="half", q_scale=1.0, rotary_scale=1.0, q_out=None,
+                   k_out=None):
+    """Normalises every head of ``q`` [..., Hq, d] and ``k`` [..., Hk, d]
+    (``norm`` is "rms", "l2" or "none", with an optional weight each), rotates
+    the first ``2 len(freqs)`` channels by ``positions * freqs`` and multiplies
+    ``q`` by ``q_scale``, in one pass.  ``q`` and ``k`` may be slices of one
+    projection; results are dense unless ``q_out`` / ``k_out`` (which may be
+    ``q`` / ``k``) are given.  See ``qk_norm_rotary`` in include/ckda.h and
+    :func:`rotary_frequencies`."""
+    code = _dtype_code(q)
+    Hq, tokens, ldq = _rows(q, "q")
+    lead, d = tuple(q.shape[:-2]), q.shape[-1]
+    Hk, _, ldk = _rows(k, "k", q.dtype, lead, d)
+    rd, positions = _angles(positions, freqs, lead, d)
+    for t, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if t is not None:
+            _need(t, n, torch.float32, (d,))
+    dev = q.device
+    qo = q_out if q_out is not None else torch.empty(q.shape, dtype=q.dtype, device=dev)
+    ko = k_out if k_out is not None else torch.empty(k.shape, dtype=q.dtype, device=dev)
+    hq, _, ldqo = _rows(qo, "q_out", q.dtype, lead, d)
+    hk, _, ldko = _rows(ko, "k_out", q.dtype, lead, d)
+    if (hq, hk) != (Hq, Hk):
+        raise ValueError("q_out and k_out must have the heads of q and k")
+    _same_device(dev, k, positions, freqs, q_weight, k_weight, qo, ko)
+    with torch.cuda.device(dev):
+        st = library().qk_norm_rotary(
+            _ptr(q), _ptr(k), _ptr(positions), _ptr(freqs), _ptr(q_weight), _ptr(k_weight),
+            tokens, Hq, Hk, d, rd, ldq, ldk, _choice(_NORMS, norm, "norm"),
+            _choice(_LAYOUTS, layout, "layout"), eps, q_scale, rotary_scale, code, _ptr(qo),
+            _ptr(ko), ldqo, ldko, _stream(dev))
+    _check(st, "qk_norm_rotary")
+    return qo, ko
+
+
+def qk_norm_rotary_backward(dq_out, dk_out, q, k, positions=None, freqs=None, *, norm="rms",
+                            q_weight=None, k_weight=None, eps=1e-6, layout="half", q_scale=1.0,
+                            rotary_scale=1.0, dq=None, dk=None, workspace=None):
+    """Gradients of :func:`qk_norm_rotary` for the gradients ``dq_out``,
+    ``dk_out`` of its results: ``(dq, dk, dq_weight, dk_weight)``, the weights'
+    fp32 (None where there is no weight).  ``dq`` / ``dk`` may be slices of the
+    projection's gradient."""
+    code = _dtype_code(q)
+    Hq, tokens, ldq = _rows(q, "q")
+    lead, d = tuple(q.shape[:-2]), q.shape[-1]
+    Hk, _, ldk = _rows(k, "k", q.dtype, lead, d)
+    uq, _, lddq = _rows(dq_out, "dq_out", q.dtype, lead, d)
+    uk, _, lddk = _rows(dk_out, "dk_out", q.dtype, lead, d)
+    rd, positions = _angles(positions, freqs, lead, d)
+    for t, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if t is not None:
+            _need(t, n, torch.float32, (d,))
+    dev = q.device
+    gq = dq if dq is not None else torch.empty(q.shape, dtype=q.dtype, device=dev)
+    gk = dk if dk is not None else torch.empty(k.shape, dtype=q.dtype, device=dev)
+    oq, _, ldgq = _rows(gq, "dq", q.dtype, lead, d)
+    ok, _, ldgk = _rows(gk, "dk", q.dtype, lead, d)
+    if (uq, uk) != (Hq, Hk) or (oq, ok) != (Hq, Hk):
+        raise ValueError("gradients must have the heads of q and k")
+    dwq = None if q_weight is None else torch.empty(d, dtype=torch.float32, device=dev)
+    dwk = None if k_weight is None else torch.empty(d, dtype=torch.float32, device=dev)
+    ws_bytes = 0
+    if q_weight is not None or k_weight is not None:
+        ws_bytes = int(library().qk_norm_rotary_backward_workspace_bytes(tokens, d))
+        if workspace is None or workspace.numel() * workspace.element_size() < ws_bytes:
+            workspace = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=dev)
+    _same_device(dev, k, dq_out, dk_out, positions, freqs, q_weight, k_weight, gq, gk, workspace)
+    with torch.cuda.device(dev):
+        st = library().qk_norm_rotary_backward(
+            _ptr(dq_out), _ptr(dk_out), _ptr(q), _ptr(k), _ptr(positions), _ptr(freqs),
+            _ptr(q_weight), _ptr(k_weight), tokens, Hq, Hk, d, rd, lddq, lddk, ldq, ldk,
+            _choice(_NORMS, norm, "norm"), _choice(_LAYOUTS, layout, "layout"), eps, q_scale,
+            rotary_scale, code, _ptr(gq), _ptr(gk), ldgq, ldgk, _ptr(dwq), _ptr(dwk),
+            _ptr(workspace), ws_bytes, _stream(dev))
+    _check(st, "qk_norm_rotary_backward")
+    return gq, gk, dwq, dwk
+
+
+def rotary(x, positions, freqs, *, layout="half", rotary_scale=1.0, inverse=False, out=None):
+    """Rotates the first ``2 len(freqs)`` channels of every head of ``x``
+    [..., H, d] by ``positions * freqs``; ``inverse`` by the opposite angle (the
+    backward).  ``out`` may be ``x``.  See ``ckda_rotary`` in include/ckda.h."""
+    code = _dtype_code(x)
+    H, tokens, ldx = _rows(x, "x")
+    lead, d = tuple(x.shape[:-2]), x.shape[-1]
+    if freqs is None:
+        raise ValueError("freqs are needed")
+    rd, positions = _angles(positions, freqs, lead, d)
+    dev = x.device
+    o = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=dev)
+    ho, _, ldo = _rows(o, "out", x.dtype, lead, d)
+    if ho != H:
+        raise ValueError("out must have the heads of x")
+    _same_device(dev, positions, freqs, o)
+    with torch.cuda.device(dev):
+        st = library().ckda_rotary(_ptr(x), _ptr(positions), _ptr(freqs), tokens, H, d, rd, ldx,
+                                   _choice(_LAYOUTS, layout, "layout"), rotary_scale,
+                                   int(inverse), code, _ptr(o), ldo, _stream(dev))
+    _check(st, "ckda_rotary")
     return o

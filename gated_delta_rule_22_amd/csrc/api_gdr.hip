@@ -1,0 +1,321 @@
+// C-ABI entry points of the gated delta rule and of the norm and rotation of
+// queries and keys: argument validation, workspace layout, dispatch.  As in
+// the other entry points every check runs on the host before anything is
+// enqueued.
+#include "api_util.h"
+
+namespace ckda {
+size_t f64_record_bytes(int dk, int dv);   // fwd_f64.hip
+}
+
+using namespace ckda;
+
+namespace {
+
+struct Span { const void *p; size_t n; };
+
+int gdr_shape_status(int B, int T, int Hk, int Hv, int dk, int dv, int N, int in_dtype,
+                     bool packed) {
+  if (in_dtype != CKDA_BF16 && in_dtype != CKDA_F32) return CKDA_ERR_DTYPE;
+  if (B < 1 || T < 0 || Hk < 1 || Hv < 1 || N < 1 || !dims_ok(dk) || !dims_ok(dv))
+    return CKDA_ERR_SHAPE;
+  if (Hv % Hk != 0) return CKDA_ERR_SHAPE;
+  if ((long long)B * T * Hv >= (1LL << 31)) return CKDA_ERR_SHAPE;
+  if ((long long)N * Hv >= (1LL << 28)) return CKDA_ERR_SHAPE;
+  if ((long long)Hv * (dk > dv ? dk : dv) * 4 * kChunk >= (1LL << 31)) return CKDA_ERR_SHAPE;
+  if (packed ? B != 1 : N != B) return CKDA_ERR_SHAPE;
+  return CKDA_OK;
+}
+
+// Chunks over all sequences, at most: uniform rows give B ceil(T / 64), packed
+// sequences add a partial chunk each.
+size_t chunks_ub(int B, int T, int N) {
+  const size_t per_row = ((size_t)T + kChunk - 1) / kChunk;
+  return N == B && B > 1 ? (size_t)B * per_row : per_row + (size_t)N;
+}
+
+struct GdrLayout {
+  size_t rec, total;                     // byte offsets; the sequence table is first
+  size_t n_chunks;
+};
+
+GdrLayout gdr_fwd_layout(int B, int T, int Hv, int N, int in_dtype) {
+  GdrLayout L{};
+  L.n_chunks = chunks_ub(B, T, N);
+  L.rec = align256(sizeof(int32_t) * (4 * (size_t)N + 1));
+  L.total = L.rec + (in_dtype == CKDA_BF16 ? L.n_chunks * Hv * gdr_forward_rec_bytes() : 0);
+  return L;
+}
+
+// Two row sets of `rows` rows, `width` bytes each, `ld` bytes apart, overlap:
+// as whole spans, unless both step by the same distance and keep to columns
+// of their own (the heads of q and of k in one packed projection).
+bool rows_overlap(const void *a, size_t wa, size_t lda, const void *b, size_t wb, size_t ldb,
+                  size_t rows) {
+  if (!a || !b || rows == 0 || wa == 0 || wb == 0) return false;
+  if (!overlaps(a, (rows - 1) * lda + wa, b, (rows - 1) * ldb + wb)) return false;
+  if (lda != ldb) return true;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  const size_t d = x >= y ? (x - y) % lda : (lda - (y - x) % lda) % lda;
+  return !(d >= wb && d + wa <= lda);
+}
+
+}  // namespace
+
+extern "C" size_t gdr_forward_workspace_bytes(int B, int T, int Hk, int Hv, int dk, int dv, int N,
+                                              int in_dtype) {
+  if (gdr_shape_status(B, T, Hk, Hv, dk, dv, N, in_dtype, B == 1 && N != B) != CKDA_OK) return 0;
+  return gdr_fwd_layout(B, T, Hv, N, in_dtype).total;
+}
+
+extern "C" int gdr_forward(const void *q, const void *k, const void *v, const float *g,
+                           const float *beta, const float *S0, const int32_t *cu_seqlens, int B,
+                           int T, int Hk, int Hv, int dk, int dv, int N, int in_dtype, void *o,
+                           float *S_T, void *workspace, size_t workspace_bytes, void *stream) {
+  const bool packed = cu_seqlens != nullptr;
+  if (int s = gdr_shape_status(B, T, Hk, Hv, dk, dv, N, in_dtype, packed)) return s;
+  const size_t rows = (size_t)B * T;
+  if (rows > 0 && (!q || !k || !v || !g || !beta || !o)) return CKDA_ERR_NULL;
+  const void *ptrs[] = {q, k, v, S0, o, S_T, workspace};
+  for (const void *p : ptrs)
+    if (p && !aligned16(p)) return CKDA_ERR_ALIGN;
+  if ((g && !aligned4(g)) || (beta && !aligned4(beta)) || (cu_seqlens && !aligned4(cu_seqlens)))
+    return CKDA_ERR_ALIGN;
+  const size_t e = in_dtype == CKDA_BF16 ? 2 : 4;
+  const size_t st_bytes = (size_t)N * Hv * dk * dv * 4, o_bytes = rows * Hv * dv * e;
+  const Span ins[] = {{q, rows * Hk * dk * e}, {k, rows * Hk * dk * e}, {v, o_bytes},
+                      {g, rows * Hv * 4},      {beta, rows * Hv * 4},
+                      {cu_seqlens, ((size_t)N + 1) * 4}};
+  const GdrLayout L = gdr_fwd_layout(B, T, Hv, N, in_dtype);
+  for (const Span &s : ins)
+    if (overlaps(o, o_bytes, s.p, s.n) || overlaps(S_T, st_bytes, s.p, s.n) ||
+        overlaps(workspace, L.total, s.p, s.n))
+      return CKDA_ERR_ALIAS;
+  if (overlaps(o, o_bytes, S0, st_bytes) || overlaps(o, o_bytes, S_T, st_bytes) ||
+      (S_T != S0 && overlaps(S_T, st_bytes, S0, st_bytes)) ||
+      overlaps(workspace, L.total, o, o_bytes) || overlaps(workspace, L.total, S_T, st_bytes) ||
+      overlaps(workspace, L.total, S0, st_bytes))
+    return CKDA_ERR_ALIAS;
+  if (!workspace || workspace_bytes < L.total) return CKDA_ERR_WORKSPACE;
+
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  if (int s = debug_prologue(cu_seqlens, N, T, workspace, L.total, st)) return s;
+  GdrArgs a{};
+  a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.S0 = S0;
+  a.tab = seq_table(workspace, N);
+  a.n_chunks_ub = L.n_chunks;
+  a.N = N; a.Hk = Hk; a.Hv = Hv; a.dk = dk; a.dv = dv;
+  a.o = o; a.S_T = S_T;
+  if (launch_seq_table(cu_seqlens, B, T, N, a.tab, st) != hipSuccess) return CKDA_ERR_LAUNCH;
+  const hipError_t r = in_dtype == CKDA_BF16
+                           ? launch_gdr_forward(a, static_cast<char *>(workspace) + L.rec, st)
+                           : launch_gdr_token(a, in_dtype, st);
+  return r == hipSuccess ? CKDA_OK : CKDA_ERR_LAUNCH;
+}
+
+extern "C" int gdr_decode_step(const void *q, const void *k, const void *v, const float *g,
+                               const float *beta, float *S, const int32_t *slots, int pool,
+                               void *o, int N, int Hk, int Hv, int dk, int dv, int in_dtype,
+                               void *stream) {
+  if (in_dtype != CKDA_BF16 && in_dtype != CKDA_F32) return CKDA_ERR_DTYPE;
+  if (N < 1 || pool < 1 || Hk < 1 || Hv < 1 || Hv % Hk != 0 || !dims_ok(dk) || !dims_ok(dv))
+    return CKDA_ERR_SHAPE;
+  if (!slots && pool != N) return CKDA_ERR_SHAPE;
+  if ((long long)N * Hv >= (1LL << 31) || (long long)pool * Hv >= (1LL << 31))
+    return CKDA_ERR_SHAPE;
+  if (!q || !k || !v || !g || !beta || !S || !o) return CKDA_ERR_NULL;
+  const void *ptrs[] = {q, k, v, S, o};
+  for (const void *p : ptrs)
+    if (!aligned16(p)) return CKDA_ERR_ALIGN;
+  if (!aligned4(g) || !aligned4(beta) || (slots && !aligned4(slots))) return CKDA_ERR_ALIGN;
+  const size_t e = in_dtype == CKDA_BF16 ? 2 : 4, n = (size_t)N;
+  const size_t s_bytes = (size_t)pool * Hv * dk * dv * 4, o_bytes = n * Hv * dv * e;
+  const Span ins[] = {{q, n * Hk * dk * e}, {k, n * Hk * dk * e}, {v, o_bytes},
+                      {g, n * Hv * 4},      {beta, n * Hv * 4},   {slots, n * 4}};
+  if (overlaps(o, o_bytes, S, s_bytes)) return CKDA_ERR_ALIAS;
+  for (const Span &s : ins)
+    if (overlaps(S, s_bytes, s.p, s.n) || overlaps(o, o_bytes, s.p, s.n)) return CKDA_ERR_ALIAS;
+  const hipError_t r = launch_gdr_step(q, k, v, g, beta, S, slots, pool, o, N, Hk, Hv, dk, dv,
+                                       in_dtype, static_cast<hipStream_t>(stream));
+  return r == hipSuccess ? CKDA_OK : CKDA_ERR_LAUNCH;
+}
+
+// ---------------------------------------------------------------- norm and rotation
+namespace {
+
+int rows_status(int tokens, int Hq, int Hk, int d, int rd, int norm, int layout, int in_dtype) {
+  if (in_dtype != CKDA_BF16 && in_dtype != CKDA_F32) return CKDA_ERR_DTYPE;
+  if (tokens < 0 || Hq < 0 || Hk < 0 || Hq + (long long)Hk < 1 || Hq > 65535 || Hk > 65535)
+    return CKDA_ERR_SHAPE;
+  if (d < 2 || d > 256 || d % 2 || rd < 0 || rd > d || rd % 2) return CKDA_ERR_SHAPE;
+  if (norm < CKDA_NORM_NONE || norm > CKDA_NORM_RMS) return CKDA_ERR_SHAPE;
+  if (layout != CKDA_ROTARY_HALF && layout != CKDA_ROTARY_INTERLEAVED) return CKDA_ERR_SHAPE;
+  return CKDA_OK;
+}
+
+bool aligned_to(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+struct Rows { const void *p; int H; long long ld; };
+
+// Rows of H heads: the pointer is there if there is anything to read, element
+// aligned, and rows do not run into each other.
+int check_rows(const Rows &r, int tokens, int d, size_t e) {
+  if (r.H == 0 || tokens == 0) return CKDA_OK;
+  if (!r.p) return CKDA_ERR_NULL;
+  if (r.ld < (long long)r.H * d) return CKDA_ERR_SHAPE;
+  if (r.ld > (1LL << 40)) return CKDA_ERR_SHAPE;
+  return aligned_to(r.p, e) ? CKDA_OK : CKDA_ERR_ALIGN;
+}
+
+bool meet(const Rows &a, const Rows &b, int tokens, int d, size_t e) {
+  return rows_overlap(a.p, (size_t)a.H * d * e, (size_t)a.ld * e, b.p, (size_t)b.H * d * e,
+                      (size_t)b.ld * e, tokens);
+}
+bool meet(const Rows &a, const void *p, size_t n, int tokens, int d, size_t e) {
+  return tokens > 0 && a.H > 0 &&
+         overlaps(a.p, ((size_t)(tokens - 1) * a.ld + (size_t)a.H * d) * e, p, n);
+}
+bool same(const Rows &a, const Rows &b) { return a.p == b.p && a.ld == b.ld && a.H == b.H; }
+
+RotaryArgs rotary_args(int tokens, int Hq, int Hk, int d, int rd, const int32_t *pos,
+                       const double *freqs, int norm, int layout, float eps, float q_scale,
+                       float rotary_scale) {
+  RotaryArgs a{};
+  a.tokens = tokens; a.Hq = Hq; a.Hk = Hk; a.d = d; a.rd = rd;
+  a.pos = pos; a.freqs = freqs;
+  a.norm = norm != CKDA_NORM_NONE;
+  a.norm_scale = norm == CKDA_NORM_RMS ? 1.f / d : 1.f;
+  a.half = layout == CKDA_ROTARY_HALF;
+  a.eps = eps; a.q_scale = q_scale; a.rotary_scale = rotary_scale;
+  return a;
+}
+
+int angle_status(int tokens, int rd, const int32_t *pos, const double *freqs) {
+  if (rd == 0 || tokens == 0) return CKDA_OK;
+  if (!pos || !freqs) return CKDA_ERR_NULL;
+  return aligned4(pos) && aligned_to(freqs, 8) ? CKDA_OK : CKDA_ERR_ALIGN;
+}
+
+}  // namespace
+
+extern "C" int qk_norm_rotary(const void *q, const void *k, const int32_t *positions,
+                              const double *freqs, const float *q_weight, const float *k_weight,
+                              int tokens, int Hq, int Hk, int d, int rd, long long ldq,
+                              long long ldk, int norm, int layout, float eps, float q_scale,
+                              float rotary_scale, int in_dtype, void *q_out, void *k_out,
+                              long long ldqo, long long ldko, void *stream) {
+  if (int s = rows_status(tokens, Hq, Hk, d, rd, norm, layout, in_dtype)) return s;
+  const size_t e = in_dtype == CKDA_BF16 ? 2 : 4;
+  const Rows in[2] = {{q, Hq, ldq}, {k, Hk, ldk}}, out[2] = {{q_out, Hq, ldqo}, {k_out, Hk, ldko}};
+  for (int i = 0; i < 2; ++i) {
+    if (int s = check_rows(in[i], tokens, d, e)) return s;
+    if (int s = check_rows(out[i], tokens, d, e)) return s;
+  }
+  if (int s = angle_status(tokens, rd, positions, freqs)) return s;
+  if ((q_weight && !aligned4(q_weight)) || (k_weight && !aligned4(k_weight)))
+    return CKDA_ERR_ALIGN;
+  const Span small[] = {{positions, rd ? (size_t)tokens * 4 : 0}, {freqs, (size_t)rd / 2 * 8},
+                        {q_weight, (size_t)d * 4}, {k_weight, (size_t)d * 4}};
+  for (int i = 0; i < 2; ++i) {
+    if (!out[i].H || !tokens) continue;
+    for (const Span &s : small)
+      if (meet(out[i], s.p, s.n, tokens, d, e)) return CKDA_ERR_ALIAS;
+    for (int j = 0; j < 2; ++j)          // q_out may be q itself, k_out k itself
+      if (in[j].H && !(i == j && same(out[i], in[j])) && meet(out[i], in[j], tokens, d, e))
+        return CKDA_ERR_ALIAS;
+  }
+  if (Hq && Hk && meet(out[0], out[1], tokens, d, e)) return CKDA_ERR_ALIAS;
+  RotaryArgs a = rotary_args(tokens, Hq, Hk, d, rd, positions, freqs, norm, layout, eps, q_scale,
+                             rotary_scale);
+  a.q = q; a.k = k; a.ldq = ldq; a.ldk = ldk;
+  a.qo = q_out; a.ko = k_out; a.ldqo = ldqo; a.ldko = ldko;
+  a.wq = q_weight; a.wk = k_weight;
+  return launch_rotary(a, in_dtype, false, static_cast<hipStream_t>(stream)) == hipSuccess
+             ? CKDA_OK : CKDA_ERR_LAUNCH;
+}
+
+extern "C" size_t qk_norm_rotary_backward_workspace_bytes(int tokens, int d) {
+  if (tokens < 0 || d < 2 || d > 256 || d % 2) return 0;
+  return (size_t)rotary_bwd_groups(tokens) * 2 * d * 4;
+}
+
+extern "C" int qk_norm_rotary_backward(
+    const void *dq_out, const void *dk_out, const void *q, const void *k, const int32_t *positions,
+    const double *freqs, const float *q_weight, const float *k_weight, int tokens, int Hq, int Hk,
+    int d, int rd, long long lddq, long long lddk, long long ldq, long long ldk, int norm,
+    int layout, float eps, float q_scale, float rotary_scale, int in_dtype, void *dq, void *d_k,
+    long long ldgq, long long ldgk, float *dq_weight, float *dk_weight, void *workspace,
+    size_t workspace_bytes, void *stream) {
+  if (int s = rows_status(tokens, Hq, Hk, d, rd, norm, layout, in_dtype)) return s;
+  const size_t e = in_dtype == CKDA_BF16 ? 2 : 4;
+  const Rows in[4] = {{q, Hq, ldq}, {k, Hk, ldk}, {dq_out, Hq, lddq}, {dk_out, Hk, lddk}};
+  const Rows out[2] = {{dq, Hq, ldgq}, {d_k, Hk, ldgk}};
+  for (const Rows &r : in)
+    if (int s = check_rows(r, tokens, d, e)) return s;
+  for (const Rows &r : out)
+    if (int s = check_rows(r, tokens, d, e)) return s;
+  if (int s = angle_status(tokens, rd, positions, freqs)) return s;
+  // A weight and its gradient come together.
+  if ((q_weight != nullptr) != (dq_weight != nullptr) ||
+      (k_weight != nullptr) != (dk_weight != nullptr))
+    return CKDA_ERR_NULL;
+  const void *fl[] = {q_weight, k_weight, dq_weight, dk_weight};
+  for (const void *p : fl)
+    if (p && !aligned4(p)) return CKDA_ERR_ALIGN;
+  if (workspace && !aligned16(workspace)) return CKDA_ERR_ALIGN;
+  const size_t need = qk_norm_rotary_backward_workspace_bytes(tokens, d), w = (size_t)d * 4;
+  const Span small[] = {{positions, rd ? (size_t)tokens * 4 : 0}, {freqs, (size_t)rd / 2 * 8},
+                        {q_weight, w}, {k_weight, w}};
+  const Span flat[] = {{dq_weight, w}, {dk_weight, w}, {workspace, need}};
+  for (int i = 0; i < 2; ++i) {
+    if (!out[i].H || !tokens) continue;
+    for (const Span &s : small)
+      if (meet(out[i], s.p, s.n, tokens, d, e)) return CKDA_ERR_ALIAS;
+    for (const Span &s : flat)
+      if (meet(out[i], s.p, s.n, tokens, d, e)) return CKDA_ERR_ALIAS;
+    for (const Rows &r : in)
+      if (r.H && meet(out[i], r, tokens, d, e)) return CKDA_ERR_ALIAS;
+  }
+  if (Hq && Hk && meet(out[0], out[1], tokens, d, e)) return CKDA_ERR_ALIAS;
+  for (int i = 0; i < 3; ++i) {
+    for (const Span &s : small)
+      if (overlaps(flat[i].p, flat[i].n, s.p, s.n)) return CKDA_ERR_ALIAS;
+    for (const Rows &r : in)
+      if (meet(r, flat[i].p, flat[i].n, tokens, d, e)) return CKDA_ERR_ALIAS;
+    for (int j = i + 1; j < 3; ++j)
+      if (overlaps(flat[i].p, flat[i].n, flat[j].p, flat[j].n)) return CKDA_ERR_ALIAS;
+  }
+  if ((q_weight || k_weight) && (!workspace || workspace_bytes < need)) return CKDA_ERR_WORKSPACE;
+  if (tokens == 0 && !q_weight && !k_weight) return CKDA_OK;
+  RotaryArgs a = rotary_args(tokens, Hq, Hk, d, rd, positions, freqs, norm, layout, eps, q_scale,
+                             rotary_scale);
+  a.q = q; a.k = k; a.ldq = ldq; a.ldk = ldk;
+  a.dq = dq_out; a.dk = dk_out; a.lddq = lddq; a.lddk = lddk;
+  a.qo = dq; a.ko = d_k; a.ldqo = ldgq; a.ldko = ldgk;
+  a.wq = q_weight; a.wk = k_weight; a.dwq = dq_weight; a.dwk = dk_weight;
+  a.partial = static_cast<float *>(workspace);
+  return launch_rotary(a, in_dtype, true, static_cast<hipStream_t>(stream)) == hipSuccess
+             ? CKDA_OK : CKDA_ERR_LAUNCH;
+}
+
+extern "C" int ckda_rotary(const void *x, const int32_t *positions, const double *freqs,
+                           int tokens, int H, int d, int rd, long long ldx, int layout,
+                           float rotary_scale, int inverse, int in_dtype, void *out,
+                           long long ldo, void *stream) {
+  if (int s = rows_status(tokens, H, 0, d, rd, CKDA_NORM_NONE, layout, in_dtype)) return s;
+  const size_t e = in_dtype == CKDA_BF16 ? 2 : 4;
+  const Rows in = {x, H, ldx}, res = {out, H, ldo};
+  if (int s = check_rows(in, tokens, d, e)) return s;
+  if (int s = check_rows(res, tokens, d, e)) return s;
+  if (int s = angle_status(tokens, rd, positions, freqs)) return s;
+  if (!same(in, res) && meet(res, in, tokens, d, e)) return CKDA_ERR_ALIAS;
+  if (meet(res, positions, rd ? (size_t)tokens * 4 : 0, tokens, d, e) ||
+      meet(res, freqs, (size_t)rd / 2 * 8, tokens, d, e))
+    return CKDA_ERR_ALIAS;
+  RotaryArgs a = rotary_args(tokens, H, 0, d, rd, positions, freqs, CKDA_NORM_NONE, layout, 0.f,
+                             1.f, rotary_scale);
+  a.q = x; a.ldq = ldx; a.qo = out; a.ldqo = ldo;
+  a.inverse = inverse != 0;
+  return launch_rotary(a, in_dtype, false, static_cast<hipStream_t>(stream)) == hipSuccess
+             ? CKDA_OK : CKDA_ERR_LAUNCH;
+}

@@ -100,4 +100,49 @@ hipError_t launch_bwd_f64(const void *q, const void *k, const void *v, const flo
                           float *dbeta, float *dS0, int signed_gates, int l2norm,
                           hipStream_t stream);
 
+// ---------------------------------------------------------------- gated delta rule
+// One log-gate per (token, head); Hv value heads share Hk query/key heads in
+// groups of Hv / Hk.
+struct GdrArgs {
+    const void *q, *k, *v;
+    const float *g, *beta, *S0;
+    SeqTable tab;
+    size_t n_chunks_ub;
+    int N, Hk, Hv, dk, dv;
+    void *o;
+    float *S_T;
+};
+hipError_t launch_gdr_step(const void *q, const void *k, const void *v, const float *g,
+                           const float *beta, float *S, const int32_t *slots, int pool, void *o,
+                           int N, int Hk, int Hv, int dk, int dv, int in_dtype,
+                           hipStream_t stream);
+// Token by token, fp32 arithmetic, any input type.
+hipError_t launch_gdr_token(const GdrArgs &a, int in_dtype, hipStream_t stream);
+// Chunkwise on bf16 matrix cores (bf16 inputs): `rec` holds
+// gdr_forward_rec_bytes() for every chunk and value head.
+size_t gdr_forward_rec_bytes();
+hipError_t launch_gdr_forward(const GdrArgs &a, void *rec, hipStream_t stream);
+// fp32 inputs' backward: layouts to and from the per-channel fp64 backward.
+hipError_t launch_gdr_expand(const float *q, const float *k, const float *g, size_t rows, int Hk,
+                             int Hv, int dk, float *qx, float *kx, float *gx, hipStream_t stream);
+hipError_t launch_gdr_collect(const float *dqx, const float *dkx, const float *dgx,
+                              const float *g, SeqTable tab, int N, size_t rows, int Hk, int Hv,
+                              int dk, float *dq, float *dk_out, float *dg, hipStream_t stream);
+
+// ---------------------------------------------------------------- norm and rotation
+struct RotaryArgs {
+    const void *q, *k, *dq, *dk;         // rows; upstream gradients (backward)
+    void *qo, *ko;                       // results (backward: gradients of q, k)
+    size_t ldq, ldk, lddq, lddk, ldqo, ldko;   // elements from token to token
+    const int32_t *pos;
+    const double *freqs;                 // radians per position, rd / 2 of them
+    const float *wq, *wk;
+    float *dwq, *dwk, *partial;
+    int tokens, Hq, Hk, d, rd, lanes;
+    int norm, half, inverse;             // norm: 0 none, else rows are normalised
+    float norm_scale, eps, q_scale, rotary_scale;   // norm_scale: 1/d (rms) or 1 (l2)
+};
+int rotary_bwd_groups(int tokens);       // workspace rows of 2 d floats
+hipError_t launch_rotary(const RotaryArgs &a, int in_dtype, bool backward, hipStream_t stream);
+
 }  // namespace ckda

@@ -1,0 +1,206 @@
+// Shared pieces of the chunkwise gated delta rule on bf16 matrix cores.
+//
+// One 16x16x32 MFMA contracts 32 indices: lane l gives row (or column) l % 16
+// of its operand and the 8 contracted values of quarter h = l / 16, and gets
+// column l % 16 and rows 4h .. 4h + 3 of the result.  Which 8 of the 32
+// indices a quarter holds is free as long as both operands agree; here slot e
+// of quarter h is index 16 (e / 4) + 4h + e % 4.  With that order two result
+// tiles (rows 0-15 and 16-31) ARE an operand of the next product, with no
+// exchange between lanes: the recurrence's chain of products stays in one
+// wave's registers.
+//
+// fp32 operands enter as two bf16 terms (hi + lo, each rounded to nearest):
+// 16 bits of the value survive, so a product is within 2^-17 of fp32's; the
+// lo * lo product (2^-18) is dropped.  q, k, v and the output's gradient are
+// bf16 already and need one term.  Accumulators and states are fp32.
+#pragma once
+
+#include "ckda_internal.h"
+
+namespace ckda {
+namespace gdr {
+
+constexpr int C = kChunk;               // 64 tokens
+constexpr int kThreads = 256;
+
+typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+typedef float f4 __attribute__((ext_vector_type(4)));
+typedef short s4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s4 lds_s4;
+typedef __attribute__((address_space(3))) char lds_char;
+
+// ---- per (chunk, head) record in the workspace, all in operand order:
+// fragment f of a lower triangular 64 x 64 matrix, tiles (it, ks) with
+// ks <= it / 2, is 64 lanes x 16 bytes: lane (m, h) holds row 16 it + m and
+// the 8 columns of quarter h of the 32 from 32 ks.
+constexpr int kFrag = 1024;             // bytes of a fragment
+constexpr int kTri = 6 * kFrag;         // a lower triangular matrix, one term
+__host__ __device__ constexpr int frag_at(int it, int ks) {
+  return (it < 2 ? it : 2 * it - 2 + ks) * kFrag;
+}
+// T' hi, T' lo, P hi, six rows of 64 gate factors, P lo (backward only)
+constexpr int kRecTh = 0, kRecTl = kTri, kRecPh = 2 * kTri, kRecGate = 3 * kTri;
+enum { kGam = 0, kLast = 1, kBeta = 2, kLastBeta = 3, kGhi = 4, kGlo = 5 };
+constexpr int kGateBytes = 6 * C * 4;
+constexpr int kRecFwd = kRecGate + kGateBytes;          // 19968
+constexpr int kRecPl = kRecFwd;
+constexpr int kRecBwd = kRecFwd + kTri;                 // 26112
+static_assert(kRecFwd % 256 == 0 && kRecBwd % 256 == 0, "records stay aligned");
+
+// |beta| is raised to this where it is smaller: the backward divides by it,
+// and a token with beta = 0 still has a gradient there.  2^-64 of a value is
+// far below fp32's rounding of what it is added to.
+constexpr float kBetaFloor = 5.42101086e-20f;
+// log-gates below this count as this (e^-10000 is 0 in every product).
+constexpr double kGateFloor = -1e4;
+
+__device__ __forceinline__ f4 mfma(bf8 a, bf8 b, f4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ bf8 join(bf4 a, bf4 b) {
+  return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+__device__ __forceinline__ bf4 round4(f4 x) {
+  return bf4{(__bf16)x[0], (__bf16)x[1], (__bf16)x[2], (__bf16)x[3]};
+}
+__device__ __forceinline__ f4 widen4(bf4 x) {
+  const uint2 u = __builtin_bit_cast(uint2, x);
+  return f4{__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u),
+            __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xFFFF0000u)};
+}
+__device__ __forceinline__ void split4(f4 x, bf4 &hi, bf4 &lo) {
+  hi = round4(x);
+  lo = round4(x - widen4(hi));
+}
+struct Split { bf8 hi, lo; };
+__device__ __forceinline__ Split split8(f4 a, f4 b) {
+  bf4 ah, al, bh, bl;
+  split4(a, ah, al);
+  split4(b, bh, bl);
+  return {join(ah, bh), join(al, bl)};
+}
+__device__ __forceinline__ f4 dot2(bf8 a, const Split &b, f4 c) {     // exact x split
+  return mfma(a, b.lo, mfma(a, b.hi, c));
+}
+__device__ __forceinline__ f4 dot2(const Split &a, bf8 b, f4 c) {
+  return mfma(a.lo, b, mfma(a.hi, b, c));
+}
+__device__ __forceinline__ f4 dot3(const Split &a, const Split &b, f4 c) {
+  return mfma(a.lo, b.hi, mfma(a.hi, b.lo, mfma(a.hi, b.hi, c)));
+}
+
+// ---- LDS operand reads.  Row-major tiles have rows of COLS bf16 and 16 bytes
+// of padding (4 banks a row, so a column of rows spreads over the banks).
+template <int COLS> constexpr int kStride = COLS * 2 + 16;
+
+// Operand whose lanes are rows: lane (m, h) gets row r0 + m, the 8 columns of
+// quarter h of the 32 from c0.
+template <int COLS>
+__device__ __forceinline__ bf8 rows_frag(const char *tile, int r0, int c0, int lane) {
+  const char *p = tile + (r0 + (lane & 15)) * kStride<COLS> + (c0 + 4 * (lane >> 4)) * 2;
+  return join(*reinterpret_cast<const bf4 *>(p), *reinterpret_cast<const bf4 *>(p + 32));
+}
+// ds_read_b64_tr_b16: in each group of 16 lanes, lane s gives the address of 4
+// values and lane i gets value i % 4 of lanes i / 4, 4 + i / 4, 8 + i / 4 and
+// 12 + i / 4.  With lane s at row s / 4, columns 4 (s % 4), lane i gets the 4
+// rows of column i.
+__device__ __forceinline__ bf4 read_tr(const char *p) {
+  const lds_char *q = (const lds_char *)p;
+  return __builtin_bit_cast(bf4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)q));
+}
+// 4 rows (r0 + 4h ..) of column c0 + lane % 16.
+template <int COLS>
+__device__ __forceinline__ bf4 cols_quad(const char *tile, int r0, int c0, int lane) {
+  const int s = lane & 15, h = lane >> 4;
+  return read_tr(tile + (r0 + 4 * h + (s >> 2)) * kStride<COLS> + (c0 + 4 * (s & 3)) * 2);
+}
+// Operand whose lanes are columns and whose contracted index is the row.
+template <int COLS>
+__device__ __forceinline__ bf8 cols_frag(const char *tile, int r0, int c0, int lane) {
+  return join(cols_quad<COLS>(tile, r0, c0, lane), cols_quad<COLS>(tile, r0 + 16, c0, lane));
+}
+__device__ __forceinline__ bf8 tri_frag(const char *mat, int it, int ks, int lane) {
+  return *reinterpret_cast<const bf8 *>(mat + frag_at(it, ks) + lane * 16);
+}
+// The same matrix transposed: lanes are its columns 16 jt + m, contracted over
+// the rows of tiles 2 ks and 2 ks + 1 (tiles above the diagonal are zero).
+__device__ __forceinline__ bf4 tri_quad_t(const char *mat, int it, int jt, int lane) {
+  const int s = lane & 15, h = lane >> 4;
+  return read_tr(mat + frag_at(it, jt >> 1) + ((s & 3) * 16 + 4 * h + (s >> 2)) * 16 +
+                 (jt & 1) * 8);
+}
+__device__ __forceinline__ bf8 tri_frag_t(const char *mat, int jt, int ks, int lane) {
+  // it = 2 ks < jt only where jt = 2 ks + 1: that tile lies above the diagonal
+  // and is stored as zeros.
+  return join(tri_quad_t(mat, 2 * ks, jt, lane), tri_quad_t(mat, 2 * ks + 1, jt, lane));
+}
+// Tile order, used for states and E, F in the workspace: a 16 x 16 result tile
+// as its 64 lanes x 4 values (8 bytes a lane).  Transposed read: lane i gets
+// the 4 columns 4h .. of row i of the tile (a result's lane is its column).
+__device__ __forceinline__ bf4 tile_quad_t(const char *tile, int lane) {
+  const int s = lane & 15, h = lane >> 4;
+  return read_tr(tile + ((s & 3) * 16 + 4 * h + (s >> 2)) * 8);
+}
+
+// ---- staging of a row-major [64][COLS] bf16 tile: global -> registers -> LDS
+template <int COLS> struct Stage {
+  static constexpr int kLanes = COLS / 8, kRows = kThreads / kLanes, kPasses = C / kRows;
+  uint4 r[kPasses];
+  __device__ __forceinline__ void load(const __hip_bfloat16 *p, size_t ld, int valid, int t) {
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const int row = t / kLanes + i * kRows;
+      r[i] = row < valid ? *reinterpret_cast<const uint4 *>(p + row * ld + (t % kLanes) * 8)
+                         : make_uint4(0, 0, 0, 0);
+    }
+  }
+  __device__ __forceinline__ void store(char *tile, int t) const {
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i)
+      *reinterpret_cast<uint4 *>(tile + (t / kLanes + i * kRows) * kStride<COLS> +
+                                 (t % kLanes) * 16) = r[i];
+  }
+};
+// Linear bytes: global -> registers -> LDS.
+template <int BYTES> struct Linear {
+  static constexpr int kPasses = (BYTES + kThreads * 16 - 1) / (kThreads * 16);
+  uint4 r[kPasses];
+  __device__ __forceinline__ void load(const char *p, int t) {
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const int at = (t + i * kThreads) * 16;
+      r[i] = BYTES % (kThreads * 16) == 0 || at < BYTES ? *reinterpret_cast<const uint4 *>(p + at)
+                                                       : make_uint4(0, 0, 0, 0);
+    }
+  }
+  __device__ __forceinline__ void store(char *dst, int t) const {
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const int at = (t + i * kThreads) * 16;
+      if (BYTES % (kThreads * 16) == 0 || at < BYTES) *reinterpret_cast<uint4 *>(dst + at) = r[i];
+    }
+  }
+};
+
+// Orders this wave's LDS writes before its later reads (the hardware runs a
+// wave's LDS operations in order; this keeps the compiler to it).
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// Sequence of a flat chunk index (the last whose first chunk is not behind it).
+__device__ __forceinline__ int find_seq(const SeqTable &tab, int N, int chunk) {
+  int lo = 0, hi = N;                    // chunk_off[lo] <= chunk < chunk_off[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (tab.chunk_off[mid] <= chunk) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+}  // namespace gdr
+}  // namespace ckda

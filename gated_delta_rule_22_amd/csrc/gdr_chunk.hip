@@ -1,0 +1,403 @@
+// Chunkwise gated delta rule for bf16 inputs.
+//
+// With a = exp(g), G_i the running sum of g in a 64-token chunk, r_ij =
+// e^(G_i - G_j), gam_i = e^(G_i) and S the state that enters the chunk:
+//
+//   Ah_ij = r_ij k_i.k_j (i > j)      P_ij = r_ij q_i.k_j (i >= j)
+//   T' = (I + Ah diag(beta))^-1       E = T' (V - gam K S)
+//   U = beta E                        O = gam Q S + P U
+//   S <- gam_n S + K^T (gam_n / gam U)
+//
+// The gate is one number per token and head, so decays scale rows and columns
+// of products of the bf16 inputs themselves: k and q stay exact bf16 operands
+// (per-channel gates would have to be multiplied into them).
+//
+// prepare_kernel makes T', P and the gate factors of every chunk in parallel;
+// chain_kernel runs the chunks of a (sequence, head) in order.
+#include "gdr_chunk.h"
+
+namespace ckda {
+using namespace gdr;
+namespace {
+
+// ------------------------------------------------------------------ prepare
+// One wave per (chunk, value head), four to a workgroup, no barriers.  The
+// 64 x 64 unit lower triangular inverse is taken by forward substitution in
+// fp32, one column a lane: row i of Ah diag(beta) is read from LDS at one
+// address for all lanes (a broadcast) and the column's earlier entries are
+// registers.
+constexpr int kMStride = C + 4;          // floats; keeps rows 16-byte aligned
+
+template <int DK, bool BWD>
+__global__ __launch_bounds__(kThreads) void prepare_kernel(
+    const __hip_bfloat16 *__restrict__ q, const __hip_bfloat16 *__restrict__ k,
+    const float *__restrict__ g, const float *__restrict__ beta, SeqTable tab, int N, int Hk,
+    int Hv, char *__restrict__ rec_base) {
+  constexpr int KS = DK / 32;
+  constexpr int kRec = BWD ? kRecBwd : kRecFwd;
+  __shared__ float s_M[4][C * kMStride];
+  __shared__ float s_g[4][3][C];         // G hi, G lo (log2 units), beta
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int m = lane & 15, h = lane >> 4;
+  const int per = (Hv + 3) / 4;
+  const int chunk = blockIdx.x / per, hv = (blockIdx.x % per) * 4 + wave;
+  if (hv >= Hv || chunk >= tab.chunk_off[N]) return;   // waves share nothing
+  const int seq = find_seq(tab, N, chunk);
+  const int at = (chunk - tab.chunk_off[seq]) * C;
+  const int valid = min(C, tab.seq_len[seq] - at);
+  const size_t row0 = (size_t)tab.seq_start[seq] + at;
+  const int hk = hv / (Hv / Hk);
+  char *rec = rec_base + ((size_t)chunk * Hv + hv) * kRec;
+  float *M = s_M[wave], *s_hi = s_g[wave][0], *s_lo = s_g[wave][1], *s_b = s_g[wave][2];
+
+  // Gate factors.  The running sum is fp64: a forgetful token early in the
+  // chunk must not cost the later tokens' differences their low bits.
+  double G = 0.;
+  float b = 0.f;
+  if (lane < valid) {
+    const float x = g[(row0 + lane) * Hv + hv];
+    G = x < (float)kGateFloor ? kGateFloor : (double)x;
+    b = beta[(row0 + lane) * Hv + hv];
+  }
+  if (fabsf(b) < kBetaFloor) b = copysignf(kBetaFloor, b);
+  G *= 1.4426950408889634074;            // log2 units
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const double y = __shfl_up(G, o);
+    if (lane >= o) G += y;
+  }
+  const double Gn = __shfl(G, 63);
+  auto pow2 = [](double x) {             // 2^x; whole and fractional part apart
+    const double w = rint(x);
+    return ldexpf(exp2f((float)(x - w)), (int)fmin(fmax(w, -3e4), 3e4));
+  };
+  const float gam = pow2(G), last = pow2(Gn - G);
+  const float ghi = (float)G, glo = (float)(G - (double)ghi);
+  s_hi[lane] = ghi;
+  s_lo[lane] = glo;
+  s_b[lane] = b;
+  float *gate = reinterpret_cast<float *>(rec + kRecGate);
+  gate[kGam * C + lane] = gam;
+  gate[kLast * C + lane] = last;
+  gate[kBeta * C + lane] = b;
+  gate[kLastBeta * C + lane] = last * b;
+  gate[kGhi * C + lane] = ghi;
+  gate[kGlo * C + lane] = glo;
+
+  bf8 kf[4][KS];
+#pragma unroll
+  for (int it = 0; it < 4; ++it)
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      const int r = 16 * it + m;
+      const uint4 z = make_uint4(0, 0, 0, 0);
+      kf[it][ks] = __builtin_bit_cast(
+          bf8, r < valid ? *reinterpret_cast<const uint4 *>(k + ((row0 + r) * Hk + hk) * DK +
+                                                            32 * ks + 8 * h)
+                         : z);
+    }
+  wave_sync();
+
+  // Ah diag(beta) to LDS: tile (it, jt), lane = column j, rows i = 4h ..
+#pragma unroll
+  for (int it = 0; it < 4; ++it) {
+    const f4 hi_i = *reinterpret_cast<const f4 *>(s_hi + 16 * it + 4 * h);
+    const f4 lo_i = *reinterpret_cast<const f4 *>(s_lo + 16 * it + 4 * h);
+#pragma unroll
+    for (int jt = 0; jt <= it; ++jt) {
+      f4 a = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) a = mfma(kf[it][ks], kf[jt][ks], a);
+      const int j = 16 * jt + m;
+      const float hj = s_hi[j], lj = s_lo[j], bj = s_b[j];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int i = 16 * it + 4 * h + r;
+        const float e = (hi_i[r] - hj) + (lo_i[r] - lj);
+        M[i * kMStride + j] = i > j ? a[r] * exp2f(e) * bj : 0.f;
+      }
+    }
+  }
+
+  // P in operand order: tiles transposed, lane = row i, 4 columns j at a time.
+#pragma unroll
+  for (int it = 0; it < 4; ++it) {
+    bf8 qf[KS];
+    const int i = 16 * it + m;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      const uint4 z = make_uint4(0, 0, 0, 0);
+      qf[ks] = __builtin_bit_cast(
+          bf8, i < valid ? *reinterpret_cast<const uint4 *>(q + ((row0 + i) * Hk + hk) * DK +
+                                                            32 * ks + 8 * h)
+                         : z);
+    }
+    const float hi_i = s_hi[i], lo_i = s_lo[i];
+#pragma unroll
+    for (int kp = 0; kp <= it / 2; ++kp) {
+      auto tile = [&](int jt) {
+        f4 p = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) p = mfma(kf[jt][ks], qf[ks], p);
+        const f4 hj = *reinterpret_cast<const f4 *>(s_hi + 16 * jt + 4 * h);
+        const f4 lj = *reinterpret_cast<const f4 *>(s_lo + 16 * jt + 4 * h);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float x = (hi_i - hj[r]) + (lo_i - lj[r]);
+          p[r] = i >= 16 * jt + 4 * h + r ? p[r] * exp2f(x) : 0.f;
+        }
+        return p;
+      };
+      const f4 p0 = tile(2 * kp);
+      f4 p1 = 0.f;
+      if (2 * kp + 1 <= it) p1 = tile(2 * kp + 1);
+      const Split s = split8(p0, p1);
+      *reinterpret_cast<bf8 *>(rec + kRecPh + frag_at(it, kp) + lane * 16) = s.hi;
+      if (BWD) *reinterpret_cast<bf8 *>(rec + kRecPl + frag_at(it, kp) + lane * 16) = s.lo;
+    }
+  }
+  wave_sync();
+
+  // Column `lane` of the inverse.
+  float x[C];
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    f4 s = 0.f;
+#pragma unroll
+    for (int j = 0; j < i; j += 4) {
+      const f4 a = *reinterpret_cast<const f4 *>(M + i * kMStride + j);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (j + e < i) s[e] += a[e] * x[j + e];
+    }
+    x[i] = (i == lane ? 1.f : 0.f) - ((s[0] + s[1]) + (s[2] + s[3]));
+  }
+  wave_sync();
+#pragma unroll
+  for (int i = 0; i < C; ++i) M[i * kMStride + lane] = x[i];
+  wave_sync();
+#pragma unroll
+  for (int it = 0; it < 4; ++it)
+#pragma unroll
+    for (int ks = 0; ks <= it / 2; ++ks) {
+      const float *p = M + (16 * it + m) * kMStride + 32 * ks + 4 * h;
+      const Split s = split8(*reinterpret_cast<const f4 *>(p),
+                             *reinterpret_cast<const f4 *>(p + 16));
+      *reinterpret_cast<bf8 *>(rec + kRecTh + frag_at(it, ks) + lane * 16) = s.hi;
+      *reinterpret_cast<bf8 *>(rec + kRecTl + frag_at(it, ks) + lane * 16) = s.lo;
+    }
+}
+
+// Workgroups of one (sequence, head) -- its column blocks -- share an XCD's
+// L2: consecutive workgroups go round the 8 XCDs.
+__device__ __forceinline__ bool chain_block(int nblk, int pairs, int &pair, int &blk) {
+  const int b = blockIdx.x;
+  blk = (b / 8) % nblk;
+  pair = (b / 8 / nblk) * 8 + b % 8;
+  return pair < pairs;
+}
+
+// -------------------------------------------------------------------- chain
+// A workgroup of 4 waves runs 64 of the state's DV columns of one (sequence,
+// head) over its chunks; a wave owns 16 columns for the whole sequence, so the
+// chain S -> K S -> E -> S of a column never leaves its wave: S is 4 DK / 16
+// accumulator registers, and each product's result tiles are the next one's
+// operand.  Waves only share the staged operands: one barrier a chunk, with
+// the next chunk's loads in flight meanwhile.
+// STORE: for the backward, keeps the state before each chunk and E (two bf16
+// terms each) and makes no output.
+template <int DK, int DV, bool STORE>
+__global__ __launch_bounds__(kThreads, 1) void chain_kernel(
+    const __hip_bfloat16 *__restrict__ q, const __hip_bfloat16 *__restrict__ k,
+    const __hip_bfloat16 *__restrict__ v, const float *__restrict__ S0, SeqTable tab, int N,
+    int Hk, int Hv, const char *__restrict__ rec_base, __hip_bfloat16 *__restrict__ o,
+    float *__restrict__ S_T, char *__restrict__ S_keep, char *__restrict__ E_keep) {
+  constexpr int KS = DK / 32, MT = DK / 16, BV = 64;
+  constexpr int kRec = STORE ? kRecBwd : kRecFwd;
+  constexpr int kK = 0, kQ = kK + C * kStride<DK>, kV = kQ + (STORE ? 0 : C * kStride<DK>);
+  constexpr int kR = kV + C * kStride<BV>, kBuf = kR + kRecFwd;
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  int pair, blk;
+  if (!chain_block(DV / BV, N * Hv, pair, blk)) return;
+  const int seq = tab.order[pair / Hv], hv = pair % Hv, hk = hv / (Hv / Hk);
+  const int t = threadIdx.x, wave = t >> 6, lane = t & 63, m = lane & 15, h = lane >> 4;
+  const int len = tab.seq_len[seq], chunks = (len + C - 1) / C;
+  const size_t row0 = tab.seq_start[seq];
+  const size_t c0 = tab.chunk_off[seq];
+  const int col = blk * BV + 16 * wave;  // of the head's DV
+
+  f4 S[MT];
+  const size_t sbase = ((size_t)seq * Hv + hv) * DK * DV + col + m;
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      S[i][r] = S0 ? S0[sbase + (size_t)(16 * i + 4 * h + r) * DV] : 0.f;
+
+  Stage<DK> gk, gq;
+  Stage<BV> gv;
+  Linear<kRecFwd> gr;
+  auto fetch = [&](int c) {
+    const int valid = min(C, len - c * C);
+    const size_t row = row0 + (size_t)c * C;
+    gk.load(k + (row * Hk + hk) * DK, (size_t)Hk * DK, valid, t);
+    if (!STORE) gq.load(q + (row * Hk + hk) * DK, (size_t)Hk * DK, valid, t);
+    gv.load(v + (row * Hv + hv) * DV + blk * BV, (size_t)Hv * DV, valid, t);
+    gr.load(rec_base + ((c0 + c) * Hv + hv) * kRec, t);
+  };
+  auto put = [&](char *buf) {
+    gk.store(buf + kK, t);
+    if (!STORE) gq.store(buf + kQ, t);
+    gv.store(buf + kV, t);
+    gr.store(buf + kR, t);
+  };
+  if (chunks > 0) {
+    fetch(0);
+    put(lds);
+  }
+  __syncthreads();
+  for (int c = 0; c < chunks; ++c) {
+    const char *buf = lds + (c & 1) * kBuf;
+    const char *K = buf + kK, *Q = buf + kQ, *V = buf + kV, *R = buf + kR;
+    const float *gate = reinterpret_cast<const float *>(R + kRecGate);
+    if (c + 1 < chunks) fetch(c + 1);
+
+    Split sf[KS];
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) sf[ks] = split8(S[2 * ks], S[2 * ks + 1]);
+    if (STORE) {
+      char *p = S_keep + (((c0 + c) * Hv + hv) * (2 * MT * (DV / 16)) + col / 16) * 512 + lane * 8;
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const bf8 hi = sf[i / 2].hi, lo = sf[i / 2].lo;
+        const bf4 x = i % 2 ? __builtin_shufflevector(hi, hi, 4, 5, 6, 7)
+                            : __builtin_shufflevector(hi, hi, 0, 1, 2, 3);
+        const bf4 y = i % 2 ? __builtin_shufflevector(lo, lo, 4, 5, 6, 7)
+                            : __builtin_shufflevector(lo, lo, 0, 1, 2, 3);
+        *reinterpret_cast<bf4 *>(p + i * (DV / 16) * 512) = x;
+        *reinterpret_cast<bf4 *>(p + (MT + i) * (DV / 16) * 512) = y;
+      }
+    }
+
+    // X = V - gam K S, as the operand of T' X
+    f4 X[4];
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      f4 y = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+        y = dot2(rows_frag<DK>(K, 16 * it, 32 * ks, lane), sf[ks], y);
+      const f4 gam = *reinterpret_cast<const f4 *>(gate + kGam * C + 16 * it + 4 * h);
+      X[it] = widen4(cols_quad<BV>(V, 16 * it, 16 * wave, lane)) - gam * y;
+    }
+    const Split x0 = split8(X[0], X[1]), x1 = split8(X[2], X[3]);
+    f4 E[4];
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      E[it] = 0.f;
+#pragma unroll
+      for (int ks = 0; ks <= it / 2; ++ks) {
+        const Split T = {tri_frag(R + kRecTh, it, ks, lane), tri_frag(R + kRecTl, it, ks, lane)};
+        E[it] = dot3(T, ks ? x1 : x0, E[it]);
+      }
+    }
+    if (STORE) {
+      char *p = E_keep + (((c0 + c) * Hv + hv) * (8 * (DV / 16)) + col / 16) * 512 + lane * 8;
+#pragma unroll
+      for (int it = 0; it < 4; ++it) {
+        bf4 x, y;
+        split4(E[it], x, y);
+        *reinterpret_cast<bf4 *>(p + it * (DV / 16) * 512) = x;
+        *reinterpret_cast<bf4 *>(p + (4 + it) * (DV / 16) * 512) = y;
+      }
+    }
+    f4 W[4];                             // gam_n / gam U
+#pragma unroll
+    for (int it = 0; it < 4; ++it)
+      W[it] = E[it] * *reinterpret_cast<const f4 *>(gate + kLastBeta * C + 16 * it + 4 * h);
+    const Split w0 = split8(W[0], W[1]), w1 = split8(W[2], W[3]);
+    const float gn = gate[kGam * C + C - 1];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      S[i] *= gn;
+      S[i] = dot2(cols_frag<DK>(K, 0, 16 * i, lane), w0, S[i]);
+      S[i] = dot2(cols_frag<DK>(K, 32, 16 * i, lane), w1, S[i]);
+    }
+
+    if (!STORE) {
+      // O, transposed: lane = token, 4 columns a lane.  One term of S, P and U
+      // is enough here: each is within 2^-9 of its value, and so is the bf16
+      // output itself.
+      f4 U[4];
+#pragma unroll
+      for (int it = 0; it < 4; ++it)
+        U[it] = E[it] * *reinterpret_cast<const f4 *>(gate + kBeta * C + 16 * it + 4 * h);
+      const bf8 u0 = join(round4(U[0]), round4(U[1])), u1 = join(round4(U[2]), round4(U[3]));
+#pragma unroll
+      for (int it = 0; it < 4; ++it) {
+        f4 a = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+          a = mfma(sf[ks].hi, rows_frag<DK>(Q, 16 * it, 32 * ks, lane), a);
+        a *= gate[kGam * C + 16 * it + m];
+#pragma unroll
+        for (int ks = 0; ks <= it / 2; ++ks)
+          a = mfma(ks ? u1 : u0, tri_frag(R + kRecPh, it, ks, lane), a);
+        const int tok = c * C + 16 * it + m;
+        if (tok < len)
+          *reinterpret_cast<bf4 *>(o + ((row0 + tok) * Hv + hv) * DV + col + 4 * h) = round4(a);
+      }
+    }
+    if (c + 1 < chunks) put(lds + ((c + 1) & 1) * kBuf);
+    __syncthreads();
+  }
+  if (S_T)
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        S_T[sbase + (size_t)(16 * i + 4 * h + r) * DV] = S[i][r];
+}
+
+template <int DK, int DV, bool STORE> constexpr int chain_lds() {
+  return 2 * (C * kStride<DK> * (STORE ? 1 : 2) + C * kStride<64> + kRecFwd);
+}
+
+unsigned chain_grid(int pairs, int nblk) { return (unsigned)((pairs + 7) / 8 * 8) * nblk; }
+
+template <typename F> hipError_t allow_lds(F *f, int bytes) {
+  return hipFuncSetAttribute(reinterpret_cast<const void *>(f),
+                             hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+template <int DK, int DV> hipError_t forward_typed(const GdrArgs &a, char *rec, hipStream_t st) {
+  const auto *q = static_cast<const __hip_bfloat16 *>(a.q);
+  const auto *k = static_cast<const __hip_bfloat16 *>(a.k);
+  const auto *v = static_cast<const __hip_bfloat16 *>(a.v);
+  if (a.n_chunks_ub > 0) {
+    hipLaunchKernelGGL((prepare_kernel<DK, false>),
+                       dim3((unsigned)(a.n_chunks_ub * ((a.Hv + 3) / 4))), dim3(kThreads), 0, st,
+                       q, k, a.g, a.beta, a.tab, a.N, a.Hk, a.Hv, rec);
+    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  }
+  constexpr int lds = chain_lds<DK, DV, false>();
+  if (hipError_t e = allow_lds(chain_kernel<DK, DV, false>, lds); e != hipSuccess) return e;
+  hipLaunchKernelGGL((chain_kernel<DK, DV, false>), dim3(chain_grid(a.N * a.Hv, DV / 64)),
+                     dim3(kThreads), lds, st, q, k, v, a.S0, a.tab, a.N, a.Hk, a.Hv, rec,
+                     static_cast<__hip_bfloat16 *>(a.o), a.S_T, (char *)nullptr,
+                     (char *)nullptr);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t gdr_forward_rec_bytes() { return kRecFwd; }
+
+hipError_t launch_gdr_forward(const GdrArgs &a, void *rec, hipStream_t stream) {
+  char *r = static_cast<char *>(rec);
+  if (a.dk == 64)
+    return a.dv == 64 ? forward_typed<64, 64>(a, r, stream) : forward_typed<64, 128>(a, r, stream);
+  return a.dv == 64 ? forward_typed<128, 64>(a, r, stream) : forward_typed<128, 128>(a, r, stream);
+}
+
+}  // namespace ckda

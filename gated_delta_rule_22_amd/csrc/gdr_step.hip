@@ -1,0 +1,339 @@
+// Gated delta rule, token by token, in fp32: the single-token step over a
+// pool of states, and the forward of a whole sequence.
+//
+//   S <- a S + k e^T,  e = beta (v - a S^T k),  o = S^T q,   a = exp(g)
+//
+// (the recurrence of ckda_decode_step with one positive gate per head instead
+// of one signed gate per key channel.)  Head h reads query/key head
+// h / (Hv / Hk).
+#include "ckda_internal.h"
+
+namespace ckda {
+namespace {
+
+constexpr int kThreads = 256;
+typedef float nf4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ void put(float *p, float x) { *p = x; }
+__device__ __forceinline__ void put(__hip_bfloat16 *p, float x) { *p = __float2bfloat16(x); }
+
+// One workgroup per (row, head): the state is read once and written once
+// (8 dk dv bytes a head), which is the bound; a thread keeps a strip of 4
+// columns by kRows rows in registers, so all loads are in flight before the
+// first reduction.  slots[n] names the row's state.  A slot outside the pool
+// marks a padded row, and so does one that an earlier row has named: the
+// pool's states are written by one row each, whatever the slots hold.
+template <typename TIn, int DK, int DV>
+__global__ __launch_bounds__(kThreads) void gdr_step_kernel(
+    const TIn *__restrict__ q, const TIn *__restrict__ k, const TIn *__restrict__ v,
+    const float *__restrict__ g, const float *__restrict__ beta, float *__restrict__ S,
+    const int32_t *__restrict__ slots, int pool, TIn *__restrict__ o, int Hk, int Hv) {
+  constexpr int kColThreads = DV / 4;
+  constexpr int kRowGroups = kThreads / kColThreads;
+  constexpr int kRows = DK / kRowGroups;
+  static_assert(kRows * kRowGroups == DK, "dk must split evenly over row groups");
+  __shared__ float s_k[DK], s_q[DK];
+  __shared__ float s_kq[kThreads / 64];
+  __shared__ float4 s_u[kRowGroups][kColThreads], s_w[kRowGroups][kColThreads];
+
+  const int n = blockIdx.x / Hv, h = blockIdx.x - n * Hv;
+  const int t = threadIdx.x, cg = t % kColThreads, rg = t / kColThreads;
+  TIn *oh = o + (size_t)blockIdx.x * DV;
+  int slot = n;
+  if (slots) {
+    slot = slots[n];
+    bool named = slot < 0 || slot >= pool;
+    for (int i = t; i < n; i += kThreads) named |= slots[i] == slot;
+    if (__syncthreads_or(named)) {
+      if (t < DV) put(oh + t, 0.f);
+      return;
+    }
+  }
+  float *Sh = S + ((size_t)slot * Hv + h) * DK * DV;
+  nf4 st[kRows];
+#pragma unroll
+  for (int r = 0; r < kRows; ++r)
+    st[r] = __builtin_nontemporal_load(
+        reinterpret_cast<const nf4 *>(Sh + (size_t)(rg * kRows + r) * DV + cg * 4));
+
+  const size_t qk = ((size_t)n * Hk + h / (Hv / Hk)) * DK;
+  float kq = 0.f;
+  if (t < DK) {
+    const float kk = to_f32(k[qk + t]), qq = to_f32(q[qk + t]);
+    s_k[t] = kk;
+    s_q[t] = qq;
+    kq = kk * qq;
+  }
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) kq += __shfl_xor(kq, off);
+  if ((t & 63) == 0) s_kq[t >> 6] = kq;
+  const float a = expf(g[blockIdx.x]), b = beta[blockIdx.x];
+  const float4 vv = load4_f32(v + (size_t)blockIdx.x * DV + cg * 4);
+  __syncthreads();
+
+  nf4 pu = 0.f, pw = 0.f;
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    const float kk = s_k[rg * kRows + r], qq = s_q[rg * kRows + r];
+    st[r] *= a;
+    pu += kk * st[r];
+    pw += qq * st[r];
+  }
+  s_u[rg][cg] = make_float4(pu.x, pu.y, pu.z, pu.w);
+  s_w[rg][cg] = make_float4(pw.x, pw.y, pw.z, pw.w);
+  __syncthreads();
+  nf4 u = 0.f, w = 0.f;
+#pragma unroll
+  for (int i = 0; i < kRowGroups; ++i) {
+    const float4 x = s_u[i][cg], y = s_w[i][cg];
+    u += nf4{x.x, x.y, x.z, x.w};
+    w += nf4{y.x, y.y, y.z, y.w};
+  }
+  float kqs = 0.f;
+#pragma unroll
+  for (int i = 0; i < (DK + 63) / 64; ++i) kqs += s_kq[i];
+  const nf4 e = b * (nf4{vv.x, vv.y, vv.z, vv.w} - u);
+  if (rg == 0) {
+    w += kqs * e;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) put(oh + cg * 4 + i, w[i]);
+  }
+#pragma unroll
+  for (int r = 0; r < kRows; ++r)
+    *reinterpret_cast<nf4 *>(Sh + (size_t)(rg * kRows + r) * DV + cg * 4) =
+        st[r] + s_k[rg * kRows + r] * e;
+}
+
+// A sequence token by token.  A wave owns 16 columns of one head's state for
+// the whole sequence: lane (r, c) keeps column c of the rows
+// {16 i + 4 r + j}, DK / 4 of them, in registers, so a token costs 3 DK / 4
+// products and two sums over 4 lanes, and nothing but the staged tokens goes
+// through LDS.  The chain of one token (sum of S^T k, the write, the next
+// token's sum) is the bound, not bandwidth: fp32 inputs take this path, where
+// a product in fp32 terms on the matrix cores would cost six bf16 products.
+constexpr int kStage = 16;               // tokens staged into LDS at a time
+
+template <typename TIn, int DK, int DV>
+__global__ __launch_bounds__(kThreads) void gdr_token_kernel(
+    const TIn *__restrict__ q, const TIn *__restrict__ k, const TIn *__restrict__ v,
+    const float *__restrict__ g, const float *__restrict__ beta, const float *__restrict__ S0,
+    SeqTable tab, int Hk, int Hv, TIn *__restrict__ o, float *__restrict__ S_T) {
+  constexpr int kCols = 64;              // columns of a workgroup: 4 waves of 16
+  constexpr int kBlocks = DV / kCols;
+  constexpr int kRows = DK / 4;
+  __shared__ float s_k[kStage][DK], s_q[kStage][DK], s_v[kStage][kCols];
+  __shared__ float s_a[kStage], s_b[kStage];
+  const int blk = blockIdx.x % kBlocks, nh = blockIdx.x / kBlocks;
+  const int n = tab.order[nh / Hv], h = nh % Hv, hk = h / (Hv / Hk);
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  const int rr = lane >> 4, c = lane & 15;
+  const int col = wave * 16 + c;
+  const size_t first = tab.seq_start[n];
+  const int len = tab.seq_len[n];
+  const size_t sbase = ((size_t)n * Hv + h) * DK * DV + (size_t)blk * kCols + col;
+
+  float S[kRows];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int row = 16 * (i >> 2) + 4 * rr + (i & 3);
+    S[i] = S0 ? S0[sbase + (size_t)row * DV] : 0.f;
+  }
+  for (int t0 = 0; t0 < len; t0 += kStage) {
+    const int m = min(kStage, len - t0);
+    __syncthreads();
+    for (int i = t; i < m * DK; i += kThreads) {
+      const size_t at = ((first + t0 + i / DK) * Hk + hk) * DK + i % DK;
+      s_k[i / DK][i % DK] = to_f32(k[at]);
+      s_q[i / DK][i % DK] = to_f32(q[at]);
+    }
+    for (int i = t; i < m * kCols; i += kThreads)
+      s_v[i / kCols][i % kCols] =
+          to_f32(v[((first + t0 + i / kCols) * Hv + h) * DV + blk * kCols + i % kCols]);
+    if (t < m) {
+      s_a[t] = expf(g[(first + t0 + t) * Hv + h]);
+      s_b[t] = beta[(first + t0 + t) * Hv + h];
+    }
+    __syncthreads();
+    for (int s = 0; s < m; ++s) {
+      const float a = s_a[s];
+      float4 kk[kRows / 4];
+      float u0 = 0.f, u1 = 0.f;
+#pragma unroll
+      for (int i = 0; i < kRows / 4; ++i) {
+        kk[i] = *reinterpret_cast<const float4 *>(&s_k[s][16 * i + 4 * rr]);
+        u0 += kk[i].x * S[4 * i] + kk[i].y * S[4 * i + 1];
+        u1 += kk[i].z * S[4 * i + 2] + kk[i].w * S[4 * i + 3];
+      }
+      float u = u0 + u1;
+      u += __shfl_xor(u, 16);
+      u += __shfl_xor(u, 32);
+      const float e = s_b[s] * (s_v[s][col] - a * u);
+      float w0 = 0.f, w1 = 0.f;
+#pragma unroll
+      for (int i = 0; i < kRows / 4; ++i) {
+        const float4 qq = *reinterpret_cast<const float4 *>(&s_q[s][16 * i + 4 * rr]);
+        S[4 * i] = a * S[4 * i] + kk[i].x * e;
+        S[4 * i + 1] = a * S[4 * i + 1] + kk[i].y * e;
+        S[4 * i + 2] = a * S[4 * i + 2] + kk[i].z * e;
+        S[4 * i + 3] = a * S[4 * i + 3] + kk[i].w * e;
+        w0 += qq.x * S[4 * i] + qq.y * S[4 * i + 1];
+        w1 += qq.z * S[4 * i + 2] + qq.w * S[4 * i + 3];
+      }
+      float w = w0 + w1;
+      w += __shfl_xor(w, 16);
+      w += __shfl_xor(w, 32);
+      if (rr == 0) put(o + ((first + t0 + s) * Hv + h) * DV + blk * kCols + col, w);
+    }
+  }
+  if (S_T)
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+      S_T[sbase + (size_t)(16 * (i >> 2) + 4 * rr + (i & 3)) * DV] = S[i];
+}
+
+// ------------------------------------------------- fp32 inputs' backward
+// The fp64 backward of the per-channel recurrence takes q, k and gates per
+// value head and channel.  These kernels lay them out and sum its gradients
+// back: over a group's heads for q and k, over the channels for the gate
+// (dg = a sum_c dalpha_c, a = exp g).  Gates below e^-87 count as e^-87, the
+// smallest that fp32 holds to full precision.
+__device__ __forceinline__ float linear_gate(float g) { return expf(g < -87.f ? -87.f : g); }
+
+__global__ __launch_bounds__(kThreads) void gdr_expand_kernel(
+    const float *__restrict__ q, const float *__restrict__ k, const float *__restrict__ g,
+    size_t rows, int Hk, int Hv, int dk, float *__restrict__ qx, float *__restrict__ kx,
+    float *__restrict__ gx) {
+  const size_t total = rows * Hv * dk;
+  for (size_t i = (size_t)blockIdx.x * kThreads + threadIdx.x; i < total;
+       i += (size_t)gridDim.x * kThreads) {
+    const size_t rh = i / dk;
+    const int c = (int)(i - rh * dk), h = (int)(rh % Hv);
+    const size_t src = ((rh / Hv) * Hk + h / (Hv / Hk)) * dk + c;
+    qx[i] = q[src];
+    kx[i] = k[src];
+    gx[i] = linear_gate(g[rh]);
+  }
+}
+
+__global__ __launch_bounds__(kThreads) void gdr_collect_kernel(
+    const float *__restrict__ dqx, const float *__restrict__ dkx, const float *__restrict__ dgx,
+    const float *__restrict__ g, int N, size_t rows, int Hk,
+    int Hv, int dk, float *__restrict__ dq, float *__restrict__ dk_out, float *__restrict__ dg,
+    SeqTable tab) {
+  // One wave per (token, query/key head).  Rows outside every sequence are
+  // left alone, as everywhere: a row belongs to the last sequence that starts
+  // at or before it, if that sequence reaches it.
+  const int lane = threadIdx.x & 63, rep = Hv / Hk;
+  const size_t waves = (size_t)gridDim.x * (kThreads / 64);
+  for (size_t w = (size_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6); w < rows * Hk;
+       w += waves) {
+    const size_t row = w / Hk;
+    const int hk = (int)(w % Hk);
+    int lo = 0, hi = N;                  // first sequence that starts behind `row`
+    while (lo < hi) {
+      const int mid = (lo + hi) / 2;
+      if ((size_t)tab.seq_start[mid] <= row) lo = mid + 1;
+      else hi = mid;
+    }
+    if (lo == 0 || row >= (size_t)tab.seq_start[lo - 1] + tab.seq_len[lo - 1]) continue;
+    for (int c = lane; c < dk; c += 64) {
+      float a = 0.f, b = 0.f;
+      for (int r = 0; r < rep; ++r) {
+        const size_t at = (row * Hv + hk * rep + r) * dk + c;
+        a += dqx[at];
+        b += dkx[at];
+      }
+      dq[w * dk + c] = a;
+      dk_out[w * dk + c] = b;
+    }
+    for (int r = 0; r < rep; ++r) {
+      const size_t rh = row * Hv + hk * rep + r;
+      const float al = linear_gate(g[rh]);
+      double s = 0.;
+      for (int c = lane; c < dk; c += 64) s += (double)dgx[rh * dk + c] * al;
+      for (int off = 32; off > 0; off >>= 1) s += __shfl_xor(s, off);
+      if (lane == 0) dg[rh] = (float)s;
+    }
+  }
+}
+
+template <typename TIn>
+hipError_t step_typed(const void *q, const void *k, const void *v, const float *g,
+                      const float *beta, float *S, const int32_t *slots, int pool, void *o, int N,
+                      int Hk, int Hv, int dk, int dv, hipStream_t stream) {
+  const dim3 grid((unsigned)(N * Hv)), block(kThreads);
+#define GDR_CASE(DK_, DV_)                                                                   \
+  if (dk == DK_ && dv == DV_) {                                                              \
+    hipLaunchKernelGGL((gdr_step_kernel<TIn, DK_, DV_>), grid, block, 0, stream,             \
+                       static_cast<const TIn *>(q), static_cast<const TIn *>(k),             \
+                       static_cast<const TIn *>(v), g, beta, S, slots, pool,                 \
+                       static_cast<TIn *>(o), Hk, Hv);                                       \
+    return hipGetLastError();                                                                \
+  }
+  GDR_CASE(64, 64)
+  GDR_CASE(64, 128)
+  GDR_CASE(128, 64)
+  GDR_CASE(128, 128)
+#undef GDR_CASE
+  return hipErrorInvalidValue;
+}
+
+template <typename TIn>
+hipError_t token_typed(const GdrArgs &a, hipStream_t stream) {
+  const dim3 grid((unsigned)((size_t)a.N * a.Hv * (a.dv / 64))), block(kThreads);
+#define GDR_CASE(DK_, DV_)                                                                   \
+  if (a.dk == DK_ && a.dv == DV_) {                                                          \
+    hipLaunchKernelGGL((gdr_token_kernel<TIn, DK_, DV_>), grid, block, 0, stream,            \
+                       static_cast<const TIn *>(a.q), static_cast<const TIn *>(a.k),         \
+                       static_cast<const TIn *>(a.v), a.g, a.beta, a.S0, a.tab, a.Hk, a.Hv,  \
+                       static_cast<TIn *>(a.o), a.S_T);                                      \
+    return hipGetLastError();                                                                \
+  }
+  GDR_CASE(64, 64)
+  GDR_CASE(64, 128)
+  GDR_CASE(128, 64)
+  GDR_CASE(128, 128)
+#undef GDR_CASE
+  return hipErrorInvalidValue;
+}
+
+unsigned blocks_for(size_t items) {
+  const size_t b = (items + kThreads - 1) / kThreads;
+  return (unsigned)(b < 1 ? 1 : (b < 8192 ? b : 8192));
+}
+
+}  // namespace
+
+hipError_t launch_gdr_step(const void *q, const void *k, const void *v, const float *g,
+                           const float *beta, float *S, const int32_t *slots, int pool, void *o,
+                           int N, int Hk, int Hv, int dk, int dv, int in_dtype,
+                           hipStream_t stream) {
+  return in_dtype == CKDA_BF16
+             ? step_typed<__hip_bfloat16>(q, k, v, g, beta, S, slots, pool, o, N, Hk, Hv, dk, dv,
+                                          stream)
+             : step_typed<float>(q, k, v, g, beta, S, slots, pool, o, N, Hk, Hv, dk, dv, stream);
+}
+
+hipError_t launch_gdr_token(const GdrArgs &a, int in_dtype, hipStream_t stream) {
+  return in_dtype == CKDA_BF16 ? token_typed<__hip_bfloat16>(a, stream)
+                               : token_typed<float>(a, stream);
+}
+
+hipError_t launch_gdr_expand(const float *q, const float *k, const float *g, size_t rows, int Hk,
+                             int Hv, int dk, float *qx, float *kx, float *gx,
+                             hipStream_t stream) {
+  hipLaunchKernelGGL(gdr_expand_kernel, dim3(blocks_for(rows * Hv * dk)), dim3(kThreads), 0,
+                     stream, q, k, g, rows, Hk, Hv, dk, qx, kx, gx);
+  return hipGetLastError();
+}
+
+hipError_t launch_gdr_collect(const float *dqx, const float *dkx, const float *dgx,
+                              const float *g, SeqTable tab, int N, size_t rows, int Hk, int Hv,
+                              int dk, float *dq, float *dk_out, float *dg, hipStream_t stream) {
+  hipLaunchKernelGGL(gdr_collect_kernel, dim3(blocks_for(rows * Hk * 64)), dim3(kThreads), 0,
+                     stream, dqx, dkx, dgx, g, N, rows, Hk, Hv, dk, dq,
+                     dk_out, dg, tab);
+  return hipGetLastError();
+}
+
+}  // namespace ckda

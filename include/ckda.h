@@ -337,6 +337,148 @@ int ckda_decode_step(const void *q, const void *k, const void *v, const float *g
                      const float *beta, float *S, float *o, int N, int H, int dk,
                      int dv, int in_dtype, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Gated delta rule: the same recurrence with ONE positive gate per head and
+ * token in place of a signed gate per key channel, given as its logarithm:
+ *
+ *   S_t = a_t (I - beta_t k_t k_t^T) S_{t-1} + beta_t k_t v_t^T
+ *   o_t = S_t^T q_t,                                      a_t = exp(g_t)
+ *
+ * Query and key heads may be shared: value head h reads query/key head
+ * h / (Hv / Hk).  Layouts, ownership, streams and errors are those of the
+ * calls above.  q, k, v, o and their gradients have in_dtype (CKDA_BF16 or
+ * CKDA_F32); g, beta, states and their gradients are fp32.  No scale is
+ * applied: q arrives pre-scaled (qk_norm_rotary does that).
+ *
+ * Gates: any g, nominally <= 0.  Log-gates below -1e4 (so also -infinity, a
+ * full reset of the state) count as -1e4; backward with fp32 inputs: below
+ * -87 as -87.  A NaN in any input reaches only the outputs of the heads that
+ * read it, in its own sequence.
+ */
+
+/* Workspace of gdr_forward in bytes (0 if the sizes are invalid): the sequence
+ * table, and for bf16 inputs about 20 KB per (64-token chunk, value head). */
+size_t gdr_forward_workspace_bytes(int B, int T, int Hk, int Hv, int dk, int dv, int N,
+                                   int in_dtype);
+
+/*
+ * Forward over a batch of sequences.
+ *
+ *  q, k        [B, T, Hk, dk]  in_dtype
+ *  v           [B, T, Hv, dv]  in_dtype
+ *  g, beta     [B, T, Hv]      fp32   log-gate; write strength (nominally [0, 2])
+ *  S0          [N, Hv, dk, dv] fp32   initial states, or NULL for zero states
+ *  cu_seqlens  NULL (N = B, sequence n is row n) or int32 [N+1] offsets into
+ *              the T axis (B = 1), made monotone on the device as above; empty
+ *              sequences are allowed, rows outside every sequence are not
+ *              written
+ *  Hk, Hv      Hv a multiple of Hk; dk, dv each 64 or 128; B*T*Hv < 2^31,
+ *              N*Hv < 2^28
+ *  o           [B, T, Hv, dv]  in_dtype
+ *  S_T         [N, Hv, dk, dv] fp32 or NULL; may be S0 itself
+ *  workspace   gdr_forward_workspace_bytes(...) bytes, 16-byte aligned
+ *
+ * Numerics: bf16 inputs run chunkwise on bf16 matrix cores with fp32
+ * accumulation; fp32 operands (state, inverse, update) enter as two bf16
+ * terms (16 bits), but for the output's own two products, whose operands are
+ * rounded once to bf16 like the output itself.  fp32 inputs run token by token
+ * in fp32.
+ */
+int gdr_forward(const void *q, const void *k, const void *v, const float *g, const float *beta,
+                const float *S0, const int32_t *cu_seqlens, int B, int T, int Hk, int Hv, int dk,
+                int dv, int N, int in_dtype, void *o, float *S_T, void *workspace,
+                size_t workspace_bytes, void *stream);
+
+/*
+ * One token for N rows, on states that live in a pool.
+ *
+ *  q, k        [N, Hk, dk]     in_dtype
+ *  v           [N, Hv, dv]     in_dtype
+ *  g, beta     [N, Hv]         fp32
+ *  S           [pool, Hv, dk, dv] fp32, the rows' states updated in place
+ *  slots       int32 [N]: the state of each row; or NULL: row n has state n
+ *              and pool must be N.  A slot outside [0, pool) marks a padded
+ *              row; a slot that an earlier row has named already does too.
+ *              Padded rows get o = 0 and touch no state.
+ *  o           [N, Hv, dv]     in_dtype, must not overlap S or an input
+ *
+ * Numerics: fp32 throughout, o rounded once.
+ */
+int gdr_decode_step(const void *q, const void *k, const void *v, const float *g,
+                    const float *beta, float *S, const int32_t *slots, int pool, void *o, int N,
+                    int Hk, int Hv, int dk, int dv, int in_dtype, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Norm of every query and key head and rotation by position, in one pass:
+ * what prepares q and k for the recurrences above.
+ */
+enum {
+    CKDA_NORM_NONE = 0,
+    CKDA_NORM_L2 = 1,        /* x (sum_c x_c^2 + eps)^(-1/2) */
+    CKDA_NORM_RMS = 2        /* x (sum_c x_c^2 / d + eps)^(-1/2) */
+};
+enum {
+    CKDA_ROTARY_HALF = 0,        /* channel i pairs with i + rd/2 */
+    CKDA_ROTARY_INTERLEAVED = 1  /* channel 2i pairs with 2i + 1 */
+};
+
+/*
+ * For each row x of d channels (one token's head):
+ *
+ *   n = norm(x), times the weight of q or k if there is one
+ *   (y0, y1) = rotary_scale (n0 cos - n1 sin, n1 cos + n0 sin)
+ *
+ * over the pairs of the first rd channels, with the angle positions[token] *
+ * freqs[pair]; y = n behind them.  Rows of q are then multiplied by q_scale.
+ *
+ *  q, k        tokens rows of Hq and Hk heads of d channels, ldq and ldk
+ *              elements apart (>= Hq d, Hk d): slices of a packed projection
+ *              are read where they are.  Hq or Hk may be 0.
+ *  positions   int32 [tokens], freqs  fp64 [rd/2] in radians per position;
+ *              both may be NULL if rd is 0.  The angle is reduced in fp64, so
+ *              far positions lose nothing.
+ *  q_weight, k_weight  fp32 [d] or NULL
+ *  d           even, 2 .. 256; rd even, 0 .. d
+ *  norm, layout        CKDA_NORM_*, CKDA_ROTARY_*
+ *  q_out, k_out        as q and k, ldqo and ldko elements apart; q_out may be
+ *              q itself (same ldq) and k_out k, no other overlap
+ *
+ * Row pointers need their element's alignment only (16 bytes is fastest).
+ * Numerics: fp32, rounded once.
+ */
+int qk_norm_rotary(const void *q, const void *k, const int32_t *positions, const double *freqs,
+                   const float *q_weight, const float *k_weight, int tokens, int Hq, int Hk,
+                   int d, int rd, long long ldq, long long ldk, int norm, int layout, float eps,
+                   float q_scale, float rotary_scale, int in_dtype, void *q_out, void *k_out,
+                   long long ldqo, long long ldko, void *stream);
+
+/* Workspace of qk_norm_rotary_backward in bytes (0 if the sizes are invalid). */
+size_t qk_norm_rotary_backward_workspace_bytes(int tokens, int d);
+
+/*
+ * Backward of qk_norm_rotary: from the gradients dq_out, dk_out of its results
+ * and the same inputs, the gradients dq, d_k (in_dtype) of q and k, and of the
+ * weights (fp32 [d], given exactly where the weight is; summed over all rows
+ * in a fixed order).  ldgq and ldgk are the row distances of dq and d_k.  No
+ * output overlaps anything else.  workspace may be NULL without weights.
+ */
+int qk_norm_rotary_backward(const void *dq_out, const void *dk_out, const void *q, const void *k,
+                            const int32_t *positions, const double *freqs, const float *q_weight,
+                            const float *k_weight, int tokens, int Hq, int Hk, int d, int rd,
+                            long long lddq, long long lddk, long long ldq, long long ldk,
+                            int norm, int layout, float eps, float q_scale, float rotary_scale,
+                            int in_dtype, void *dq, void *d_k, long long ldgq, long long ldgk,
+                            float *dq_weight, float *dk_weight, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
+/*
+ * The rotation alone, of H heads a token; `inverse` turns by the opposite
+ * angle (the backward of the forward rotation).  out may be x (same ldx).
+ */
+int ckda_rotary(const void *x, const int32_t *positions, const double *freqs, int tokens, int H,
+                int d, int rd, long long ldx, int layout, float rotary_scale, int inverse,
+                int in_dtype, void *out, long long ldo, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,224 @@
+"""Host-side refusals of the gated delta rule and of the norm and rotation of
+queries and keys: every call below fails validation before any launch, so the
+addresses are never dereferenced (no GPU needed)."""
+import ctypes
+import math
+import os
+import re
+
+import pytest
+import torch
+
+import gated_delta_rule_22_amd as ck
+from gated_delta_rule_22_amd import _lib
+
+HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include",
+                      "ckda.h")
+NULL, SHAPE, DTYPE, ALIGN, WORKSPACE, ALIAS = 1, 2, 3, 4, 5, 7
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return _lib.library()
+
+
+def _addresses(names, null=(), shift=(), alias=()):
+    a = {n: (i + 1) << 40 for i, n in enumerate(names)}
+    for n, by in shift:
+        a[n] += by
+    for n, of in alias:
+        a[n] = a[of]
+    return {n: None if n in null else ctypes.c_void_p(x) for n, x in a.items()}
+
+
+def test_every_declared_function_is_exported(lib):
+    src = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+    names = set(re.findall(r"\b((?:gdr|qk|ckda_rotary)\w*)\s*\(", src))
+    assert {"gdr_forward", "gdr_decode_step", "qk_norm_rotary", "ckda_rotary",
+            "qk_norm_rotary_backward", "gdr_forward_workspace_bytes"} <= names
+    for n in names:
+        assert hasattr(lib, n), n
+
+
+def _fwd(lib, B=2, T=64, Hk=2, Hv=4, dk=128, dv=128, N=None, dtype=0, ws=1 << 50, cu=False, **kw):
+    names = ["q", "k", "v", "g", "beta", "S0", "cu", "o", "ST", "ws"]
+    p = _addresses(names, **kw)
+    return lib.gdr_forward(p["q"], p["k"], p["v"], p["g"], p["beta"], p["S0"],
+                           p["cu"] if cu else None, B, T, Hk, Hv, dk, dv, B if N is None else N,
+                           dtype, p["o"], p["ST"], p["ws"], ws, None)
+
+
+def test_forward_refusals(lib):
+    for kw in (dict(dk=96), dict(dv=32), dict(Hk=0), dict(Hv=3), dict(Hk=4, Hv=2), dict(B=0),
+               dict(T=-1), dict(N=3), dict(cu=True), dict(T=1 << 28, B=8), dict(Hv=1 << 20)):
+        assert _fwd(lib, **kw) == SHAPE, kw
+    assert _fwd(lib, dtype=2) == DTYPE
+    for n in ("q", "k", "v", "g", "beta", "o"):
+        assert _fwd(lib, null=(n,)) == NULL, n
+    for n in ("q", "k", "v", "S0", "o", "ST", "ws"):
+        assert _fwd(lib, shift=((n, 8),)) == ALIGN, n
+    for n in ("g", "beta"):
+        assert _fwd(lib, shift=((n, 2),)) == ALIGN, n
+    assert _fwd(lib, null=("ws",)) == WORKSPACE
+    need = lib.gdr_forward_workspace_bytes(2, 64, 2, 4, 128, 128, 2, 0)
+    assert need > 0 and _fwd(lib, ws=need - 1) == WORKSPACE
+    for pair in (("o", "q"), ("o", "v"), ("o", "S0"), ("ST", "k"), ("ST", "o"), ("ws", "q"),
+                 ("ws", "o"), ("ws", "ST"), ("ws", "S0"), ("o", "beta")):
+        assert _fwd(lib, alias=(pair,)) == ALIAS, pair
+    # S_T over part of S0, not all of it
+    p = (1 << 46)
+    st = lib.gdr_forward(*[ctypes.c_void_p((i + 1) << 40) for i in range(5)], ctypes.c_void_p(p),
+                         None, 2, 64, 2, 4, 128, 128, 2, 0, ctypes.c_void_p(9 << 40),
+                         ctypes.c_void_p(p + 64), ctypes.c_void_p(10 << 40), 1 << 50, None)
+    assert st == ALIAS
+
+
+def test_workspace_sizes(lib):
+    f = lib.gdr_forward_workspace_bytes
+    assert f(2, 64, 3, 4, 128, 128, 2, 0) == 0 and f(2, 64, 2, 4, 100, 128, 2, 0) == 0
+    assert f(1, 1000, 2, 4, 128, 128, 7, 0) >= f(1, 1000, 2, 4, 128, 128, 1, 0) > 0
+    # no overflow of 32 bits: 2^19 chunks of 64 heads
+    assert f(1, 1 << 25, 32, 32, 64, 64, 1, 0) > 1 << 38
+
+
+def _step(lib, N=3, pool=8, Hk=2, Hv=4, dk=128, dv=64, dtype=0, slots=True, **kw):
+    p = _addresses(["q", "k", "v", "g", "beta", "S", "slots", "o"], **kw)
+    return lib.gdr_decode_step(p["q"], p["k"], p["v"], p["g"], p["beta"], p["S"],
+                               p["slots"] if slots else None, pool, p["o"], N, Hk, Hv, dk, dv,
+                               dtype, None)
+
+
+def test_step_refusals(lib):
+    for kw in (dict(N=0), dict(pool=0), dict(Hv=3), dict(Hk=0), dict(dk=32), dict(dv=256),
+               dict(slots=False), dict(N=1 << 30)):
+        assert _step(lib, **kw) == SHAPE, kw
+    assert _step(lib, dtype=9) == DTYPE
+    for n in ("q", "k", "v", "g", "beta", "S", "o"):
+        assert _step(lib, null=(n,)) == NULL, n
+    for n in ("q", "S", "o"):
+        assert _step(lib, shift=((n, 4),)) == ALIGN, n
+    assert _step(lib, shift=(("slots", 2),)) == ALIGN
+    for pair in (("o", "S"), ("S", "q"), ("o", "v"), ("S", "slots"), ("o", "g")):
+        assert _step(lib, alias=(pair,)) == ALIAS, pair
+
+
+def _norm(lib, tokens=8, Hq=4, Hk=2, d=128, rd=64, ldq=None, ldk=None, ldqo=None, ldko=None,
+          norm=2, layout=0, dtype=0, **kw):
+    p = _addresses(["q", "k", "pos", "freqs", "wq", "wk", "qo", "ko"], **kw)
+    ld = lambda x, h: h * d if x is None else x
+    return lib.qk_norm_rotary(p["q"], p["k"], p["pos"], p["freqs"], p["wq"], p["wk"], tokens, Hq,
+                              Hk, d, rd, ld(ldq, Hq), ld(ldk, Hk), norm, layout, 1e-6, 1.0, 1.0,
+                              dtype, p["qo"], p["ko"], ld(ldqo, Hq), ld(ldko, Hk), None)
+
+
+def test_norm_rotary_refusals(lib):
+    for kw in (dict(d=127), dict(d=258), dict(d=0, rd=0), dict(rd=130), dict(rd=3), dict(rd=-2),
+               dict(norm=3), dict(norm=-1), dict(layout=2), dict(Hq=0, Hk=0), dict(Hq=-1),
+               dict(tokens=-1), dict(ldq=511), dict(ldko=100), dict(ldk=1 << 41)):
+        assert _norm(lib, **kw) == SHAPE, kw
+    assert _norm(lib, dtype=5) == DTYPE
+    for n in ("q", "k", "qo", "ko", "pos", "freqs"):
+        assert _norm(lib, null=(n,)) == NULL, n
+    for n, by in (("q", 1), ("ko", 1), ("pos", 2), ("freqs", 4), ("wq", 2)):
+        assert _norm(lib, shift=((n, by),)) == ALIGN, n
+    for pair in (("qo", "k"), ("ko", "q"), ("qo", "pos"), ("ko", "freqs"), ("qo", "wq"),
+                 ("qo", "ko")):
+        assert _norm(lib, alias=(pair,)) == ALIAS, pair
+    # in place with another row distance
+    assert _norm(lib, alias=(("qo", "q"),), ldq=1024) == ALIAS
+    # q and k of one projection (8 heads a row), results over a shifted q
+    row = 8 * 128
+    p = 1 << 46
+    call = lambda qo: lib.qk_norm_rotary(
+        ctypes.c_void_p(p), ctypes.c_void_p(p + 4 * 256), ctypes.c_void_p(1 << 41),
+        ctypes.c_void_p(1 << 42), None, None, 8, 4, 2, 128, 64, row, row, 2, 0, 1e-6, 1.0, 1.0, 0,
+        ctypes.c_void_p(p + qo), ctypes.c_void_p(1 << 43), row, 256, None)
+    assert call(256) == ALIAS                 # one head to the right: over q and k
+    assert call(3 * 256) == ALIAS             # over q's last head, k and a value head
+    assert call(5 * 256) == ALIAS             # over k's last head, wraps into the next row
+    assert call(8 * 256 - 256) == ALIAS       # wraps into the next token's q
+
+
+def _norm_bwd(lib, tokens=8, Hq=4, Hk=2, d=128, rd=64, ws=1 << 40, norm=2, dtype=0, ldq=None, **kw):
+    p = _addresses(["dqo", "dko", "q", "k", "pos", "freqs", "wq", "wk", "dq", "dk", "dwq", "dwk",
+                    "ws"], **kw)
+    return lib.qk_norm_rotary_backward(
+        p["dqo"], p["dko"], p["q"], p["k"], p["pos"], p["freqs"], p["wq"], p["wk"], tokens, Hq, Hk,
+        d, rd, Hq * d, Hk * d, Hq * d if ldq is None else ldq, Hk * d, norm, 0, 1e-6, 1.0, 1.0,
+        dtype, p["dq"], p["dk"], Hq * d, Hk * d, p["dwq"], p["dwk"], p["ws"], ws, None)
+
+
+def test_norm_rotary_backward_refusals(lib):
+    for kw in (dict(d=300), dict(rd=129), dict(norm=7), dict(tokens=-2), dict(ldq=100)):
+        assert _norm_bwd(lib, **kw) == SHAPE, kw
+    assert _norm_bwd(lib, dtype=2) == DTYPE
+    for n in ("dqo", "dko", "q", "k", "pos", "freqs", "dq", "dk", "dwq", "wk"):
+        assert _norm_bwd(lib, null=(n,)) == NULL, n
+    for n, by in (("dqo", 1), ("dq", 1), ("dwk", 2), ("ws", 8)):
+        assert _norm_bwd(lib, shift=((n, by),)) == ALIGN, n
+    for pair in (("dq", "q"), ("dq", "dqo"), ("dk", "dko"), ("dk", "dq"), ("dwq", "wq"),
+                 ("dwq", "dwk"), ("ws", "q"), ("ws", "dwk"), ("dq", "wk"), ("dwk", "freqs")):
+        assert _norm_bwd(lib, alias=(pair,)) == ALIAS, pair
+    need = lib.qk_norm_rotary_backward_workspace_bytes(8, 128)
+    assert need > 0 and _norm_bwd(lib, ws=need - 1) == WORKSPACE
+    assert _norm_bwd(lib, null=("ws",)) == WORKSPACE
+    assert lib.qk_norm_rotary_backward_workspace_bytes(8, 127) == 0
+
+
+def _rot(lib, tokens=8, H=4, d=64, rd=64, ldx=None, ldo=None, layout=0, dtype=0, **kw):
+    p = _addresses(["x", "pos", "freqs", "out"], **kw)
+    return lib.ckda_rotary(p["x"], p["pos"], p["freqs"], tokens, H, d, rd,
+                           H * d if ldx is None else ldx, layout, 1.0, 0, dtype, p["out"],
+                           H * d if ldo is None else ldo, None)
+
+
+def test_rotary_refusals(lib):
+    for kw in (dict(H=0), dict(d=65), dict(rd=66), dict(layout=-1), dict(ldx=255), dict(tokens=-1)):
+        assert _rot(lib, **kw) == SHAPE, kw
+    assert _rot(lib, dtype=2) == DTYPE
+    for n in ("x", "pos", "freqs", "out"):
+        assert _rot(lib, null=(n,)) == NULL, n
+    assert _rot(lib, alias=(("out", "pos"),)) == ALIAS
+    assert _rot(lib, alias=(("out", "x"),), ldx=512) == ALIAS
+
+
+def test_binding_refusals_on_cpu():
+    """Wrong tensors are refused with a Python error before the library."""
+    q = torch.zeros(1, 4, 2, 64, dtype=torch.bfloat16)
+    g = torch.zeros(1, 4, 2)
+    with pytest.raises(ValueError, match="device"):
+        ck.gdr_forward(q, q, q, g, g)
+    with pytest.raises(TypeError, match="bfloat16 or float32"):
+        ck.gdr_forward(q.half(), q, q, g, g)
+    with pytest.raises(ValueError, match="dimensions"):
+        ck.gdr_forward(q[0], q, q[0], g, g)
+    with pytest.raises(ValueError, match="device"):
+        ck.gdr_decode_step(q[0], q[0], q[0], g[0], g[0], torch.zeros(4, 2, 64, 64))
+    with pytest.raises(ValueError, match="device"):
+        ck.qk_norm_rotary(q, q)
+    with pytest.raises(ValueError, match="device"):
+        ck.rotary(q, None, None)
+
+
+def test_frequencies():
+    f, s = ck.rotary_frequencies(8, 100.0)
+    assert s == 1.0 and f.dtype == torch.float64
+    assert torch.allclose(f, torch.tensor([1.0, 100 ** -0.25, 0.1, 100 ** -0.75], dtype=torch.float64))
+    lin, _ = ck.rotary_frequencies(8, 100.0, scaling="linear", factor=4.0)
+    assert torch.allclose(lin, f / 4)
+    b, _ = ck.rotary_frequencies(8, 100.0, scaling="base", factor=4.0)
+    assert b[0] == 1.0 and torch.isclose(b[-1], f[-1] / 4)
+    # ramp: fast pairs kept, slow pairs divided, monotone between
+    r, s = ck.rotary_frequencies(128, scaling="ramp", factor=8.0, original_length=4096)
+    full, _ = ck.rotary_frequencies(128)
+    ratio = full / r
+    assert ratio[0] == 1 and torch.isclose(ratio[-1], torch.tensor(8.0, dtype=torch.float64))
+    assert bool((ratio[1:] >= ratio[:-1] - 1e-12).all())
+    turns = 4096 * full / (2 * math.pi)
+    assert bool((ratio[turns > 36] == 1).all()) and bool((ratio[turns < 0.9] > 7.99).all())
+    assert s == pytest.approx(0.1 * math.log(8) + 1)
+    for kw in (dict(rotary_dim=7), dict(rotary_dim=0), dict(rotary_dim=8, factor=0.5),
+               dict(rotary_dim=8, scaling="what"), dict(rotary_dim=8, scaling="ramp"),
+               dict(rotary_dim=2, scaling="base"), dict(rotary_dim=8, base=1.0)):
+        with pytest.raises(ValueError):
+            ck.rotary_frequencies(**kw)
