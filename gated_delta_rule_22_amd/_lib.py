@@ -69,6 +69,10 @@ def library() -> ctypes.CDLL:
         lib.gdr_forward_workspace_bytes.restype = sz
         lib.gdr_forward.argtypes = [vp] * 7 + [ci] * 8 + [vp, vp, vp, sz, vp]
         lib.gdr_forward.restype = ci
+        lib.gdr_backward_workspace_bytes.argtypes = [ci] * 8
+        lib.gdr_backward_workspace_bytes.restype = sz
+        lib.gdr_backward.argtypes = [vp] * 7 + [ci] * 8 + [vp] * 8 + [vp, sz, vp]
+        lib.gdr_backward.restype = ci
         lib.gdr_decode_step.argtypes = [vp] * 7 + [ci, vp] + [ci] * 6 + [vp]
         lib.gdr_decode_step.restype = ci
         lib.qk_norm_rotary.argtypes = ([vp] * 6 + [ci] * 5 + [ll] * 2 + [ci] * 2 + [fl] * 3
@@ -342,6 +346,41 @@ def gdr_forward(q, k, v, g, beta, S0=None, cu_seqlens=None, *, out=None, final_s
                                    _ptr(S_T), _ptr(workspace), ws_bytes, _stream(dev))
     _check(st, "gdr_forward")
     return o, S_T
+
+
+def gdr_backward_workspace_bytes(B, T, Hk, Hv, dk, dv, N, dtype) -> int:
+    code = dtype if isinstance(dtype, int) else (CKDA_BF16 if dtype == torch.bfloat16 else CKDA_F32)
+    return int(library().gdr_backward_workspace_bytes(B, T, Hk, Hv, dk, dv, N, code))
+
+
+def gdr_backward(q, k, v, g, beta, do, S0=None, dS_T=None, cu_seqlens=None, *, workspace=None,
+                 need_dS0=True):
+    """Gradients of ``sum(do * o) + sum(dS_T * S_T)`` of :func:`gdr_forward`:
+    ``(dq, dk, dv, dg, dbeta, dS0)``, the first three in the type of ``q``, the
+    others fp32 (``dS0`` is None when ``need_dS0`` is False).  See
+    ``gdr_backward`` in include/ckda.h."""
+    code = _dtype_code(q)
+    B, T, Hk, Hv, dk, dv, N = _gdr_sizes(q, k, v, g, beta, cu_seqlens)
+    _need(do, "do", q.dtype, (B, T, Hv, dv))
+    for t, n in ((S0, "S0"), (dS_T, "dS_T")):
+        if t is not None:
+            _need(t, n, torch.float32, (N, Hv, dk, dv))
+    dev = q.device
+    f32 = dict(dtype=torch.float32, device=dev)
+    dq, dk_, dv_ = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    dg, db = torch.empty((B, T, Hv), **f32), torch.empty((B, T, Hv), **f32)
+    dS0 = torch.empty((N, Hv, dk, dv), **f32) if need_dS0 else None
+    ws_bytes = gdr_backward_workspace_bytes(B, T, Hk, Hv, dk, dv, N, code)
+    if workspace is None or workspace.numel() * workspace.element_size() < ws_bytes:
+        workspace = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=dev)
+    _same_device(dev, k, v, g, beta, do, S0, dS_T, cu_seqlens, workspace)
+    with torch.cuda.device(dev):
+        st = library().gdr_backward(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S0),
+                                    _ptr(cu_seqlens), B, T, Hk, Hv, dk, dv, N, code, _ptr(do),
+                                    _ptr(dS_T), _ptr(dq), _ptr(dk_), _ptr(dv_), _ptr(dg),
+                                    _ptr(db), _ptr(dS0), _ptr(workspace), ws_bytes, _stream(dev))
+    _check(st, "gdr_backward")
+    return dq, dk_, dv_, dg, db, dS0
 
 
 def gdr_decode_step(q, k, v, g, beta, S, slots=None, *, out=None):

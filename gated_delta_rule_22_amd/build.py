@@ -20,7 +20,7 @@ LIB = os.path.join(PKG, "libckda.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["api.hip", "api_gdr.hip", "schedule.hip", "decode.hip", "fwd_f64.hip", "fwd_bf16.hip",
-           "bwd_f64.hip", "gdr_step.hip", "gdr_chunk.hip", "rotary.hip"]
+           "bwd_f64.hip", "gdr_step.hip", "gdr_chunk.hip", "gdr_bwd.hip", "rotary.hip"]
 
 # Packed fp32 VALU ops stay off: the compiler is not allowed to form them.
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall",

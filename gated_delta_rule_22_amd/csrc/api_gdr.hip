@@ -140,6 +140,116 @@ extern "C" int gdr_decode_step(const void *q, const void *k, const void *v, cons
   return r == hipSuccess ? CKDA_OK : CKDA_ERR_LAUNCH;
 }
 
+namespace {
+
+// Workspace of the backward.  bf16 inputs: the sequence table, then per
+// (chunk, value head) the records, S, E, dS and F.  fp32 inputs: the table,
+// the expanded q, k, gates and their gradients, then the fp64 backward's own
+// workspace (its table included).
+struct GdrBwdLayout {
+  size_t n_chunks, total;
+  size_t rec, S, E, dS, F;               // bf16
+  size_t x[6], inner;                    // fp32
+};
+
+GdrBwdLayout gdr_bwd_layout(int B, int T, int Hv, int dk, int dv, int N, int in_dtype) {
+  GdrBwdLayout L{};
+  L.n_chunks = chunks_ub(B, T, N);
+  const size_t ch = L.n_chunks * Hv;
+  size_t at = align256(sizeof(int32_t) * (4 * (size_t)N + 1));
+  auto take = [&](size_t n) { const size_t p = at; at += align256(n); return p; };
+  if (in_dtype == CKDA_BF16) {
+    const GdrBwdBytes b = gdr_backward_bytes(dk, dv);
+    L.rec = take(ch * b.rec);
+    L.S = take(ch * b.state);
+    L.E = take(ch * b.rows);
+    L.dS = take(ch * b.state);
+    L.F = take(ch * b.rows);
+  } else {
+    for (size_t &x : L.x) x = take((size_t)B * T * Hv * dk * 4);
+    L.inner = take(ckda_backward_workspace_bytes(B, T, Hv, dk, dv, N, CKDA_F32));
+  }
+  L.total = at;
+  return L;
+}
+
+}  // namespace
+
+extern "C" size_t gdr_backward_workspace_bytes(int B, int T, int Hk, int Hv, int dk, int dv, int N,
+                                               int in_dtype) {
+  if (gdr_shape_status(B, T, Hk, Hv, dk, dv, N, in_dtype, B == 1 && N != B) != CKDA_OK) return 0;
+  return gdr_bwd_layout(B, T, Hv, dk, dv, N, in_dtype).total;
+}
+
+extern "C" int gdr_backward(const void *q, const void *k, const void *v, const float *g,
+                            const float *beta, const float *S0, const int32_t *cu_seqlens, int B,
+                            int T, int Hk, int Hv, int dk, int dv, int N, int in_dtype,
+                            const void *d_o, const float *dS_T, void *dq, void *d_k, void *d_v,
+                            float *dg, float *dbeta, float *dS0, void *workspace,
+                            size_t workspace_bytes, void *stream) {
+  const bool packed = cu_seqlens != nullptr;
+  if (int s = gdr_shape_status(B, T, Hk, Hv, dk, dv, N, in_dtype, packed)) return s;
+  const size_t rows = (size_t)B * T;
+  if (rows > 0 &&
+      (!q || !k || !v || !g || !beta || !d_o || !dq || !d_k || !d_v || !dg || !dbeta))
+    return CKDA_ERR_NULL;
+  const void *ptrs[] = {q, k, v, S0, d_o, dS_T, dq, d_k, d_v, dS0, workspace};
+  for (const void *p : ptrs)
+    if (p && !aligned16(p)) return CKDA_ERR_ALIGN;
+  const void *small[] = {g, beta, cu_seqlens, dg, dbeta};
+  for (const void *p : small)
+    if (p && !aligned4(p)) return CKDA_ERR_ALIGN;
+  const size_t e = in_dtype == CKDA_BF16 ? 2 : 4;
+  const size_t st_bytes = (size_t)N * Hv * dk * dv * 4;
+  const size_t nq = rows * Hk * dk * e, nv = rows * Hv * dv * e, ng = rows * Hv * 4;
+  const GdrBwdLayout L = gdr_bwd_layout(B, T, Hv, dk, dv, N, in_dtype);
+  const Span ins[] = {{q, nq}, {k, nq}, {v, nv}, {g, ng}, {beta, ng}, {S0, st_bytes},
+                      {cu_seqlens, ((size_t)N + 1) * 4}, {d_o, nv}, {dS_T, st_bytes}};
+  const Span outs[] = {{dq, nq}, {d_k, nq}, {d_v, nv}, {dg, ng}, {dbeta, ng}, {dS0, st_bytes},
+                       {workspace, L.total}};
+  constexpr int n_outs = sizeof(outs) / sizeof(outs[0]);
+  for (int a = 0; a < n_outs; ++a) {
+    for (const Span &s : ins)
+      if (overlaps(outs[a].p, outs[a].n, s.p, s.n)) return CKDA_ERR_ALIAS;
+    for (int b = a + 1; b < n_outs; ++b)
+      if (overlaps(outs[a].p, outs[a].n, outs[b].p, outs[b].n)) return CKDA_ERR_ALIAS;
+  }
+  if (!workspace || workspace_bytes < L.total) return CKDA_ERR_WORKSPACE;
+
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  if (int s = debug_prologue(cu_seqlens, N, T, workspace, L.total, st)) return s;
+  char *w = static_cast<char *>(workspace);
+  const SeqTable tab = seq_table(workspace, N);
+  if (launch_seq_table(cu_seqlens, B, T, N, tab, st) != hipSuccess) return CKDA_ERR_LAUNCH;
+  if (in_dtype == CKDA_BF16) {
+    GdrBwdArgs a{};
+    a.fwd.q = q; a.fwd.k = k; a.fwd.v = v; a.fwd.g = g; a.fwd.beta = beta; a.fwd.S0 = S0;
+    a.fwd.tab = tab; a.fwd.n_chunks_ub = L.n_chunks;
+    a.fwd.N = N; a.fwd.Hk = Hk; a.fwd.Hv = Hv; a.fwd.dk = dk; a.fwd.dv = dv;
+    a.d_o = d_o; a.dS_T = dS_T;
+    a.rec = w + L.rec; a.S = w + L.S; a.E = w + L.E; a.dS = w + L.dS; a.F = w + L.F;
+    a.dq = dq; a.dk = d_k; a.dv = d_v; a.dg = dg; a.dbeta = dbeta; a.dS0 = dS0;
+    return launch_gdr_backward(a, st) == hipSuccess ? CKDA_OK : CKDA_ERR_LAUNCH;
+  }
+  float *x[6];
+  for (int i = 0; i < 6; ++i) x[i] = reinterpret_cast<float *>(w + L.x[i]);
+  if (rows > 0 &&
+      launch_gdr_expand(static_cast<const float *>(q), static_cast<const float *>(k), g, rows, Hk,
+                        Hv, dk, x[0], x[1], x[2], st) != hipSuccess)
+    return CKDA_ERR_LAUNCH;
+  // The per-channel backward, signs ignored (the gates are positive).
+  if (int s = kda_backward(x[0], x[1], v, x[2], beta, S0, cu_seqlens, B, T, Hv, dk, dv, N, CKDA_F32,
+                           static_cast<const float *>(d_o), dS_T, x[3], x[4],
+                           static_cast<float *>(d_v), x[5], dbeta, dS0, w + L.inner,
+                           L.total - L.inner, stream))
+    return s;
+  if (rows > 0 &&
+      launch_gdr_collect(x[3], x[4], x[5], g, tab, N, rows, Hk, Hv, dk, static_cast<float *>(dq),
+                         static_cast<float *>(d_k), dg, st) != hipSuccess)
+    return CKDA_ERR_LAUNCH;
+  return CKDA_OK;
+}
+
 // ---------------------------------------------------------------- norm and rotation
 namespace {
 

@@ -1,0 +1,494 @@
+// Backward of the chunkwise gated delta rule for bf16 inputs.
+//
+// With dS' the gradient of the state behind the chunk and the forward's
+// symbols (gdr_chunk.hip):
+//
+//   dU = P^T dO + (gam_n / gam) K dS'        F = T'^T (beta dU)   ( = dV )
+//   dS = gam_n dS' + Q^T (gam dO) - K^T (gam F)
+//   dP_ij = r_ij dO_i.U_j                    dA_ij = -r_ij beta_j F_i.E_j
+//   dQ = gam dO S^T + dP K
+//   dK = [-gam F S^T + dA K] + [dP^T Q + dA^T K + (gam_n / gam) U dS'^T]
+//   dbeta = F.E / beta
+//   dG_i = q_i.dQ_i + k_i.dK_i[first bracket] - k_i.dK_i[second bracket]
+//   dg_t = sum_{i >= t} dG_i + sum_j w_j + gam_n <S, dS'>
+//
+// where w_j is the last term's part of k_j.dK_j.  (U = beta E and beta is kept
+// off zero by kBetaFloor, so F.E / beta holds at beta = 0 too.)
+//
+// Three passes: the forward's chain kept per chunk (S, E), the chain of dS
+// backwards (dS', F), each serial in the chunks of a (sequence, head), and the
+// gradients, parallel over chunks.  Everything that feeds an fp32 gradient
+// (dg, dbeta, dS0) runs in two bf16 terms, as in the forward.
+#include "gdr_chunk.h"
+
+namespace ckda {
+using namespace gdr;
+namespace {
+
+__device__ __forceinline__ bool chain_block(int nblk, int pairs, int &pair, int &blk) {
+  const int b = blockIdx.x;              // as in the forward: a head's blocks share an XCD
+  blk = (b / 8) % nblk;
+  pair = (b / 8 / nblk) * 8 + b % 8;
+  return pair < pairs;
+}
+
+// The chain of dS, last chunk first; a wave owns 16 of the DV columns as in
+// the forward's chain, so dS -> dU -> F -> dS stays in its registers.
+template <int DK, int DV>
+__global__ __launch_bounds__(kThreads, 1) void reverse_kernel(
+    const __hip_bfloat16 *__restrict__ q, const __hip_bfloat16 *__restrict__ k,
+    const __hip_bfloat16 *__restrict__ d_o, const float *__restrict__ dS_T, SeqTable tab, int N,
+    int Hk, int Hv, const char *__restrict__ rec_base, char *__restrict__ dS_keep,
+    char *__restrict__ F_keep, float *__restrict__ dS0) {
+  constexpr int KS = DK / 32, MT = DK / 16, BV = 64;
+  constexpr int kK = 0, kQ = kK + C * kStride<DK>, kD = kQ + C * kStride<DK>;
+  constexpr int kR = kD + C * kStride<BV>, kBuf = kR + kRecBwd;
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  int pair, blk;
+  if (!chain_block(DV / BV, N * Hv, pair, blk)) return;
+  const int seq = tab.order[pair / Hv], hv = pair % Hv, hk = hv / (Hv / Hk);
+  const int t = threadIdx.x, wave = t >> 6, lane = t & 63, m = lane & 15, h = lane >> 4;
+  const int len = tab.seq_len[seq], chunks = (len + C - 1) / C;
+  const size_t row0 = tab.seq_start[seq];
+  const size_t c0 = tab.chunk_off[seq];
+  const int col = blk * BV + 16 * wave;
+
+  f4 S[MT];                              // dS
+  const size_t sbase = ((size_t)seq * Hv + hv) * DK * DV + col + m;
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      S[i][r] = dS_T ? dS_T[sbase + (size_t)(16 * i + 4 * h + r) * DV] : 0.f;
+
+  Stage<DK> gk, gq;
+  Stage<BV> gd;
+  Linear<kRecBwd> gr;
+  auto fetch = [&](int c) {
+    const int valid = min(C, len - c * C);
+    const size_t row = row0 + (size_t)c * C;
+    gk.load(k + (row * Hk + hk) * DK, (size_t)Hk * DK, valid, t);
+    gq.load(q + (row * Hk + hk) * DK, (size_t)Hk * DK, valid, t);
+    gd.load(d_o + (row * Hv + hv) * DV + blk * BV, (size_t)Hv * DV, valid, t);
+    gr.load(rec_base + ((c0 + c) * Hv + hv) * kRecBwd, t);
+  };
+  auto put = [&](char *buf) {
+    gk.store(buf + kK, t);
+    gq.store(buf + kQ, t);
+    gd.store(buf + kD, t);
+    gr.store(buf + kR, t);
+  };
+  if (chunks > 0) {
+    fetch(chunks - 1);
+    put(lds + ((chunks - 1) & 1) * kBuf);
+  }
+  __syncthreads();
+  for (int c = chunks - 1; c >= 0; --c) {
+    const char *buf = lds + (c & 1) * kBuf;
+    const char *K = buf + kK, *Q = buf + kQ, *D = buf + kD, *R = buf + kR;
+    const float *gate = reinterpret_cast<const float *>(R + kRecGate);
+    if (c > 0) fetch(c - 1);
+
+    Split sf[KS];
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) sf[ks] = split8(S[2 * ks], S[2 * ks + 1]);
+    {
+      char *p = dS_keep + (((c0 + c) * Hv + hv) * (2 * MT * (DV / 16)) + col / 16) * 512 + lane * 8;
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const bf8 hi = sf[i / 2].hi, lo = sf[i / 2].lo;
+        *reinterpret_cast<bf4 *>(p + i * (DV / 16) * 512) =
+            i % 2 ? __builtin_shufflevector(hi, hi, 4, 5, 6, 7)
+                  : __builtin_shufflevector(hi, hi, 0, 1, 2, 3);
+        *reinterpret_cast<bf4 *>(p + (MT + i) * (DV / 16) * 512) =
+            i % 2 ? __builtin_shufflevector(lo, lo, 4, 5, 6, 7)
+                  : __builtin_shufflevector(lo, lo, 0, 1, 2, 3);
+      }
+    }
+    f4 d[4];                             // dO: lane = column, 4 tokens a tile
+#pragma unroll
+    for (int it = 0; it < 4; ++it) d[it] = widen4(cols_quad<BV>(D, 16 * it, 16 * wave, lane));
+    const bf8 d0 = join(round4(d[0]), round4(d[1])), d1 = join(round4(d[2]), round4(d[3]));
+    f4 X[4];                             // beta dU
+#pragma unroll
+    for (int jt = 0; jt < 4; ++jt) {
+      f4 y = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+        y = dot2(rows_frag<DK>(K, 16 * jt, 32 * ks, lane), sf[ks], y);
+      y *= *reinterpret_cast<const f4 *>(gate + kLast * C + 16 * jt + 4 * h);
+#pragma unroll
+      for (int ks = jt / 2; ks < 2; ++ks) {
+        const Split P = {tri_frag_t(R + kRecPh, jt, ks, lane), tri_frag_t(R + kRecPl, jt, ks, lane)};
+        y = dot2(P, ks ? d1 : d0, y);
+      }
+      X[jt] = y * *reinterpret_cast<const f4 *>(gate + kBeta * C + 16 * jt + 4 * h);
+    }
+    const Split x0 = split8(X[0], X[1]), x1 = split8(X[2], X[3]);
+    f4 F[4];
+    char *p = F_keep + (((c0 + c) * Hv + hv) * (8 * (DV / 16)) + col / 16) * 512 + lane * 8;
+#pragma unroll
+    for (int jt = 0; jt < 4; ++jt) {
+      F[jt] = 0.f;
+#pragma unroll
+      for (int ks = jt / 2; ks < 2; ++ks) {
+        const Split T = {tri_frag_t(R + kRecTh, jt, ks, lane), tri_frag_t(R + kRecTl, jt, ks, lane)};
+        F[jt] = dot3(T, ks ? x1 : x0, F[jt]);
+      }
+      bf4 x, y;
+      split4(F[jt], x, y);
+      *reinterpret_cast<bf4 *>(p + jt * (DV / 16) * 512) = x;
+      *reinterpret_cast<bf4 *>(p + (4 + jt) * (DV / 16) * 512) = y;
+      const f4 gam = *reinterpret_cast<const f4 *>(gate + kGam * C + 16 * jt + 4 * h);
+      F[jt] *= -gam;
+      d[jt] *= gam;
+    }
+    const Split f0 = split8(F[0], F[1]), f1 = split8(F[2], F[3]);
+    const Split e0 = split8(d[0], d[1]), e1 = split8(d[2], d[3]);
+    const float gn = gate[kGam * C + C - 1];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      S[i] *= gn;
+      S[i] = dot2(cols_frag<DK>(Q, 0, 16 * i, lane), e0, S[i]);
+      S[i] = dot2(cols_frag<DK>(Q, 32, 16 * i, lane), e1, S[i]);
+      S[i] = dot2(cols_frag<DK>(K, 0, 16 * i, lane), f0, S[i]);
+      S[i] = dot2(cols_frag<DK>(K, 32, 16 * i, lane), f1, S[i]);
+    }
+    if (c > 0) put(lds + ((c - 1) & 1) * kBuf);
+    __syncthreads();
+  }
+  if (dS0)
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        dS0[sbase + (size_t)(16 * i + 4 * h + r) * DV] = S[i][r];
+}
+
+// ---------------------------------------------------------------- gradients
+// One workgroup per (chunk, query/key head); it goes over the group's value
+// heads one after another, so dQ and dK of a shared head are summed in
+// registers, in a fixed order.  Wave w owns tokens 16 w .. 16 w + 15: as rows
+// i it needs the tiles j <= w of the triangular products, as columns j the
+// tiles i >= w, five tiles for every wave.  Results have lane = token and 4
+// key channels a lane, so stores are 8 bytes and q.dq needs two exchanges.
+template <int DK, int DV> struct GradLds {
+  static constexpr int kK = 0, kQ = kK + C * kStride<DK>, kGate = kQ + C * kStride<DK>;
+  static constexpr int kSum = kGate + kGateBytes, kX = kSum + 512;
+  static constexpr int kD = kX, kE = kD + C * kStride<DV>, kF = kE + 4 * C * DV;
+  static constexpr int kEnd1 = kF + 4 * C * DV, kEnd2 = kX + 4 * DK * DV;
+  static constexpr int kBytes = kEnd1 > kEnd2 ? kEnd1 : kEnd2;
+};
+
+__device__ __forceinline__ float sum4(f4 a) { return (a[0] + a[1]) + (a[2] + a[3]); }
+__device__ __forceinline__ float over_quarters(float x) {
+  x += __shfl_xor(x, 16);
+  return x + __shfl_xor(x, 32);
+}
+
+template <int DK, int DV>
+__global__ __launch_bounds__(kThreads, 1) void grad_kernel(
+    const __hip_bfloat16 *__restrict__ q, const __hip_bfloat16 *__restrict__ k,
+    const float *__restrict__ g, const float *__restrict__ beta,
+    const __hip_bfloat16 *__restrict__ d_o, SeqTable tab, int N, int Hk, int Hv,
+    const char *__restrict__ rec_base, const char *__restrict__ S_keep,
+    const char *__restrict__ E_keep, const char *__restrict__ dS_keep,
+    const char *__restrict__ F_keep, __hip_bfloat16 *__restrict__ dq,
+    __hip_bfloat16 *__restrict__ dk_out, __hip_bfloat16 *__restrict__ dv_out,
+    float *__restrict__ dg, float *__restrict__ dbeta) {
+  using L = GradLds<DK, DV>;
+  constexpr int MT = DK / 16, NT = DV / 16, KV = DV / 32;
+  constexpr int kPlane = DK * DV * 2;    // bytes of one term of a state
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  const int chunk = blockIdx.x / Hk, hk = blockIdx.x % Hk, rep = Hv / Hk;
+  if (chunk >= tab.chunk_off[N]) return;
+  const int seq = find_seq(tab, N, chunk);
+  const int at = (chunk - tab.chunk_off[seq]) * C;
+  const int valid = min(C, tab.seq_len[seq] - at);
+  const size_t row0 = (size_t)tab.seq_start[seq] + at;
+  const int t = threadIdx.x, w = t >> 6, lane = t & 63, m = lane & 15, h = lane >> 4;
+  const int tok = 16 * w + m;            // this lane's token
+  const char *K = lds + L::kK, *Q = lds + L::kQ;
+  float *gate = reinterpret_cast<float *>(lds + L::kGate);
+  float *s_dG = reinterpret_cast<float *>(lds + L::kSum), *s_n = s_dG + C;
+
+  {
+    Stage<DK> a, b;
+    a.load(k + (row0 * Hk + hk) * DK, (size_t)Hk * DK, valid, t);
+    b.load(q + (row0 * Hk + hk) * DK, (size_t)Hk * DK, valid, t);
+    a.store(lds + L::kK, t);
+    b.store(lds + L::kQ, t);
+  }
+  f4 dQ[MT], dK[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) dQ[i] = dK[i] = 0.f;
+
+  for (int u = 0; u < rep; ++u) {
+    const int hv = hk * rep + u;
+    const size_t ch = (size_t)chunk * Hv + hv;
+    {
+      Stage<DV> a;
+      Linear<4 * C * DV> e, f;
+      a.load(d_o + (row0 * Hv + hv) * DV, (size_t)Hv * DV, valid, t);
+      e.load(E_keep + ch * (4 * C * DV), t);
+      f.load(F_keep + ch * (4 * C * DV), t);
+      const float *rg = reinterpret_cast<const float *>(rec_base + ch * kRecBwd + kRecGate);
+      float ga = rg[t], gb = t < 2 * C ? rg[kThreads + t] : 0.f;
+      a.store(lds + L::kD, t);
+      e.store(lds + L::kE, t);
+      f.store(lds + L::kF, t);
+      gate[t] = ga;
+      if (t < 2 * C) gate[kThreads + t] = gb;
+    }
+    __syncthreads();
+    const char *D = lds + L::kD;
+    auto tile_split = [&](const char *base, int row, int rows, int ks) {
+      const char *a = base + (row * NT + 2 * ks) * 512, *b = a + rows * NT * 512;
+      return Split{join(tile_quad_t(a, lane), tile_quad_t(a + 512, lane)),
+                   join(tile_quad_t(b, lane), tile_quad_t(b + 512, lane))};
+    };
+    auto Ef = [&](int tile, int ks) { return tile_split(lds + L::kE, tile, 4, ks); };
+    auto Ff = [&](int tile, int ks) { return tile_split(lds + L::kF, tile, 4, ks); };
+    bf8 d[KV];
+    Split e[KV], f[KV];
+#pragma unroll
+    for (int ks = 0; ks < KV; ++ks) {
+      d[ks] = rows_frag<DV>(D, 16 * w, 32 * ks, lane);
+      e[ks] = Ef(w, ks);
+      f[ks] = Ff(w, ks);
+    }
+    const float ghi = gate[kGhi * C + tok], glo = gate[kGlo * C + tok];
+    const float bet = gate[kBeta * C + tok], gam = gate[kGam * C + tok];
+
+    // The triangular products, as operands: [lane i, over j] and [lane j, over i].
+    Split pt[2], at_[2], pn[2], an[2];
+    {
+      f4 p[4], a[4];
+#pragma unroll
+      for (int jt = 0; jt < 4; ++jt) {
+        p[jt] = a[jt] = 0.f;
+        if (jt <= w) {
+#pragma unroll
+          for (int ks = 0; ks < KV; ++ks) {
+            const Split x = Ef(jt, ks);
+            p[jt] = dot2(x, d[ks], p[jt]);
+            a[jt] = dot3(x, f[ks], a[jt]);
+          }
+          const f4 hj = *reinterpret_cast<const f4 *>(gate + kGhi * C + 16 * jt + 4 * h);
+          const f4 lj = *reinterpret_cast<const f4 *>(gate + kGlo * C + 16 * jt + 4 * h);
+          const f4 bj = *reinterpret_cast<const f4 *>(gate + kBeta * C + 16 * jt + 4 * h);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int j = 16 * jt + 4 * h + r;
+            const float x = exp2f((ghi - hj[r]) + (glo - lj[r])) * bj[r];
+            p[jt][r] = tok >= j ? p[jt][r] * x : 0.f;
+            a[jt][r] = tok > j ? -a[jt][r] * x : 0.f;
+          }
+        }
+      }
+      pt[0] = split8(p[0], p[1]); pt[1] = split8(p[2], p[3]);
+      at_[0] = split8(a[0], a[1]); at_[1] = split8(a[2], a[3]);
+#pragma unroll
+      for (int it = 0; it < 4; ++it) {
+        p[it] = a[it] = 0.f;
+        if (it >= w) {
+#pragma unroll
+          for (int ks = 0; ks < KV; ++ks) {
+            p[it] = dot2(rows_frag<DV>(D, 16 * it, 32 * ks, lane), e[ks], p[it]);
+            a[it] = dot3(Ff(it, ks), e[ks], a[it]);
+          }
+          const f4 hi = *reinterpret_cast<const f4 *>(gate + kGhi * C + 16 * it + 4 * h);
+          const f4 li = *reinterpret_cast<const f4 *>(gate + kGlo * C + 16 * it + 4 * h);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int i = 16 * it + 4 * h + r;
+            const float x = exp2f((hi[r] - ghi) + (li[r] - glo)) * bet;
+            p[it][r] = i >= tok ? p[it][r] * x : 0.f;
+            a[it][r] = i > tok ? -a[it][r] * x : 0.f;
+          }
+        }
+      }
+      pn[0] = split8(p[0], p[1]); pn[1] = split8(p[2], p[3]);
+      an[0] = split8(a[0], a[1]); an[1] = split8(a[2], a[3]);
+    }
+    // dV and dbeta from the wave's own rows.
+    {
+      float s = 0.f;
+      const float own = tok < valid ? beta[(row0 + tok) * Hv + hv] : 0.f;
+      const float back = own / bet;      // 1, or below 1 where beta was raised
+      __hip_bfloat16 *o = dv_out + ((row0 + tok) * Hv + hv) * DV;
+#pragma unroll
+      for (int ks = 0; ks < KV; ++ks)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          auto part = [&](const Split &x) {
+            const bf4 a = half ? __builtin_shufflevector(x.hi, x.hi, 4, 5, 6, 7)
+                               : __builtin_shufflevector(x.hi, x.hi, 0, 1, 2, 3);
+            const bf4 b = half ? __builtin_shufflevector(x.lo, x.lo, 4, 5, 6, 7)
+                               : __builtin_shufflevector(x.lo, x.lo, 0, 1, 2, 3);
+            return widen4(a) + widen4(b);
+          };
+          const f4 x = part(f[ks]);
+          s += sum4(x * part(e[ks]));
+          if (tok < valid)
+            *reinterpret_cast<bf4 *>(o + 32 * ks + 16 * half + 4 * h) = round4(x * back);
+        }
+      s = over_quarters(s);
+      if (h == 0 && tok < valid) dbeta[(row0 + tok) * Hv + hv] = s / bet;
+    }
+    __syncthreads();
+    {
+      Linear<2 * kPlane> s;
+      s.load(S_keep + ch * (2 * kPlane), t);
+      s.store(lds + L::kX, t);
+    }
+    __syncthreads();
+    auto Sf = [&](int mt, int ks) { return tile_split(lds + L::kX, mt, MT, ks); };
+    float dG = 0.f;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      f4 a = 0.f, b = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < KV; ++ks) {
+        const Split s = Sf(mt, ks);
+        a = dot2(s, d[ks], a);
+        b = dot3(s, f[ks], b);
+      }
+      a *= gam;
+      b *= -gam;
+      const bf8 k0 = cols_frag<DK>(K, 0, 16 * mt, lane), k1 = cols_frag<DK>(K, 32, 16 * mt, lane);
+      const bf8 q0 = cols_frag<DK>(Q, 0, 16 * mt, lane), q1 = cols_frag<DK>(Q, 32, 16 * mt, lane);
+      a = dot2(k0, pt[0], a);
+      b = dot2(k0, at_[0], b);
+      if (w >= 2) {                      // tiles j >= 32 lie above the diagonal for w < 2
+        a = dot2(k1, pt[1], a);
+        b = dot2(k1, at_[1], b);
+      }
+      f4 c = 0.f;
+      if (w < 2) {
+        c = dot2(q0, pn[0], c);
+        c = dot2(k0, an[0], c);
+      }
+      c = dot2(q1, pn[1], c);
+      c = dot2(k1, an[1], c);
+      const int off = tok * kStride<DK> + (16 * mt + 4 * h) * 2;
+      const f4 qv = widen4(*reinterpret_cast<const bf4 *>(Q + off));
+      const f4 kv = widen4(*reinterpret_cast<const bf4 *>(K + off));
+      dG += sum4(qv * a) + sum4(kv * (b - c));
+      dQ[mt] += a;
+      dK[mt] += b + c;
+    }
+    // <S, dS'>, then dS' in place of S.
+    float dot = 0.f;
+    {
+      Linear<2 * kPlane> s;
+      s.load(dS_keep + ch * (2 * kPlane), t);
+      constexpr int kHalf = kPlane / (kThreads * 16);
+#pragma unroll
+      for (int i = 0; i < kHalf; ++i) {
+        const char *p = lds + L::kX + (t + i * kThreads) * 16;
+        const uint4 a = *reinterpret_cast<const uint4 *>(p);
+        const uint4 b = *reinterpret_cast<const uint4 *>(p + kPlane);
+        const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+        const uint4 c = s.r[i], e2 = s.r[i + kHalf];
+        const uint32_t z[4] = {c.x, c.y, c.z, c.w}, v[4] = {e2.x, e2.y, e2.z, e2.w};
+        auto low = [](uint32_t a) { return __uint_as_float(a << 16); };
+        auto high = [](uint32_t a) { return __uint_as_float(a & 0xFFFF0000u); };
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          dot += (low(x[j]) + low(y[j])) * (low(z[j]) + low(v[j])) +
+                 (high(x[j]) + high(y[j])) * (high(z[j]) + high(v[j]));
+      }
+      __syncthreads();
+      s.store(lds + L::kX, t);
+    }
+    __syncthreads();
+    const float lb = gate[kLastBeta * C + tok];
+    float ws = 0.f;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      f4 c = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < KV; ++ks) c = dot3(Sf(mt, ks), e[ks], c);
+      c *= lb;
+      const f4 kv = widen4(*reinterpret_cast<const bf4 *>(K + tok * kStride<DK> +
+                                                          (16 * mt + 4 * h) * 2));
+      ws += sum4(kv * c);
+      dK[mt] += c;
+    }
+    dG = over_quarters(dG - ws);
+    if (h == 0) s_dG[tok] = dG;
+    // sum_j w_j + gam_n <S, dS'> over the workgroup
+    float n = ws + gate[kGam * C + C - 1] * dot;
+    for (int o = 32; o > 0; o >>= 1) n += __shfl_xor(n, o);
+    if (lane == 0) s_n[w] = n;
+    __syncthreads();
+    if (w == 0) {
+      float x = s_dG[lane];
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const float y = __shfl_down(x, o);
+        if (lane + o < 64) x += y;
+      }
+      x += (s_n[0] + s_n[1]) + (s_n[2] + s_n[3]);
+      if (lane < valid) {
+        const size_t gi = (row0 + lane) * Hv + hv;
+        dg[gi] = g[gi] < (float)kGateFloor ? 0.f : x;   // a floored gate is constant
+      }
+    }
+    __syncthreads();
+  }
+  if (tok < valid) {
+    const size_t o = ((row0 + tok) * Hk + hk) * DK + 4 * h;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      *reinterpret_cast<bf4 *>(dq + o + 16 * mt) = round4(dQ[mt]);
+      *reinterpret_cast<bf4 *>(dk_out + o + 16 * mt) = round4(dK[mt]);
+    }
+  }
+}
+
+template <int DK, int DV> hipError_t backward_typed(const GdrBwdArgs &a, hipStream_t st) {
+  const GdrArgs &f = a.fwd;
+  const auto *q = static_cast<const __hip_bfloat16 *>(f.q);
+  const auto *k = static_cast<const __hip_bfloat16 *>(f.k);
+  const auto *d_o = static_cast<const __hip_bfloat16 *>(a.d_o);
+  char *rec = static_cast<char *>(a.rec), *S = static_cast<char *>(a.S);
+  char *E = static_cast<char *>(a.E), *dS = static_cast<char *>(a.dS);
+  char *F = static_cast<char *>(a.F);
+  if (hipError_t e = launch_gdr_keep(f, rec, S, E, st); e != hipSuccess) return e;
+  constexpr int lds = 2 * (2 * C * kStride<DK> + C * kStride<64> + kRecBwd);
+  auto *rev = reverse_kernel<DK, DV>;
+  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(rev),
+                                     hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  if (e != hipSuccess) return e;
+  const unsigned pairs = (unsigned)((f.N * f.Hv + 7) / 8 * 8);
+  hipLaunchKernelGGL(rev, dim3(pairs * (DV / 64)), dim3(kThreads), lds, st, q, k, d_o, a.dS_T,
+                     f.tab, f.N, f.Hk, f.Hv, rec, dS, F, a.dS0);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  if (f.n_chunks_ub == 0) return hipSuccess;
+  auto *gr = grad_kernel<DK, DV>;
+  constexpr int gl = GradLds<DK, DV>::kBytes;
+  e = hipFuncSetAttribute(reinterpret_cast<const void *>(gr),
+                          hipFuncAttributeMaxDynamicSharedMemorySize, gl);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(gr, dim3((unsigned)(f.n_chunks_ub * f.Hk)), dim3(kThreads), gl, st, q, k, f.g,
+                     f.beta, d_o, f.tab, f.N, f.Hk, f.Hv, rec, S, E, dS, F,
+                     static_cast<__hip_bfloat16 *>(a.dq), static_cast<__hip_bfloat16 *>(a.dk),
+                     static_cast<__hip_bfloat16 *>(a.dv), a.dg, a.dbeta);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+GdrBwdBytes gdr_backward_bytes(int dk, int dv) {
+  return {(size_t)kRecBwd, (size_t)4 * dk * dv, (size_t)4 * C * dv};
+}
+
+hipError_t launch_gdr_backward(const GdrBwdArgs &a, hipStream_t stream) {
+  if (a.fwd.dk == 64)
+    return a.fwd.dv == 64 ? backward_typed<64, 64>(a, stream) : backward_typed<64, 128>(a, stream);
+  return a.fwd.dv == 64 ? backward_typed<128, 64>(a, stream) : backward_typed<128, 128>(a, stream);
+}
+
+}  // namespace ckda

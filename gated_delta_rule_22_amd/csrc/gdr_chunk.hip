@@ -370,23 +370,34 @@ template <typename F> hipError_t allow_lds(F *f, int bytes) {
                              hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
-template <int DK, int DV> hipError_t forward_typed(const GdrArgs &a, char *rec, hipStream_t st) {
+// prepare, then the chain; with STORE it keeps S and E and makes no output.
+template <int DK, int DV, bool STORE>
+hipError_t forward_typed(const GdrArgs &a, char *rec, char *S, char *E, hipStream_t st) {
   const auto *q = static_cast<const __hip_bfloat16 *>(a.q);
   const auto *k = static_cast<const __hip_bfloat16 *>(a.k);
   const auto *v = static_cast<const __hip_bfloat16 *>(a.v);
   if (a.n_chunks_ub > 0) {
-    hipLaunchKernelGGL((prepare_kernel<DK, false>),
+    hipLaunchKernelGGL((prepare_kernel<DK, STORE>),
                        dim3((unsigned)(a.n_chunks_ub * ((a.Hv + 3) / 4))), dim3(kThreads), 0, st,
                        q, k, a.g, a.beta, a.tab, a.N, a.Hk, a.Hv, rec);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }
-  constexpr int lds = chain_lds<DK, DV, false>();
-  if (hipError_t e = allow_lds(chain_kernel<DK, DV, false>, lds); e != hipSuccess) return e;
-  hipLaunchKernelGGL((chain_kernel<DK, DV, false>), dim3(chain_grid(a.N * a.Hv, DV / 64)),
+  constexpr int lds = chain_lds<DK, DV, STORE>();
+  if (hipError_t e = allow_lds(chain_kernel<DK, DV, STORE>, lds); e != hipSuccess) return e;
+  hipLaunchKernelGGL((chain_kernel<DK, DV, STORE>), dim3(chain_grid(a.N * a.Hv, DV / 64)),
                      dim3(kThreads), lds, st, q, k, v, a.S0, a.tab, a.N, a.Hk, a.Hv, rec,
-                     static_cast<__hip_bfloat16 *>(a.o), a.S_T, (char *)nullptr,
-                     (char *)nullptr);
+                     static_cast<__hip_bfloat16 *>(a.o), a.S_T, S, E);
   return hipGetLastError();
+}
+
+template <bool STORE>
+hipError_t forward_any(const GdrArgs &a, void *rec, void *S, void *E, hipStream_t st) {
+  char *r = static_cast<char *>(rec), *s = static_cast<char *>(S), *e = static_cast<char *>(E);
+  if (a.dk == 64)
+    return a.dv == 64 ? forward_typed<64, 64, STORE>(a, r, s, e, st)
+                      : forward_typed<64, 128, STORE>(a, r, s, e, st);
+  return a.dv == 64 ? forward_typed<128, 64, STORE>(a, r, s, e, st)
+                    : forward_typed<128, 128, STORE>(a, r, s, e, st);
 }
 
 }  // namespace
@@ -394,10 +405,10 @@ template <int DK, int DV> hipError_t forward_typed(const GdrArgs &a, char *rec, 
 size_t gdr_forward_rec_bytes() { return kRecFwd; }
 
 hipError_t launch_gdr_forward(const GdrArgs &a, void *rec, hipStream_t stream) {
-  char *r = static_cast<char *>(rec);
-  if (a.dk == 64)
-    return a.dv == 64 ? forward_typed<64, 64>(a, r, stream) : forward_typed<64, 128>(a, r, stream);
-  return a.dv == 64 ? forward_typed<128, 64>(a, r, stream) : forward_typed<128, 128>(a, r, stream);
+  return forward_any<false>(a, rec, nullptr, nullptr, stream);
+}
+hipError_t launch_gdr_keep(const GdrArgs &a, void *rec, void *S, void *E, hipStream_t stream) {
+  return forward_any<true>(a, rec, S, E, stream);
 }
 
 }  // namespace ckda

@@ -389,6 +389,35 @@ int gdr_forward(const void *q, const void *k, const void *v, const float *g, con
                 int dv, int N, int in_dtype, void *o, float *S_T, void *workspace,
                 size_t workspace_bytes, void *stream);
 
+/* Workspace of gdr_backward in bytes (0 if the sizes are invalid): for bf16
+ * inputs about 220 KB per (64-token chunk, value head) at dk = dv = 128. */
+size_t gdr_backward_workspace_bytes(int B, int T, int Hk, int Hv, int dk, int dv, int N,
+                                    int in_dtype);
+
+/*
+ * Backward of gdr_forward: the gradient of sum(d_o * o) + sum(dS_T * S_T).
+ *
+ *  q .. N, in_dtype    as for gdr_forward (recomputed; nothing of it is needed)
+ *  d_o         [B, T, Hv, dv]  in_dtype
+ *  dS_T        [N, Hv, dk, dv] fp32 or NULL for zero
+ *  dq, d_k     [B, T, Hk, dk]  in_dtype, summed over the value heads that share
+ *              the head
+ *  d_v         [B, T, Hv, dv]  in_dtype
+ *  dg, dbeta   [B, T, Hv]      fp32 (dg: of the log-gate; 0 where it is below
+ *              the floor, for bf16 inputs)
+ *  dS0         [N, Hv, dk, dv] fp32, or NULL to skip
+ *
+ * No output overlaps an input, another output or the workspace.  Numerics:
+ * bf16 inputs as the forward's states (fp32 accumulation, fp32 operands in two
+ * bf16 terms), also where only bf16 gradients depend on it; fp32 inputs run
+ * ckda_backward's fp64 path on expanded operands.
+ */
+int gdr_backward(const void *q, const void *k, const void *v, const float *g, const float *beta,
+                 const float *S0, const int32_t *cu_seqlens, int B, int T, int Hk, int Hv, int dk,
+                 int dv, int N, int in_dtype, const void *d_o, const float *dS_T, void *dq,
+                 void *d_k, void *d_v, float *dg, float *dbeta, float *dS0, void *workspace,
+                 size_t workspace_bytes, void *stream);
+
 /*
  * One token for N rows, on states that live in a pool.
  *

@@ -73,6 +73,36 @@ def test_forward_refusals(lib):
     assert st == ALIAS
 
 
+def _bwd(lib, B=2, T=64, Hk=2, Hv=4, dk=128, dv=128, N=None, dtype=0, ws=1 << 50, cu=False, **kw):
+    p = _addresses(["q", "k", "v", "g", "beta", "S0", "cu", "do", "dST", "dq", "dk", "dv", "dg",
+                    "dbeta", "dS0", "ws"], **kw)
+    return lib.gdr_backward(p["q"], p["k"], p["v"], p["g"], p["beta"], p["S0"],
+                            p["cu"] if cu else None, B, T, Hk, Hv, dk, dv, B if N is None else N,
+                            dtype, p["do"], p["dST"], p["dq"], p["dk"], p["dv"], p["dg"],
+                            p["dbeta"], p["dS0"], p["ws"], ws, None)
+
+
+def test_backward_refusals(lib):
+    for kw in (dict(dk=96), dict(dv=32), dict(Hk=0), dict(Hv=3), dict(B=0), dict(T=-1), dict(N=3),
+               dict(cu=True)):
+        assert _bwd(lib, **kw) == SHAPE, kw
+    assert _bwd(lib, dtype=2) == DTYPE
+    for n in ("q", "k", "v", "g", "beta", "do", "dq", "dk", "dv", "dg", "dbeta"):
+        assert _bwd(lib, null=(n,)) == NULL, n
+    for n in ("q", "do", "dST", "dq", "dk", "dv", "dS0", "ws"):
+        assert _bwd(lib, shift=((n, 8),)) == ALIGN, n
+    for n in ("g", "dg", "dbeta"):
+        assert _bwd(lib, shift=((n, 2),)) == ALIGN, n
+    for pair in (("dq", "q"), ("dk", "dq"), ("dv", "do"), ("dS0", "S0"), ("dS0", "dST"),
+                 ("ws", "do"), ("ws", "dg"), ("dbeta", "beta"), ("dg", "dbeta")):
+        assert _bwd(lib, alias=(pair,)) == ALIAS, pair
+    for dtype in (0, 1):
+        need = lib.gdr_backward_workspace_bytes(2, 64, 2, 4, 128, 128, 2, dtype)
+        assert need > 0 and _bwd(lib, ws=need - 1, dtype=dtype) == WORKSPACE
+    assert _bwd(lib, null=("ws",)) == WORKSPACE
+    assert lib.gdr_backward_workspace_bytes(2, 64, 3, 4, 128, 128, 2, 0) == 0
+
+
 def test_workspace_sizes(lib):
     f = lib.gdr_forward_workspace_bytes
     assert f(2, 64, 3, 4, 128, 128, 2, 0) == 0 and f(2, 64, 2, 4, 100, 128, 2, 0) == 0
