@@ -32,83 +32,167 @@ __device__ __forceinline__ bool chain_block(int nblk, int pairs, int &pair, int 
   return pair < pairs;
 }
 
-// The chain of dS, last chunk first; a wave owns 16 of the DV columns as in
-// the forward's chain, so dS -> dU -> F -> dS stays in its registers.
+// The chain of dS, last chunk first.  As in the forward's chain four waves own
+// 16 of the DV columns each, so dS -> dU -> F -> dS stays in their registers,
+// and four helper waves run beside them: they load, and one chunk ahead they
+// compute the chain's inputs that do not depend on dS, P^T dO and
+// Q^T (gam dO), which the chain takes from LDS as result tiles.
+// Barrier A: the chunk's operands and those tiles are in LDS; barrier B: the
+// chain has read all of them but K.
+template <int DK> struct ReverseLds {
+  static constexpr int kBufK = C * kStride<DK>, kTiles = (4 + DK / 16) * 1024;   // a wave's
+  static constexpr int kK = 0, kT = 2 * kBufK, kGate = kT + 2 * kTri;
+  static constexpr int kQ = kGate + kGateBytes, kD = kQ + C * kStride<DK>;
+  static constexpr int kP = kD + C * kStride<64>, kGam = kP + 2 * kTri;
+  static constexpr int kTile = kGam + C * 4, kBytes = kTile + 4 * kTiles;
+};
+
 template <int DK, int DV>
-__global__ __launch_bounds__(kThreads, 1) void reverse_kernel(
+__global__ __launch_bounds__(2 * kThreads, 2) void reverse_kernel(
     const __hip_bfloat16 *__restrict__ q, const __hip_bfloat16 *__restrict__ k,
     const __hip_bfloat16 *__restrict__ d_o, const float *__restrict__ dS_T, SeqTable tab, int N,
     int Hk, int Hv, const char *__restrict__ rec_base, char *__restrict__ dS_keep,
     char *__restrict__ F_keep, float *__restrict__ dS0) {
+  using L = ReverseLds<DK>;
   constexpr int KS = DK / 32, MT = DK / 16, BV = 64;
-  constexpr int kK = 0, kQ = kK + C * kStride<DK>, kD = kQ + C * kStride<DK>;
-  constexpr int kR = kD + C * kStride<BV>, kBuf = kR + kRecBwd;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   int pair, blk;
   if (!chain_block(DV / BV, N * Hv, pair, blk)) return;
   const int seq = tab.order[pair / Hv], hv = pair % Hv, hk = hv / (Hv / Hk);
-  const int t = threadIdx.x, wave = t >> 6, lane = t & 63, m = lane & 15, h = lane >> 4;
+  const int wave = (threadIdx.x >> 6) & 3, lane = threadIdx.x & 63, m = lane & 15, h = lane >> 4;
   const int len = tab.seq_len[seq], chunks = (len + C - 1) / C;
   const size_t row0 = tab.seq_start[seq];
   const size_t c0 = tab.chunk_off[seq];
   const int col = blk * BV + 16 * wave;
+  const float *gate = reinterpret_cast<const float *>(lds + L::kGate);
+  char *tiles = lds + L::kTile + wave * L::kTiles + lane * 16;
+
+  if (threadIdx.x >= kThreads) {         // helper waves
+    const int t = threadIdx.x - kThreads;
+    const char *Q = lds + L::kQ, *D = lds + L::kD, *P = lds + L::kP;
+    const float *s_gam = reinterpret_cast<const float *>(lds + L::kGam);
+    Stage<DK> gk, gq;
+    Stage<BV> gd;
+    Linear<2 * kTri> gt, gp;
+    Linear<kGateBytes> gg;
+    float gam = 0.f;
+    // The chain's operands of chunk c, and the helpers' own of the chunk before.
+    auto fetch_chain = [&](int c) {
+      const size_t row = row0 + (size_t)c * C;
+      const char *rec = rec_base + ((c0 + c) * Hv + hv) * kRecBwd;
+      gk.load(k + (row * Hk + hk) * DK, (size_t)Hk * DK, min(C, len - c * C), t);
+      gt.load(rec + kRecTh, t);
+      gg.load(rec + kRecGate, t);
+    };
+    auto put_chain = [&](int c) {
+      gk.store(lds + L::kK + (c & 1) * L::kBufK, t);
+      gt.store(lds + L::kT, t);
+      gg.store(lds + L::kGate, t);
+    };
+    auto fetch_own = [&](int c) {
+      const int valid = min(C, len - c * C);
+      const size_t row = row0 + (size_t)c * C;
+      const char *rec = rec_base + ((c0 + c) * Hv + hv) * kRecBwd;
+      gq.load(q + (row * Hk + hk) * DK, (size_t)Hk * DK, valid, t);
+      gd.load(d_o + (row * Hv + hv) * DV + blk * BV, (size_t)Hv * DV, valid, t);
+      // P hi and P lo: two matrices, not next to each other in the record
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        const int at = (t + i * kThreads) * 16;
+        gp.r[i] = load16(rec + (at < kTri ? kRecPh + at : kRecPl + at - kTri), true);
+      }
+      if (t < C) gam = reinterpret_cast<const float *>(rec + kRecGate)[kGam * C + t];
+    };
+    auto put_own = [&]() {
+      gq.store(lds + L::kQ, t);
+      gd.store(lds + L::kD, t);
+      gp.store(lds + L::kP, t);
+      if (t < C) reinterpret_cast<float *>(lds + L::kGam)[t] = gam;
+    };
+    f4 pd[4], qd[MT];
+    auto ahead = [&]() {
+      f4 d[4];                           // dO: lane = column, 4 tokens a tile
+      bf4 r[4];
+#pragma unroll
+      for (int it = 0; it < 4; ++it) r[it] = cols_quad<BV>(D, 16 * it, 16 * wave, lane);
+      const bf8 d0 = join(r[0], r[1]), d1 = join(r[2], r[3]);
+#pragma unroll
+      for (int jt = 0; jt < 4; ++jt) {
+        pd[jt] = 0.f;
+#pragma unroll
+        for (int ks = jt / 2; ks < 2; ++ks) {
+          const Split p = {tri_frag_t(P, jt, ks, lane), tri_frag_t(P + kTri, jt, ks, lane)};
+          pd[jt] = dot2(p, ks ? d1 : d0, pd[jt]);
+        }
+        d[jt] = widen4(r[jt]) * *reinterpret_cast<const f4 *>(s_gam + 16 * jt + 4 * h);
+      }
+      const Split e0 = split8(d[0], d[1]), e1 = split8(d[2], d[3]);
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+        qd[i] = dot2(cols_frag<DK>(Q, 32, 16 * i, lane), e1,
+                     dot2(cols_frag<DK>(Q, 0, 16 * i, lane), e0, f4(0.f)));
+    };
+    auto put_tiles = [&]() {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) *reinterpret_cast<f4 *>(tiles + i * 1024) = pd[i];
+#pragma unroll
+      for (int i = 0; i < MT; ++i) *reinterpret_cast<f4 *>(tiles + (4 + i) * 1024) = qd[i];
+    };
+    const int last = chunks - 1;
+    if (chunks > 0) {
+      fetch_own(last);
+      fetch_chain(last);
+      put_own();
+      put_chain(last);
+    }
+    lds_barrier();                       // the helpers' operands of the last chunk
+    if (chunks > 0) {
+      if (last > 0) fetch_own(last - 1);
+      ahead();
+      put_tiles();
+    }
+    lds_barrier();                       // all helpers have read them
+    if (last > 0) put_own();
+    for (int c = last; c >= 0; --c) {
+      lds_barrier();                     // A
+      if (c > 0) {
+        fetch_chain(c - 1);
+        if (c > 1) fetch_own(c - 2);
+        ahead();
+      }
+      lds_barrier();                     // B
+      if (c > 0) {
+        put_tiles();
+        put_chain(c - 1);
+        if (c > 1) put_own();
+      }
+    }
+    return;
+  }
 
   f4 S[MT];                              // dS
   const size_t sbase = ((size_t)seq * Hv + hv) * DK * DV + col + m;
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
+  for (int i = 0; i < MT; ++i) S[i] = 0.f;
+  if (dS_T)
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-      S[i][r] = dS_T ? dS_T[sbase + (size_t)(16 * i + 4 * h + r) * DV] : 0.f;
-
-  Stage<DK> gk, gq;
-  Stage<BV> gd;
-  Linear<kRecBwd> gr;
-  auto fetch = [&](int c) {
-    const int valid = min(C, len - c * C);
-    const size_t row = row0 + (size_t)c * C;
-    gk.load(k + (row * Hk + hk) * DK, (size_t)Hk * DK, valid, t);
-    gq.load(q + (row * Hk + hk) * DK, (size_t)Hk * DK, valid, t);
-    gd.load(d_o + (row * Hv + hv) * DV + blk * BV, (size_t)Hv * DV, valid, t);
-    gr.load(rec_base + ((c0 + c) * Hv + hv) * kRecBwd, t);
-  };
-  auto put = [&](char *buf) {
-    gk.store(buf + kK, t);
-    gq.store(buf + kQ, t);
-    gd.store(buf + kD, t);
-    gr.store(buf + kR, t);
-  };
-  if (chunks > 0) {
-    fetch(chunks - 1);
-    put(lds + ((chunks - 1) & 1) * kBuf);
-  }
-  __syncthreads();
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) S[i][r] = dS_T[sbase + (size_t)(16 * i + 4 * h + r) * DV];
+  lds_barrier();                         // the helpers' two, before the loop
+  lds_barrier();
   for (int c = chunks - 1; c >= 0; --c) {
-    const char *buf = lds + (c & 1) * kBuf;
-    const char *K = buf + kK, *Q = buf + kQ, *D = buf + kD, *R = buf + kR;
-    const float *gate = reinterpret_cast<const float *>(R + kRecGate);
-    if (c > 0) fetch(c - 1);
-
+    const char *K = lds + L::kK + (c & 1) * L::kBufK, *T = lds + L::kT;
     Split sf[KS];
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) sf[ks] = split8(S[2 * ks], S[2 * ks + 1]);
-    {
-      char *p = dS_keep + (((c0 + c) * Hv + hv) * (2 * MT * (DV / 16)) + col / 16) * 512 + lane * 8;
+    lds_barrier();                       // A
+    char *p = dS_keep + (((c0 + c) * Hv + hv) * (2 * KS * (DV / 16)) + col / 16) * kFrag + lane * 16;
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        const bf8 hi = sf[i / 2].hi, lo = sf[i / 2].lo;
-        *reinterpret_cast<bf4 *>(p + i * (DV / 16) * 512) =
-            i % 2 ? __builtin_shufflevector(hi, hi, 4, 5, 6, 7)
-                  : __builtin_shufflevector(hi, hi, 0, 1, 2, 3);
-        *reinterpret_cast<bf4 *>(p + (MT + i) * (DV / 16) * 512) =
-            i % 2 ? __builtin_shufflevector(lo, lo, 4, 5, 6, 7)
-                  : __builtin_shufflevector(lo, lo, 0, 1, 2, 3);
-      }
+    for (int ks = 0; ks < KS; ++ks) {
+      *reinterpret_cast<bf8 *>(p + ks * (DV / 16) * kFrag) = sf[ks].hi;
+      *reinterpret_cast<bf8 *>(p + (KS + ks) * (DV / 16) * kFrag) = sf[ks].lo;
     }
-    f4 d[4];                             // dO: lane = column, 4 tokens a tile
-#pragma unroll
-    for (int it = 0; it < 4; ++it) d[it] = widen4(cols_quad<BV>(D, 16 * it, 16 * wave, lane));
-    const bf8 d0 = join(round4(d[0]), round4(d[1])), d1 = join(round4(d[2]), round4(d[3]));
     f4 X[4];                             // beta dU
 #pragma unroll
     for (int jt = 0; jt < 4; ++jt) {
@@ -116,46 +200,41 @@ __global__ __launch_bounds__(kThreads, 1) void reverse_kernel(
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks)
         y = dot2(rows_frag<DK>(K, 16 * jt, 32 * ks, lane), sf[ks], y);
-      y *= *reinterpret_cast<const f4 *>(gate + kLast * C + 16 * jt + 4 * h);
-#pragma unroll
-      for (int ks = jt / 2; ks < 2; ++ks) {
-        const Split P = {tri_frag_t(R + kRecPh, jt, ks, lane), tri_frag_t(R + kRecPl, jt, ks, lane)};
-        y = dot2(P, ks ? d1 : d0, y);
-      }
+      y = y * *reinterpret_cast<const f4 *>(gate + kLast * C + 16 * jt + 4 * h) +
+          *reinterpret_cast<const f4 *>(tiles + jt * 1024);
       X[jt] = y * *reinterpret_cast<const f4 *>(gate + kBeta * C + 16 * jt + 4 * h);
     }
     const Split x0 = split8(X[0], X[1]), x1 = split8(X[2], X[3]);
-    f4 F[4];
-    char *p = F_keep + (((c0 + c) * Hv + hv) * (8 * (DV / 16)) + col / 16) * 512 + lane * 8;
+    const float gn = gate[kGam * C + C - 1];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+      S[i] = S[i] * gn + *reinterpret_cast<const f4 *>(tiles + (4 + i) * 1024);
+    f4 F[4], gam[4];
 #pragma unroll
     for (int jt = 0; jt < 4; ++jt) {
       F[jt] = 0.f;
 #pragma unroll
       for (int ks = jt / 2; ks < 2; ++ks) {
-        const Split T = {tri_frag_t(R + kRecTh, jt, ks, lane), tri_frag_t(R + kRecTl, jt, ks, lane)};
-        F[jt] = dot3(T, ks ? x1 : x0, F[jt]);
+        const Split t = {tri_frag_t(T, jt, ks, lane), tri_frag_t(T + kTri, jt, ks, lane)};
+        F[jt] = dot3(t, ks ? x1 : x0, F[jt]);
       }
-      bf4 x, y;
-      split4(F[jt], x, y);
-      *reinterpret_cast<bf4 *>(p + jt * (DV / 16) * 512) = x;
-      *reinterpret_cast<bf4 *>(p + (4 + jt) * (DV / 16) * 512) = y;
-      const f4 gam = *reinterpret_cast<const f4 *>(gate + kGam * C + 16 * jt + 4 * h);
-      F[jt] *= -gam;
-      d[jt] *= gam;
+      gam[jt] = *reinterpret_cast<const f4 *>(gate + kGam * C + 16 * jt + 4 * h);
     }
+    lds_barrier();                       // B
+    p = F_keep + (((c0 + c) * Hv + hv) * (4 * (DV / 16)) + col / 16) * kFrag + lane * 16;
     const Split f0 = split8(F[0], F[1]), f1 = split8(F[2], F[3]);
-    const Split e0 = split8(d[0], d[1]), e1 = split8(d[2], d[3]);
-    const float gn = gate[kGam * C + C - 1];
+    *reinterpret_cast<bf8 *>(p) = f0.hi;
+    *reinterpret_cast<bf8 *>(p + (DV / 16) * kFrag) = f1.hi;
+    *reinterpret_cast<bf8 *>(p + 2 * (DV / 16) * kFrag) = f0.lo;
+    *reinterpret_cast<bf8 *>(p + 3 * (DV / 16) * kFrag) = f1.lo;
+#pragma unroll
+    for (int jt = 0; jt < 4; ++jt) F[jt] *= -gam[jt];
+    const Split w0 = split8(F[0], F[1]), w1 = split8(F[2], F[3]);
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-      S[i] *= gn;
-      S[i] = dot2(cols_frag<DK>(Q, 0, 16 * i, lane), e0, S[i]);
-      S[i] = dot2(cols_frag<DK>(Q, 32, 16 * i, lane), e1, S[i]);
-      S[i] = dot2(cols_frag<DK>(K, 0, 16 * i, lane), f0, S[i]);
-      S[i] = dot2(cols_frag<DK>(K, 32, 16 * i, lane), f1, S[i]);
+      S[i] = dot2(cols_frag<DK>(K, 0, 16 * i, lane), w0, S[i]);
+      S[i] = dot2(cols_frag<DK>(K, 32, 16 * i, lane), w1, S[i]);
     }
-    if (c > 0) put(lds + ((c - 1) & 1) * kBuf);
-    __syncthreads();
   }
   if (dS0)
 #pragma unroll
@@ -243,9 +322,11 @@ __global__ __launch_bounds__(kThreads, 1) void grad_kernel(
     __syncthreads();
     const char *D = lds + L::kD;
     auto tile_split = [&](const char *base, int row, int rows, int ks) {
-      const char *a = base + (row * NT + 2 * ks) * 512, *b = a + rows * NT * 512;
-      return Split{join(tile_quad_t(a, lane), tile_quad_t(a + 512, lane)),
-                   join(tile_quad_t(b, lane), tile_quad_t(b + 512, lane))};
+      const char *a = base + ((row >> 1) * NT + 2 * ks) * kFrag;
+      const char *b = a + (rows / 2) * NT * kFrag;
+      const int half = row & 1;
+      return Split{join(pair_quad_t(a, half, lane), pair_quad_t(a + kFrag, half, lane)),
+                   join(pair_quad_t(b, half, lane), pair_quad_t(b + kFrag, half, lane))};
     };
     auto Ef = [&](int tile, int ks) { return tile_split(lds + L::kE, tile, 4, ks); };
     auto Ff = [&](int tile, int ks) { return tile_split(lds + L::kF, tile, 4, ks); };
@@ -387,11 +468,9 @@ __global__ __launch_bounds__(kThreads, 1) void grad_kernel(
 #pragma unroll
       for (int i = 0; i < kHalf; ++i) {
         const char *p = lds + L::kX + (t + i * kThreads) * 16;
-        const uint4 a = *reinterpret_cast<const uint4 *>(p);
-        const uint4 b = *reinterpret_cast<const uint4 *>(p + kPlane);
-        const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
-        const uint4 c = s.r[i], e2 = s.r[i + kHalf];
-        const uint32_t z[4] = {c.x, c.y, c.z, c.w}, v[4] = {e2.x, e2.y, e2.z, e2.w};
+        const u4 x = *reinterpret_cast<const u4 *>(p);
+        const u4 y = *reinterpret_cast<const u4 *>(p + kPlane);
+        const u4 z = s.r[i], v = s.r[i + kHalf];
         auto low = [](uint32_t a) { return __uint_as_float(a << 16); };
         auto high = [](uint32_t a) { return __uint_as_float(a & 0xFFFF0000u); };
 #pragma unroll
@@ -457,13 +536,13 @@ template <int DK, int DV> hipError_t backward_typed(const GdrBwdArgs &a, hipStre
   char *E = static_cast<char *>(a.E), *dS = static_cast<char *>(a.dS);
   char *F = static_cast<char *>(a.F);
   if (hipError_t e = launch_gdr_keep(f, rec, S, E, st); e != hipSuccess) return e;
-  constexpr int lds = 2 * (2 * C * kStride<DK> + C * kStride<64> + kRecBwd);
+  constexpr int lds = ReverseLds<DK>::kBytes;
   auto *rev = reverse_kernel<DK, DV>;
   hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(rev),
                                      hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   if (e != hipSuccess) return e;
   const unsigned pairs = (unsigned)((f.N * f.Hv + 7) / 8 * 8);
-  hipLaunchKernelGGL(rev, dim3(pairs * (DV / 64)), dim3(kThreads), lds, st, q, k, d_o, a.dS_T,
+  hipLaunchKernelGGL(rev, dim3(pairs * (DV / 64)), dim3(2 * kThreads), lds, st, q, k, d_o, a.dS_T,
                      f.tab, f.N, f.Hk, f.Hv, rec, dS, F, a.dS0);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   if (f.n_chunks_ub == 0) return hipSuccess;

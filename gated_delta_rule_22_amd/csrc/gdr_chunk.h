@@ -28,6 +28,7 @@ typedef __bf16 bf4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
 typedef float f4 __attribute__((ext_vector_type(4)));
 typedef short s4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));   // 16 bytes on their way
 typedef __attribute__((address_space(3))) s4 lds_s4;
 typedef __attribute__((address_space(3))) char lds_char;
 
@@ -91,9 +92,10 @@ __device__ __forceinline__ f4 dot3(const Split &a, const Split &b, f4 c) {
   return mfma(a.lo, b.hi, mfma(a.hi, b.lo, mfma(a.hi, b.hi, c)));
 }
 
-// ---- LDS operand reads.  Row-major tiles have rows of COLS bf16 and 16 bytes
-// of padding (4 banks a row, so a column of rows spreads over the banks).
-template <int COLS> constexpr int kStride = COLS * 2 + 16;
+// ---- LDS operand reads.  Row-major tiles have rows of COLS bf16 and 32 bytes
+// of padding: the 16 rows x 32 bytes that one read covers then fall on each of
+// the 64 banks exactly twice (16 bytes of padding: 1.5 times the LDS cycles).
+template <int COLS> constexpr int kStride = COLS * 2 + 32;
 
 // Operand whose lanes are rows: lane (m, h) gets row r0 + m, the 8 columns of
 // quarter h of the 32 from c0.
@@ -136,53 +138,64 @@ __device__ __forceinline__ bf8 tri_frag_t(const char *mat, int jt, int ks, int l
   // and is stored as zeros.
   return join(tri_quad_t(mat, 2 * ks, jt, lane), tri_quad_t(mat, 2 * ks + 1, jt, lane));
 }
-// Tile order, used for states and E, F in the workspace: a 16 x 16 result tile
-// as its 64 lanes x 4 values (8 bytes a lane).  Transposed read: lane i gets
-// the 4 columns 4h .. of row i of the tile (a result's lane is its column).
-__device__ __forceinline__ bf4 tile_quad_t(const char *tile, int lane) {
+// Pair order, used for states and E, F in the workspace: two 16 x 16 result
+// tiles, one above the other, as their 64 lanes x 8 values (16 bytes a lane),
+// which is the operand they make.  Transposed read of tile `half`: lane i gets
+// the 4 columns 4h .. of row i (a result's lane is its column).
+__device__ __forceinline__ bf4 pair_quad_t(const char *pair, int half, int lane) {
   const int s = lane & 15, h = lane >> 4;
-  return read_tr(tile + ((s & 3) * 16 + 4 * h + (s >> 2)) * 8);
+  return read_tr(pair + ((s & 3) * 16 + 4 * h + (s >> 2)) * 16 + half * 8);
+}
+
+__device__ __forceinline__ u4 load16(const void *p, bool there) {
+  u4 r = 0u;
+  if (there) r = *static_cast<const u4 *>(p);
+  return r;
 }
 
 // ---- staging of a row-major [64][COLS] bf16 tile: global -> registers -> LDS
 template <int COLS> struct Stage {
   static constexpr int kLanes = COLS / 8, kRows = kThreads / kLanes, kPasses = C / kRows;
-  uint4 r[kPasses];
+  u4 r[kPasses];
   __device__ __forceinline__ void load(const __hip_bfloat16 *p, size_t ld, int valid, int t) {
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
       const int row = t / kLanes + i * kRows;
-      r[i] = row < valid ? *reinterpret_cast<const uint4 *>(p + row * ld + (t % kLanes) * 8)
-                         : make_uint4(0, 0, 0, 0);
+      r[i] = load16(p + row * ld + (t % kLanes) * 8, row < valid);
     }
   }
   __device__ __forceinline__ void store(char *tile, int t) const {
 #pragma unroll
     for (int i = 0; i < kPasses; ++i)
-      *reinterpret_cast<uint4 *>(tile + (t / kLanes + i * kRows) * kStride<COLS> +
+      *reinterpret_cast<u4 *>(tile + (t / kLanes + i * kRows) * kStride<COLS> +
                                  (t % kLanes) * 16) = r[i];
   }
 };
 // Linear bytes: global -> registers -> LDS.
 template <int BYTES> struct Linear {
   static constexpr int kPasses = (BYTES + kThreads * 16 - 1) / (kThreads * 16);
-  uint4 r[kPasses];
+  u4 r[kPasses];
   __device__ __forceinline__ void load(const char *p, int t) {
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
       const int at = (t + i * kThreads) * 16;
-      r[i] = BYTES % (kThreads * 16) == 0 || at < BYTES ? *reinterpret_cast<const uint4 *>(p + at)
-                                                       : make_uint4(0, 0, 0, 0);
+      r[i] = load16(p + at, BYTES % (kThreads * 16) == 0 || at < BYTES);
     }
   }
   __device__ __forceinline__ void store(char *dst, int t) const {
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
       const int at = (t + i * kThreads) * 16;
-      if (BYTES % (kThreads * 16) == 0 || at < BYTES) *reinterpret_cast<uint4 *>(dst + at) = r[i];
+      if (BYTES % (kThreads * 16) == 0 || at < BYTES) *reinterpret_cast<u4 *>(dst + at) = r[i];
     }
   }
 };
+
+// Workgroup barrier that waits for this wave's LDS operations only: loads from
+// and stores to global memory stay in flight across it.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
 
 // Orders this wave's LDS writes before its later reads (the hardware runs a
 // wave's LDS operations in order; this keeps the compiler to it).

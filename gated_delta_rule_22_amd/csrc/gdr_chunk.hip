@@ -90,11 +90,8 @@ __global__ __launch_bounds__(kThreads) void prepare_kernel(
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       const int r = 16 * it + m;
-      const uint4 z = make_uint4(0, 0, 0, 0);
       kf[it][ks] = __builtin_bit_cast(
-          bf8, r < valid ? *reinterpret_cast<const uint4 *>(k + ((row0 + r) * Hk + hk) * DK +
-                                                            32 * ks + 8 * h)
-                         : z);
+          bf8, load16(k + ((row0 + r) * Hk + hk) * DK + 32 * ks + 8 * h, r < valid));
     }
   wave_sync();
 
@@ -126,11 +123,8 @@ __global__ __launch_bounds__(kThreads) void prepare_kernel(
     const int i = 16 * it + m;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
-      const uint4 z = make_uint4(0, 0, 0, 0);
       qf[ks] = __builtin_bit_cast(
-          bf8, i < valid ? *reinterpret_cast<const uint4 *>(q + ((row0 + i) * Hk + hk) * DK +
-                                                            32 * ks + 8 * h)
-                         : z);
+          bf8, load16(q + ((row0 + i) * Hk + hk) * DK + 32 * ks + 8 * h, i < valid));
     }
     const float hi_i = s_hi[i], lo_i = s_lo[i];
 #pragma unroll
@@ -198,87 +192,150 @@ __device__ __forceinline__ bool chain_block(int nblk, int pairs, int &pair, int 
 }
 
 // -------------------------------------------------------------------- chain
-// A workgroup of 4 waves runs 64 of the state's DV columns of one (sequence,
-// head) over its chunks; a wave owns 16 columns for the whole sequence, so the
-// chain S -> K S -> E -> S of a column never leaves its wave: S is 4 DK / 16
-// accumulator registers, and each product's result tiles are the next one's
-// operand.  Waves only share the staged operands: one barrier a chunk, with
-// the next chunk's loads in flight meanwhile.
+// A workgroup runs 64 of the state's DV columns of one (sequence, head) over
+// its chunks.  Four chain waves own 16 columns each for the whole sequence, so
+// the chain S -> K S -> E -> S of a column never leaves its wave: S is 4 DK /
+// 16 accumulator registers, and each product's result tiles are the next one's
+// operand.  Four helper waves (one more on each SIMD) do what the chain does
+// not wait for: they load the next chunk and make the output of this one.
+// Two barriers a chunk, A when the chunk's operands and S's terms are in LDS,
+// B when the chain has read all of them but K and has written U; what the next
+// chunk overwrites between B and the next A is only K's other buffer and those.
 // STORE: for the backward, keeps the state before each chunk and E (two bf16
 // terms each) and makes no output.
+template <int DK, int DV, bool STORE> struct ChainLds {
+  static constexpr int kBufK = C * kStride<DK>;
+  static constexpr int kK = 0, kV = 2 * kBufK, kRec = kV + C * kStride<64>;
+  static constexpr int kQ = kRec + kRecFwd;                      // the rest: !STORE
+  static constexpr int kS = kQ + C * kStride<DK>, kSWave = 2 * (DK / 32) * kFrag;
+  static constexpr int kU = kS + 4 * kSWave;
+  static constexpr int kBytes = STORE ? kQ : kU + 4 * 2 * kFrag;
+};
+
 template <int DK, int DV, bool STORE>
-__global__ __launch_bounds__(kThreads, 1) void chain_kernel(
+__global__ __launch_bounds__(2 * kThreads, 2) void chain_kernel(
     const __hip_bfloat16 *__restrict__ q, const __hip_bfloat16 *__restrict__ k,
     const __hip_bfloat16 *__restrict__ v, const float *__restrict__ S0, SeqTable tab, int N,
     int Hk, int Hv, const char *__restrict__ rec_base, __hip_bfloat16 *__restrict__ o,
     float *__restrict__ S_T, char *__restrict__ S_keep, char *__restrict__ E_keep) {
+  using L = ChainLds<DK, DV, STORE>;
   constexpr int KS = DK / 32, MT = DK / 16, BV = 64;
   constexpr int kRec = STORE ? kRecBwd : kRecFwd;
-  constexpr int kK = 0, kQ = kK + C * kStride<DK>, kV = kQ + (STORE ? 0 : C * kStride<DK>);
-  constexpr int kR = kV + C * kStride<BV>, kBuf = kR + kRecFwd;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   int pair, blk;
   if (!chain_block(DV / BV, N * Hv, pair, blk)) return;
   const int seq = tab.order[pair / Hv], hv = pair % Hv, hk = hv / (Hv / Hk);
-  const int t = threadIdx.x, wave = t >> 6, lane = t & 63, m = lane & 15, h = lane >> 4;
+  const int wave = (threadIdx.x >> 6) & 3, lane = threadIdx.x & 63, m = lane & 15, h = lane >> 4;
   const int len = tab.seq_len[seq], chunks = (len + C - 1) / C;
   const size_t row0 = tab.seq_start[seq];
   const size_t c0 = tab.chunk_off[seq];
   const int col = blk * BV + 16 * wave;  // of the head's DV
+  const char *V = lds + L::kV, *R = lds + L::kRec, *Q = lds + L::kQ;
+  const float *gate = reinterpret_cast<const float *>(R + kRecGate);
+  char *s_S = lds + L::kS + wave * L::kSWave + lane * 16;
+  char *s_U = lds + L::kU + wave * 2 * kFrag + lane * 16;
+
+  if (threadIdx.x >= kThreads) {         // helper waves
+    const int t = threadIdx.x - kThreads;
+    Stage<DK> gk, gq;
+    Stage<BV> gv;
+    Linear<kRecFwd> gr;
+    auto fetch = [&](int c) {
+      const int valid = min(C, len - c * C);
+      const size_t row = row0 + (size_t)c * C;
+      gk.load(k + (row * Hk + hk) * DK, (size_t)Hk * DK, valid, t);
+      if (!STORE) gq.load(q + (row * Hk + hk) * DK, (size_t)Hk * DK, valid, t);
+      gv.load(v + (row * Hv + hv) * DV + blk * BV, (size_t)Hv * DV, valid, t);
+      gr.load(rec_base + ((c0 + c) * Hv + hv) * kRec, t);
+    };
+    auto put = [&](int c) {
+      gk.store(lds + L::kK + (c & 1) * L::kBufK, t);
+      if (!STORE) gq.store(lds + L::kQ, t);
+      gv.store(lds + L::kV, t);
+      gr.store(lds + L::kRec, t);
+    };
+    if (chunks > 0) {
+      fetch(0);
+      put(0);
+    }
+    for (int c = 0; c < chunks; ++c) {
+      lds_barrier();                     // A
+      if (c + 1 < chunks) fetch(c + 1);
+      f4 a[4];
+      bf8 p[6];
+      if (!STORE) {
+        // O, transposed: lane = token, 4 columns a lane.
+#pragma unroll
+        for (int it = 0; it < 4; ++it) a[it] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          const Split s = {*reinterpret_cast<const bf8 *>(s_S + ks * kFrag),
+                           *reinterpret_cast<const bf8 *>(s_S + (KS + ks) * kFrag)};
+#pragma unroll
+          for (int it = 0; it < 4; ++it)
+            a[it] = dot2(s, rows_frag<DK>(Q, 16 * it, 32 * ks, lane), a[it]);
+        }
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+          a[it] *= gate[kGam * C + 16 * it + m];
+#pragma unroll
+          for (int ks = 0; ks <= it / 2; ++ks)
+            p[frag_at(it, ks) / kFrag] = tri_frag(R + kRecPh, it, ks, lane);
+        }
+      }
+      lds_barrier();                     // B
+      if (!STORE) {
+        // One term of P and of U: each is within 2^-9 of its value, and so is
+        // the bf16 output itself.
+        const bf8 u0 = *reinterpret_cast<const bf8 *>(s_U);
+        const bf8 u1 = *reinterpret_cast<const bf8 *>(s_U + kFrag);
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+#pragma unroll
+          for (int ks = 0; ks <= it / 2; ++ks)
+            a[it] = mfma(ks ? u1 : u0, p[frag_at(it, ks) / kFrag], a[it]);
+          const int tok = c * C + 16 * it + m;
+          if (tok < len)
+            *reinterpret_cast<bf4 *>(o + ((row0 + tok) * Hv + hv) * DV + col + 4 * h) =
+                round4(a[it]);
+        }
+      }
+      if (c + 1 < chunks) put(c + 1);
+    }
+    return;
+  }
 
   f4 S[MT];
   const size_t sbase = ((size_t)seq * Hv + hv) * DK * DV + col + m;
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
+  for (int i = 0; i < MT; ++i) S[i] = 0.f;
+  if (S0)
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-      S[i][r] = S0 ? S0[sbase + (size_t)(16 * i + 4 * h + r) * DV] : 0.f;
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) S[i][r] = S0[sbase + (size_t)(16 * i + 4 * h + r) * DV];
 
-  Stage<DK> gk, gq;
-  Stage<BV> gv;
-  Linear<kRecFwd> gr;
-  auto fetch = [&](int c) {
-    const int valid = min(C, len - c * C);
-    const size_t row = row0 + (size_t)c * C;
-    gk.load(k + (row * Hk + hk) * DK, (size_t)Hk * DK, valid, t);
-    if (!STORE) gq.load(q + (row * Hk + hk) * DK, (size_t)Hk * DK, valid, t);
-    gv.load(v + (row * Hv + hv) * DV + blk * BV, (size_t)Hv * DV, valid, t);
-    gr.load(rec_base + ((c0 + c) * Hv + hv) * kRec, t);
-  };
-  auto put = [&](char *buf) {
-    gk.store(buf + kK, t);
-    if (!STORE) gq.store(buf + kQ, t);
-    gv.store(buf + kV, t);
-    gr.store(buf + kR, t);
-  };
-  if (chunks > 0) {
-    fetch(0);
-    put(lds);
-  }
-  __syncthreads();
   for (int c = 0; c < chunks; ++c) {
-    const char *buf = lds + (c & 1) * kBuf;
-    const char *K = buf + kK, *Q = buf + kQ, *V = buf + kV, *R = buf + kR;
-    const float *gate = reinterpret_cast<const float *>(R + kRecGate);
-    if (c + 1 < chunks) fetch(c + 1);
-
+    const char *K = lds + L::kK + (c & 1) * L::kBufK;
     Split sf[KS];
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) sf[ks] = split8(S[2 * ks], S[2 * ks + 1]);
-    if (STORE) {
-      char *p = S_keep + (((c0 + c) * Hv + hv) * (2 * MT * (DV / 16)) + col / 16) * 512 + lane * 8;
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        const bf8 hi = sf[i / 2].hi, lo = sf[i / 2].lo;
-        const bf4 x = i % 2 ? __builtin_shufflevector(hi, hi, 4, 5, 6, 7)
-                            : __builtin_shufflevector(hi, hi, 0, 1, 2, 3);
-        const bf4 y = i % 2 ? __builtin_shufflevector(lo, lo, 4, 5, 6, 7)
-                            : __builtin_shufflevector(lo, lo, 0, 1, 2, 3);
-        *reinterpret_cast<bf4 *>(p + i * (DV / 16) * 512) = x;
-        *reinterpret_cast<bf4 *>(p + (MT + i) * (DV / 16) * 512) = y;
+    for (int ks = 0; ks < KS; ++ks) {
+      sf[ks] = split8(S[2 * ks], S[2 * ks + 1]);
+      if (!STORE) {
+        *reinterpret_cast<bf8 *>(s_S + ks * kFrag) = sf[ks].hi;
+        *reinterpret_cast<bf8 *>(s_S + (KS + ks) * kFrag) = sf[ks].lo;
       }
     }
-
+    lds_barrier();                       // A
+    if (STORE) {
+      char *p = S_keep + (((c0 + c) * Hv + hv) * (2 * KS * (DV / 16)) + col / 16) * kFrag +
+                lane * 16;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        *reinterpret_cast<bf8 *>(p + ks * (DV / 16) * kFrag) = sf[ks].hi;
+        *reinterpret_cast<bf8 *>(p + (KS + ks) * (DV / 16) * kFrag) = sf[ks].lo;
+      }
+    }
     // X = V - gam K S, as the operand of T' X
     f4 X[4];
 #pragma unroll
@@ -301,55 +358,33 @@ __global__ __launch_bounds__(kThreads, 1) void chain_kernel(
         E[it] = dot3(T, ks ? x1 : x0, E[it]);
       }
     }
-    if (STORE) {
-      char *p = E_keep + (((c0 + c) * Hv + hv) * (8 * (DV / 16)) + col / 16) * 512 + lane * 8;
-#pragma unroll
-      for (int it = 0; it < 4; ++it) {
-        bf4 x, y;
-        split4(E[it], x, y);
-        *reinterpret_cast<bf4 *>(p + it * (DV / 16) * 512) = x;
-        *reinterpret_cast<bf4 *>(p + (4 + it) * (DV / 16) * 512) = y;
-      }
-    }
     f4 W[4];                             // gam_n / gam U
 #pragma unroll
     for (int it = 0; it < 4; ++it)
       W[it] = E[it] * *reinterpret_cast<const f4 *>(gate + kLastBeta * C + 16 * it + 4 * h);
-    const Split w0 = split8(W[0], W[1]), w1 = split8(W[2], W[3]);
     const float gn = gate[kGam * C + C - 1];
+    if (STORE) {
+      char *p = E_keep + (((c0 + c) * Hv + hv) * (4 * (DV / 16)) + col / 16) * kFrag + lane * 16;
+      const Split e0 = split8(E[0], E[1]), e1 = split8(E[2], E[3]);
+      *reinterpret_cast<bf8 *>(p) = e0.hi;
+      *reinterpret_cast<bf8 *>(p + (DV / 16) * kFrag) = e1.hi;
+      *reinterpret_cast<bf8 *>(p + 2 * (DV / 16) * kFrag) = e0.lo;
+      *reinterpret_cast<bf8 *>(p + 3 * (DV / 16) * kFrag) = e1.lo;
+    } else {
+#pragma unroll
+      for (int it = 0; it < 4; ++it)
+        E[it] *= *reinterpret_cast<const f4 *>(gate + kBeta * C + 16 * it + 4 * h);
+      *reinterpret_cast<bf8 *>(s_U) = join(round4(E[0]), round4(E[1]));
+      *reinterpret_cast<bf8 *>(s_U + kFrag) = join(round4(E[2]), round4(E[3]));
+    }
+    lds_barrier();                       // B
+    const Split w0 = split8(W[0], W[1]), w1 = split8(W[2], W[3]);
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
       S[i] *= gn;
       S[i] = dot2(cols_frag<DK>(K, 0, 16 * i, lane), w0, S[i]);
       S[i] = dot2(cols_frag<DK>(K, 32, 16 * i, lane), w1, S[i]);
     }
-
-    if (!STORE) {
-      // O, transposed: lane = token, 4 columns a lane.  One term of S, P and U
-      // is enough here: each is within 2^-9 of its value, and so is the bf16
-      // output itself.
-      f4 U[4];
-#pragma unroll
-      for (int it = 0; it < 4; ++it)
-        U[it] = E[it] * *reinterpret_cast<const f4 *>(gate + kBeta * C + 16 * it + 4 * h);
-      const bf8 u0 = join(round4(U[0]), round4(U[1])), u1 = join(round4(U[2]), round4(U[3]));
-#pragma unroll
-      for (int it = 0; it < 4; ++it) {
-        f4 a = 0.f;
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
-          a = mfma(sf[ks].hi, rows_frag<DK>(Q, 16 * it, 32 * ks, lane), a);
-        a *= gate[kGam * C + 16 * it + m];
-#pragma unroll
-        for (int ks = 0; ks <= it / 2; ++ks)
-          a = mfma(ks ? u1 : u0, tri_frag(R + kRecPh, it, ks, lane), a);
-        const int tok = c * C + 16 * it + m;
-        if (tok < len)
-          *reinterpret_cast<bf4 *>(o + ((row0 + tok) * Hv + hv) * DV + col + 4 * h) = round4(a);
-      }
-    }
-    if (c + 1 < chunks) put(lds + ((c + 1) & 1) * kBuf);
-    __syncthreads();
   }
   if (S_T)
 #pragma unroll
@@ -357,10 +392,6 @@ __global__ __launch_bounds__(kThreads, 1) void chain_kernel(
 #pragma unroll
       for (int r = 0; r < 4; ++r)
         S_T[sbase + (size_t)(16 * i + 4 * h + r) * DV] = S[i][r];
-}
-
-template <int DK, int DV, bool STORE> constexpr int chain_lds() {
-  return 2 * (C * kStride<DK> * (STORE ? 1 : 2) + C * kStride<64> + kRecFwd);
 }
 
 unsigned chain_grid(int pairs, int nblk) { return (unsigned)((pairs + 7) / 8 * 8) * nblk; }
@@ -382,10 +413,10 @@ hipError_t forward_typed(const GdrArgs &a, char *rec, char *S, char *E, hipStrea
                        q, k, a.g, a.beta, a.tab, a.N, a.Hk, a.Hv, rec);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }
-  constexpr int lds = chain_lds<DK, DV, STORE>();
+  constexpr int lds = ChainLds<DK, DV, STORE>::kBytes;
   if (hipError_t e = allow_lds(chain_kernel<DK, DV, STORE>, lds); e != hipSuccess) return e;
   hipLaunchKernelGGL((chain_kernel<DK, DV, STORE>), dim3(chain_grid(a.N * a.Hv, DV / 64)),
-                     dim3(kThreads), lds, st, q, k, v, a.S0, a.tab, a.N, a.Hk, a.Hv, rec,
+                     dim3(2 * kThreads), lds, st, q, k, v, a.S0, a.tab, a.N, a.Hk, a.Hv, rec,
                      static_cast<__hip_bfloat16 *>(a.o), a.S_T, S, E);
   return hipGetLastError();
 }
