@@ -143,12 +143,12 @@ extern "C" int gdr_decode_step(const void *q, const void *k, const void *v, cons
 namespace {
 
 // Workspace of the backward.  bf16 inputs: the sequence table, then per
-// (chunk, value head) the records, S, E, dS and F.  fp32 inputs: the table,
+// (chunk, value head) the records, S, U, dS and F.  fp32 inputs: the table,
 // the expanded q, k, gates and their gradients, then the fp64 backward's own
 // workspace (its table included).
 struct GdrBwdLayout {
   size_t n_chunks, total;
-  size_t rec, S, E, dS, F;               // bf16
+  size_t rec, S, U, dS, F;               // bf16
   size_t x[6], inner;                    // fp32
 };
 
@@ -162,7 +162,7 @@ GdrBwdLayout gdr_bwd_layout(int B, int T, int Hv, int dk, int dv, int N, int in_
     const GdrBwdBytes b = gdr_backward_bytes(dk, dv);
     L.rec = take(ch * b.rec);
     L.S = take(ch * b.state);
-    L.E = take(ch * b.rows);
+    L.U = take(ch * b.rows);
     L.dS = take(ch * b.state);
     L.F = take(ch * b.rows);
   } else {
@@ -227,7 +227,7 @@ extern "C" int gdr_backward(const void *q, const void *k, const void *v, const f
     a.fwd.tab = tab; a.fwd.n_chunks_ub = L.n_chunks;
     a.fwd.N = N; a.fwd.Hk = Hk; a.fwd.Hv = Hv; a.fwd.dk = dk; a.fwd.dv = dv;
     a.d_o = d_o; a.dS_T = dS_T;
-    a.rec = w + L.rec; a.S = w + L.S; a.E = w + L.E; a.dS = w + L.dS; a.F = w + L.F;
+    a.rec = w + L.rec; a.S = w + L.S; a.U = w + L.U; a.dS = w + L.dS; a.F = w + L.F;
     a.dq = dq; a.dk = d_k; a.dv = d_v; a.dg = dg; a.dbeta = dbeta; a.dS0 = dS0;
     return launch_gdr_backward(a, st) == hipSuccess ? CKDA_OK : CKDA_ERR_LAUNCH;
   }

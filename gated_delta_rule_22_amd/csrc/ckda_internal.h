@@ -122,18 +122,18 @@ hipError_t launch_gdr_token(const GdrArgs &a, int in_dtype, hipStream_t stream);
 // gdr_forward_rec_bytes() for every chunk and value head.
 size_t gdr_forward_rec_bytes();
 hipError_t launch_gdr_forward(const GdrArgs &a, void *rec, hipStream_t stream);
-// The same chain for the backward: keeps the state before every chunk and E
+// The same chain for the backward: keeps the state before every chunk and U
 // (two bf16 terms each, in result-tile order) and makes no output.
-hipError_t launch_gdr_keep(const GdrArgs &a, void *rec, void *S, void *E, hipStream_t stream);
+hipError_t launch_gdr_keep(const GdrArgs &a, void *rec, void *S, void *U, hipStream_t stream);
 struct GdrBwdArgs {
     GdrArgs fwd;                         // fwd.S_T is NULL
     const void *d_o;
     const float *dS_T;
-    void *rec, *S, *E, *dS, *F;          // per (chunk, value head): see GdrBwdBytes
+    void *rec, *S, *U, *dS, *F;          // per (chunk, value head): see GdrBwdBytes
     void *dq, *dk, *dv;
     float *dg, *dbeta, *dS0;
 };
-struct GdrBwdBytes { size_t rec, state, rows; };   // rec; S and dS; E and F
+struct GdrBwdBytes { size_t rec, state, rows; };   // rec; S and dS; U and F
 GdrBwdBytes gdr_backward_bytes(int dk, int dv);
 hipError_t launch_gdr_backward(const GdrBwdArgs &a, hipStream_t stream);
 // fp32 inputs' backward: layouts to and from the per-channel fp64 backward.

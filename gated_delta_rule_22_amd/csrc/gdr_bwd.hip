@@ -3,19 +3,20 @@
 // With dS' the gradient of the state behind the chunk and the forward's
 // symbols (gdr_chunk.hip):
 //
-//   dU = P^T dO + (gam_n / gam) K dS'        F = T'^T (beta dU)   ( = dV )
+//   dU = P^T dO + (gam_n / gam) K dS'        F = T^T dU   ( = dV )
 //   dS = gam_n dS' + Q^T (gam dO) - K^T (gam F)
-//   dP_ij = r_ij dO_i.U_j                    dA_ij = -r_ij beta_j F_i.E_j
+//   dP_ij = r_ij dO_i.U_j                    dA_ij = -r_ij F_i.U_j
 //   dQ = gam dO S^T + dP K
 //   dK = [-gam F S^T + dA K] + [dP^T Q + dA^T K + (gam_n / gam) U dS'^T]
-//   dbeta = F.E / beta
+//   dbeta = F.U / beta^2
 //   dG_i = q_i.dQ_i + k_i.dK_i[first bracket] - k_i.dK_i[second bracket]
 //   dg_t = sum_{i >= t} dG_i + sum_j w_j + gam_n <S, dS'>
 //
-// where w_j is the last term's part of k_j.dK_j.  (U = beta E and beta is kept
-// off zero by kBetaFloor, so F.E / beta holds at beta = 0 too.)
+// where w_j is the last term's part of k_j.dK_j.  (F and U carry a factor beta
+// each, and beta is kept off zero by kBetaFloor, so F.U / beta^2 holds at
+// beta = 0 too.)
 //
-// Three passes: the forward's chain kept per chunk (S, E), the chain of dS
+// Three passes: the forward's chain kept per chunk (S, U), the chain of dS
 // backwards (dS', F), each serial in the chunks of a (sequence, head), and the
 // gradients, parallel over chunks.  Everything that feeds an fp32 gradient
 // (dg, dbeta, dS0) runs in two bf16 terms, as in the forward.
@@ -40,11 +41,10 @@ __device__ __forceinline__ bool chain_block(int nblk, int pairs, int &pair, int 
 // Barrier A: the chunk's operands and those tiles are in LDS; barrier B: the
 // chain has read all of them but K.
 template <int DK> struct ReverseLds {
-  static constexpr int kBufK = C * kStride<DK>, kTiles = (4 + DK / 16) * 1024;   // a wave's
-  static constexpr int kK = 0, kT = 2 * kBufK, kGate = kT + 2 * kTri;
-  static constexpr int kQ = kGate + kGateBytes, kD = kQ + C * kStride<DK>;
-  static constexpr int kP = kD + C * kStride<64>, kGam = kP + 2 * kTri;
-  static constexpr int kTile = kGam + C * 4, kBytes = kTile + 4 * kTiles;
+  static constexpr int kBufK = kTile<DK>, kWave = (4 + DK / 16) * 1024;   // a wave's tiles
+  static constexpr int kK = 0, kT = 2 * kBufK, kQ = kT + 2 * kTri, kD = kQ + kTile<DK>;
+  static constexpr int kP = kD + kTile<64>, kGam = kP + 2 * kTri;
+  static constexpr int kTiles = kGam + C * 4, kBytes = kTiles + 4 * kWave;
 };
 
 template <int DK, int DV>
@@ -64,8 +64,7 @@ __global__ __launch_bounds__(2 * kThreads, 2) void reverse_kernel(
   const size_t row0 = tab.seq_start[seq];
   const size_t c0 = tab.chunk_off[seq];
   const int col = blk * BV + 16 * wave;
-  const float *gate = reinterpret_cast<const float *>(lds + L::kGate);
-  char *tiles = lds + L::kTile + wave * L::kTiles + lane * 16;
+  char *tiles = lds + L::kTiles + wave * L::kWave + lane * 16;
 
   if (threadIdx.x >= kThreads) {         // helper waves
     const int t = threadIdx.x - kThreads;
@@ -74,7 +73,6 @@ __global__ __launch_bounds__(2 * kThreads, 2) void reverse_kernel(
     Stage<DK> gk, gq;
     Stage<BV> gd;
     Linear<2 * kTri> gt, gp;
-    Linear<kGateBytes> gg;
     float gam = 0.f;
     // The chain's operands of chunk c, and the helpers' own of the chunk before.
     auto fetch_chain = [&](int c) {
@@ -82,12 +80,10 @@ __global__ __launch_bounds__(2 * kThreads, 2) void reverse_kernel(
       const char *rec = rec_base + ((c0 + c) * Hv + hv) * kRecBwd;
       gk.load(k + (row * Hk + hk) * DK, (size_t)Hk * DK, min(C, len - c * C), t);
       gt.load(rec + kRecTh, t);
-      gg.load(rec + kRecGate, t);
     };
-    auto put_chain = [&](int c) {
-      gk.store(lds + L::kK + (c & 1) * L::kBufK, t);
+    auto put_chain = [&](int c, int buf) {
+      gk.store(lds + L::kK + (buf & 1) * L::kBufK, min(C, len - c * C), t);
       gt.store(lds + L::kT, t);
-      gg.store(lds + L::kGate, t);
     };
     auto fetch_own = [&](int c) {
       const int valid = min(C, len - c * C);
@@ -101,11 +97,12 @@ __global__ __launch_bounds__(2 * kThreads, 2) void reverse_kernel(
         const int at = (t + i * kThreads) * 16;
         gp.r[i] = load16(rec + (at < kTri ? kRecPh + at : kRecPl + at - kTri), true);
       }
-      if (t < C) gam = reinterpret_cast<const float *>(rec + kRecGate)[kGam * C + t];
+      gam = reinterpret_cast<const float *>(rec + kRecGate)[kGam * C + t % C];
     };
-    auto put_own = [&]() {
-      gq.store(lds + L::kQ, t);
-      gd.store(lds + L::kD, t);
+    auto put_own = [&](int c) {
+      const int valid = min(C, len - c * C);
+      gq.store(lds + L::kQ, valid, t);
+      gd.store(lds + L::kD, valid, t);
       gp.store(lds + L::kP, t);
       if (t < C) reinterpret_cast<float *>(lds + L::kGam)[t] = gam;
     };
@@ -138,34 +135,32 @@ __global__ __launch_bounds__(2 * kThreads, 2) void reverse_kernel(
 #pragma unroll
       for (int i = 0; i < MT; ++i) *reinterpret_cast<f4 *>(tiles + (4 + i) * 1024) = qd[i];
     };
+    // Behind the first chunk the first one is staged again, read by nobody.
     const int last = chunks - 1;
     if (chunks > 0) {
       fetch_own(last);
       fetch_chain(last);
-      put_own();
-      put_chain(last);
+      put_own(last);
+      put_chain(last, last);
     }
     lds_barrier();                       // the helpers' operands of the last chunk
     if (chunks > 0) {
-      if (last > 0) fetch_own(last - 1);
+      fetch_own(max(last - 1, 0));
       ahead();
       put_tiles();
     }
     lds_barrier();                       // all helpers have read them
-    if (last > 0) put_own();
+    if (chunks > 0) put_own(max(last - 1, 0));
     for (int c = last; c >= 0; --c) {
       lds_barrier();                     // A
-      if (c > 0) {
-        fetch_chain(c - 1);
-        if (c > 1) fetch_own(c - 2);
-        ahead();
-      }
+      const int c1 = max(c - 1, 0), c2 = max(c - 2, 0);
+      fetch_chain(c1);
+      fetch_own(c2);
+      ahead();
       lds_barrier();                     // B
-      if (c > 0) {
-        put_tiles();
-        put_chain(c - 1);
-        if (c > 1) put_own();
-      }
+      put_tiles();
+      put_chain(c1, c - 1);
+      put_own(c2);
     }
     return;
   }
@@ -179,6 +174,20 @@ __global__ __launch_bounds__(2 * kThreads, 2) void reverse_kernel(
     for (int i = 0; i < MT; ++i)
 #pragma unroll
       for (int r = 0; r < 4; ++r) S[i][r] = dS_T[sbase + (size_t)(16 * i + 4 * h + r) * DV];
+  // The gate factors of a lane's tokens, from memory a chunk ahead.
+  f4 gam[4], last[4];
+  float gn = 0.f;
+  auto fetch_gates = [&](int c) {
+    const float *g = reinterpret_cast<const float *>(rec_base + ((c0 + c) * Hv + hv) * kRecBwd +
+                                                     kRecGate);
+#pragma unroll
+    for (int jt = 0; jt < 4; ++jt) {
+      gam[jt] = *reinterpret_cast<const f4 *>(g + kGam * C + 16 * jt + 4 * h);
+      last[jt] = *reinterpret_cast<const f4 *>(g + kLast * C + 16 * jt + 4 * h);
+    }
+    gn = g[kGam * C + C - 1];
+  };
+  if (chunks > 0) fetch_gates(chunks - 1);
   lds_barrier();                         // the helpers' two, before the loop
   lds_barrier();
   for (int c = chunks - 1; c >= 0; --c) {
@@ -193,33 +202,65 @@ __global__ __launch_bounds__(2 * kThreads, 2) void reverse_kernel(
       *reinterpret_cast<bf8 *>(p + ks * (DV / 16) * kFrag) = sf[ks].hi;
       *reinterpret_cast<bf8 *>(p + (KS + ks) * (DV / 16) * kFrag) = sf[ks].lo;
     }
-    f4 X[4];                             // beta dU
+    bf8 kf[KS][4];
+    f4 X[4];                             // dU
+    auto read_k = [&](int ks) {
 #pragma unroll
-    for (int jt = 0; jt < 4; ++jt) {
-      f4 y = 0.f;
+      for (int jt = 0; jt < 4; ++jt) kf[ks][jt] = rows_frag<DK>(K, 16 * jt, 32 * ks, lane);
+    };
+    auto times_s = [&](int ks) {
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks)
-        y = dot2(rows_frag<DK>(K, 16 * jt, 32 * ks, lane), sf[ks], y);
-      y = y * *reinterpret_cast<const f4 *>(gate + kLast * C + 16 * jt + 4 * h) +
-          *reinterpret_cast<const f4 *>(tiles + jt * 1024);
-      X[jt] = y * *reinterpret_cast<const f4 *>(gate + kBeta * C + 16 * jt + 4 * h);
+      for (int jt = 0; jt < 4; ++jt) X[jt] = mfma(kf[ks][jt], sf[ks].hi, ks ? X[jt] : f4(0.f));
+#pragma unroll
+      for (int jt = 0; jt < 4; ++jt) X[jt] = mfma(kf[ks][jt], sf[ks].lo, X[jt]);
+    };
+    read_k(0);
+    read_k(1);
+    fence_schedule();
+    if (KS > 2) {
+      read_k(KS - 2);
+      read_k(KS - 1);
     }
+    times_s(0);
+    fence_schedule();
+    f4 pd[4];
+#pragma unroll
+    for (int jt = 0; jt < 4; ++jt) pd[jt] = *reinterpret_cast<const f4 *>(tiles + jt * 1024);
+    Split t[4][2];                       // T^T: tiles jt, rows of ks >= jt / 2
+#pragma unroll
+    for (int jt = 0; jt < 4; ++jt)
+#pragma unroll
+      for (int ks = jt / 2; ks < 2; ++ks)
+        t[jt][ks] = {tri_frag_t(T, jt, ks, lane), tri_frag_t(T + kTri, jt, ks, lane)};
+#pragma unroll
+    for (int ks = 1; ks < KS; ++ks) times_s(ks);
+    fence_schedule();
+    bf8 kt[2][MT];                       // K^T for the update, read meanwhile
+    f4 qd[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) kt[0][i] = cols_frag<DK>(K, 0, 16 * i, lane);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) qd[i] = *reinterpret_cast<const f4 *>(tiles + (4 + i) * 1024);
+#pragma unroll
+    for (int jt = 0; jt < 4; ++jt) X[jt] = X[jt] * last[jt] + pd[jt];
     const Split x0 = split8(X[0], X[1]), x1 = split8(X[2], X[3]);
-    const float gn = gate[kGam * C + C - 1];
+    fence_schedule();
+    f4 F[4];
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
-      S[i] = S[i] * gn + *reinterpret_cast<const f4 *>(tiles + (4 + i) * 1024);
-    f4 F[4], gam[4];
+    for (int jt = 0; jt < 4; ++jt) F[jt] = 0.f;
 #pragma unroll
-    for (int jt = 0; jt < 4; ++jt) {
-      F[jt] = 0.f;
+    for (int term = 0; term < 3; ++term)
 #pragma unroll
-      for (int ks = jt / 2; ks < 2; ++ks) {
-        const Split t = {tri_frag_t(T, jt, ks, lane), tri_frag_t(T + kTri, jt, ks, lane)};
-        F[jt] = dot3(t, ks ? x1 : x0, F[jt]);
-      }
-      gam[jt] = *reinterpret_cast<const f4 *>(gate + kGam * C + 16 * jt + 4 * h);
-    }
+      for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int jt = 0; jt < 2 * ks + 2; ++jt) {
+          const Split &x = ks ? x1 : x0;
+          F[jt] = mfma(term == 2 ? t[jt][ks].lo : t[jt][ks].hi, term == 1 ? x.lo : x.hi, F[jt]);
+        }
+#pragma unroll
+    for (int i = 0; i < MT; ++i) S[i] = S[i] * gn + qd[i];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) kt[1][i] = cols_frag<DK>(K, 32, 16 * i, lane);
     lds_barrier();                       // B
     p = F_keep + (((c0 + c) * Hv + hv) * (4 * (DV / 16)) + col / 16) * kFrag + lane * 16;
     const Split f0 = split8(F[0], F[1]), f1 = split8(F[2], F[3]);
@@ -229,12 +270,17 @@ __global__ __launch_bounds__(2 * kThreads, 2) void reverse_kernel(
     *reinterpret_cast<bf8 *>(p + 3 * (DV / 16) * kFrag) = f1.lo;
 #pragma unroll
     for (int jt = 0; jt < 4; ++jt) F[jt] *= -gam[jt];
+    fetch_gates(max(c - 1, 0));
     const Split w0 = split8(F[0], F[1]), w1 = split8(F[2], F[3]);
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      S[i] = dot2(cols_frag<DK>(K, 0, 16 * i, lane), w0, S[i]);
-      S[i] = dot2(cols_frag<DK>(K, 32, 16 * i, lane), w1, S[i]);
-    }
+    for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+      for (int term = 0; term < 2; ++term)
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          const Split &w = ks ? w1 : w0;
+          S[i] = mfma(kt[ks][i], term ? w.lo : w.hi, S[i]);
+        }
   }
   if (dS0)
 #pragma unroll
@@ -252,9 +298,9 @@ __global__ __launch_bounds__(2 * kThreads, 2) void reverse_kernel(
 // tiles i >= w, five tiles for every wave.  Results have lane = token and 4
 // key channels a lane, so stores are 8 bytes and q.dq needs two exchanges.
 template <int DK, int DV> struct GradLds {
-  static constexpr int kK = 0, kQ = kK + C * kStride<DK>, kGate = kQ + C * kStride<DK>;
+  static constexpr int kK = 0, kQ = kK + kTile<DK>, kGate = kQ + kTile<DK>;
   static constexpr int kSum = kGate + kGateBytes, kX = kSum + 512;
-  static constexpr int kD = kX, kE = kD + C * kStride<DV>, kF = kE + 4 * C * DV;
+  static constexpr int kD = kX, kU = kD + kTile<DV>, kF = kU + 4 * C * DV;
   static constexpr int kEnd1 = kF + 4 * C * DV, kEnd2 = kX + 4 * DK * DV;
   static constexpr int kBytes = kEnd1 > kEnd2 ? kEnd1 : kEnd2;
 };
@@ -271,7 +317,7 @@ __global__ __launch_bounds__(kThreads, 1) void grad_kernel(
     const float *__restrict__ g, const float *__restrict__ beta,
     const __hip_bfloat16 *__restrict__ d_o, SeqTable tab, int N, int Hk, int Hv,
     const char *__restrict__ rec_base, const char *__restrict__ S_keep,
-    const char *__restrict__ E_keep, const char *__restrict__ dS_keep,
+    const char *__restrict__ U_keep, const char *__restrict__ dS_keep,
     const char *__restrict__ F_keep, __hip_bfloat16 *__restrict__ dq,
     __hip_bfloat16 *__restrict__ dk_out, __hip_bfloat16 *__restrict__ dv_out,
     float *__restrict__ dg, float *__restrict__ dbeta) {
@@ -295,8 +341,8 @@ __global__ __launch_bounds__(kThreads, 1) void grad_kernel(
     Stage<DK> a, b;
     a.load(k + (row0 * Hk + hk) * DK, (size_t)Hk * DK, valid, t);
     b.load(q + (row0 * Hk + hk) * DK, (size_t)Hk * DK, valid, t);
-    a.store(lds + L::kK, t);
-    b.store(lds + L::kQ, t);
+    a.store(lds + L::kK, valid, t);
+    b.store(lds + L::kQ, valid, t);
   }
   f4 dQ[MT], dK[MT];
 #pragma unroll
@@ -309,15 +355,15 @@ __global__ __launch_bounds__(kThreads, 1) void grad_kernel(
       Stage<DV> a;
       Linear<4 * C * DV> e, f;
       a.load(d_o + (row0 * Hv + hv) * DV, (size_t)Hv * DV, valid, t);
-      e.load(E_keep + ch * (4 * C * DV), t);
+      e.load(U_keep + ch * (4 * C * DV), t);
       f.load(F_keep + ch * (4 * C * DV), t);
       const float *rg = reinterpret_cast<const float *>(rec_base + ch * kRecBwd + kRecGate);
-      float ga = rg[t], gb = t < 2 * C ? rg[kThreads + t] : 0.f;
-      a.store(lds + L::kD, t);
-      e.store(lds + L::kE, t);
+      float ga = rg[t], gb = t < C ? rg[kThreads + t] : 0.f;
+      a.store(lds + L::kD, valid, t);
+      e.store(lds + L::kU, t);
       f.store(lds + L::kF, t);
       gate[t] = ga;
-      if (t < 2 * C) gate[kThreads + t] = gb;
+      if (t < C) gate[kThreads + t] = gb;
     }
     __syncthreads();
     const char *D = lds + L::kD;
@@ -328,14 +374,14 @@ __global__ __launch_bounds__(kThreads, 1) void grad_kernel(
       return Split{join(pair_quad_t(a, half, lane), pair_quad_t(a + kFrag, half, lane)),
                    join(pair_quad_t(b, half, lane), pair_quad_t(b + kFrag, half, lane))};
     };
-    auto Ef = [&](int tile, int ks) { return tile_split(lds + L::kE, tile, 4, ks); };
+    auto Uf = [&](int tile, int ks) { return tile_split(lds + L::kU, tile, 4, ks); };
     auto Ff = [&](int tile, int ks) { return tile_split(lds + L::kF, tile, 4, ks); };
     bf8 d[KV];
-    Split e[KV], f[KV];
+    Split u_[KV], f[KV];
 #pragma unroll
     for (int ks = 0; ks < KV; ++ks) {
       d[ks] = rows_frag<DV>(D, 16 * w, 32 * ks, lane);
-      e[ks] = Ef(w, ks);
+      u_[ks] = Uf(w, ks);
       f[ks] = Ff(w, ks);
     }
     const float ghi = gate[kGhi * C + tok], glo = gate[kGlo * C + tok];
@@ -351,17 +397,16 @@ __global__ __launch_bounds__(kThreads, 1) void grad_kernel(
         if (jt <= w) {
 #pragma unroll
           for (int ks = 0; ks < KV; ++ks) {
-            const Split x = Ef(jt, ks);
+            const Split x = Uf(jt, ks);
             p[jt] = dot2(x, d[ks], p[jt]);
             a[jt] = dot3(x, f[ks], a[jt]);
           }
           const f4 hj = *reinterpret_cast<const f4 *>(gate + kGhi * C + 16 * jt + 4 * h);
           const f4 lj = *reinterpret_cast<const f4 *>(gate + kGlo * C + 16 * jt + 4 * h);
-          const f4 bj = *reinterpret_cast<const f4 *>(gate + kBeta * C + 16 * jt + 4 * h);
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const int j = 16 * jt + 4 * h + r;
-            const float x = exp2f((ghi - hj[r]) + (glo - lj[r])) * bj[r];
+            const float x = exp2f((ghi - hj[r]) + (glo - lj[r]));
             p[jt][r] = tok >= j ? p[jt][r] * x : 0.f;
             a[jt][r] = tok > j ? -a[jt][r] * x : 0.f;
           }
@@ -375,15 +420,15 @@ __global__ __launch_bounds__(kThreads, 1) void grad_kernel(
         if (it >= w) {
 #pragma unroll
           for (int ks = 0; ks < KV; ++ks) {
-            p[it] = dot2(rows_frag<DV>(D, 16 * it, 32 * ks, lane), e[ks], p[it]);
-            a[it] = dot3(Ff(it, ks), e[ks], a[it]);
+            p[it] = dot2(rows_frag<DV>(D, 16 * it, 32 * ks, lane), u_[ks], p[it]);
+            a[it] = dot3(Ff(it, ks), u_[ks], a[it]);
           }
           const f4 hi = *reinterpret_cast<const f4 *>(gate + kGhi * C + 16 * it + 4 * h);
           const f4 li = *reinterpret_cast<const f4 *>(gate + kGlo * C + 16 * it + 4 * h);
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const int i = 16 * it + 4 * h + r;
-            const float x = exp2f((hi[r] - ghi) + (li[r] - glo)) * bet;
+            const float x = exp2f((hi[r] - ghi) + (li[r] - glo));
             p[it][r] = i >= tok ? p[it][r] * x : 0.f;
             a[it][r] = i > tok ? -a[it][r] * x : 0.f;
           }
@@ -410,12 +455,12 @@ __global__ __launch_bounds__(kThreads, 1) void grad_kernel(
             return widen4(a) + widen4(b);
           };
           const f4 x = part(f[ks]);
-          s += sum4(x * part(e[ks]));
+          s += sum4(x * part(u_[ks]));
           if (tok < valid)
             *reinterpret_cast<bf4 *>(o + 32 * ks + 16 * half + 4 * h) = round4(x * back);
         }
       s = over_quarters(s);
-      if (h == 0 && tok < valid) dbeta[(row0 + tok) * Hv + hv] = s / bet;
+      if (h == 0 && tok < valid) dbeta[(row0 + tok) * Hv + hv] = s / (bet * bet);
     }
     __syncthreads();
     {
@@ -452,7 +497,7 @@ __global__ __launch_bounds__(kThreads, 1) void grad_kernel(
       }
       c = dot2(q1, pn[1], c);
       c = dot2(k1, an[1], c);
-      const int off = tok * kStride<DK> + (16 * mt + 4 * h) * 2;
+      const int off = place_of<DK>(tok, 16 * mt + 4 * h);
       const f4 qv = widen4(*reinterpret_cast<const bf4 *>(Q + off));
       const f4 kv = widen4(*reinterpret_cast<const bf4 *>(K + off));
       dG += sum4(qv * a) + sum4(kv * (b - c));
@@ -482,16 +527,15 @@ __global__ __launch_bounds__(kThreads, 1) void grad_kernel(
       s.store(lds + L::kX, t);
     }
     __syncthreads();
-    const float lb = gate[kLastBeta * C + tok];
+    const float last = gate[kLast * C + tok];
     float ws = 0.f;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       f4 c = 0.f;
 #pragma unroll
-      for (int ks = 0; ks < KV; ++ks) c = dot3(Sf(mt, ks), e[ks], c);
-      c *= lb;
-      const f4 kv = widen4(*reinterpret_cast<const bf4 *>(K + tok * kStride<DK> +
-                                                          (16 * mt + 4 * h) * 2));
+      for (int ks = 0; ks < KV; ++ks) c = dot3(Sf(mt, ks), u_[ks], c);
+      c *= last;
+      const f4 kv = widen4(*reinterpret_cast<const bf4 *>(K + place_of<DK>(tok, 16 * mt + 4 * h)));
       ws += sum4(kv * c);
       dK[mt] += c;
     }
@@ -533,9 +577,9 @@ template <int DK, int DV> hipError_t backward_typed(const GdrBwdArgs &a, hipStre
   const auto *k = static_cast<const __hip_bfloat16 *>(f.k);
   const auto *d_o = static_cast<const __hip_bfloat16 *>(a.d_o);
   char *rec = static_cast<char *>(a.rec), *S = static_cast<char *>(a.S);
-  char *E = static_cast<char *>(a.E), *dS = static_cast<char *>(a.dS);
+  char *U = static_cast<char *>(a.U), *dS = static_cast<char *>(a.dS);
   char *F = static_cast<char *>(a.F);
-  if (hipError_t e = launch_gdr_keep(f, rec, S, E, st); e != hipSuccess) return e;
+  if (hipError_t e = launch_gdr_keep(f, rec, S, U, st); e != hipSuccess) return e;
   constexpr int lds = ReverseLds<DK>::kBytes;
   auto *rev = reverse_kernel<DK, DV>;
   hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(rev),
@@ -552,7 +596,7 @@ template <int DK, int DV> hipError_t backward_typed(const GdrBwdArgs &a, hipStre
                           hipFuncAttributeMaxDynamicSharedMemorySize, gl);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(gr, dim3((unsigned)(f.n_chunks_ub * f.Hk)), dim3(kThreads), gl, st, q, k, f.g,
-                     f.beta, d_o, f.tab, f.N, f.Hk, f.Hv, rec, S, E, dS, F,
+                     f.beta, d_o, f.tab, f.N, f.Hk, f.Hv, rec, S, U, dS, F,
                      static_cast<__hip_bfloat16 *>(a.dq), static_cast<__hip_bfloat16 *>(a.dk),
                      static_cast<__hip_bfloat16 *>(a.dv), a.dg, a.dbeta);
   return hipGetLastError();

@@ -41,19 +41,19 @@ constexpr int kTri = 6 * kFrag;         // a lower triangular matrix, one term
 __host__ __device__ constexpr int frag_at(int it, int ks) {
   return (it < 2 ? it : 2 * it - 2 + ks) * kFrag;
 }
-// T' hi, T' lo, P hi, six rows of 64 gate factors, P lo (backward only)
+// T hi, T lo, P hi, five rows of 64 gate factors, P lo (backward only)
 constexpr int kRecTh = 0, kRecTl = kTri, kRecPh = 2 * kTri, kRecGate = 3 * kTri;
-enum { kGam = 0, kLast = 1, kBeta = 2, kLastBeta = 3, kGhi = 4, kGlo = 5 };
-constexpr int kGateBytes = 6 * C * 4;
-constexpr int kRecFwd = kRecGate + kGateBytes;          // 19968
+enum { kGam = 0, kLast = 1, kBeta = 2, kGhi = 3, kGlo = 4 };
+constexpr int kGateBytes = 5 * C * 4;
+constexpr int kRecFwd = kRecGate + 2048;
 constexpr int kRecPl = kRecFwd;
-constexpr int kRecBwd = kRecFwd + kTri;                 // 26112
-static_assert(kRecFwd % 256 == 0 && kRecBwd % 256 == 0, "records stay aligned");
+constexpr int kRecBwd = kRecFwd + kTri;                 // 26624
+static_assert(kRecFwd % 4096 == 0 && kRecBwd % 256 == 0, "records stay aligned");
 
-// |beta| is raised to this where it is smaller: the backward divides by it,
-// and a token with beta = 0 still has a gradient there.  2^-64 of a value is
-// far below fp32's rounding of what it is added to.
-constexpr float kBetaFloor = 5.42101086e-20f;
+// |beta| is raised to this where it is smaller: the backward divides by its
+// square, and a token with beta = 0 still has a gradient there.  2^-40 of a
+// value is far below fp32's rounding of what it is added to.
+constexpr float kBetaFloor = 9.09494702e-13f;
 // log-gates below this count as this (e^-10000 is 0 in every product).
 constexpr double kGateFloor = -1e4;
 
@@ -92,17 +92,26 @@ __device__ __forceinline__ f4 dot3(const Split &a, const Split &b, f4 c) {
   return mfma(a.lo, b.hi, mfma(a.hi, b.lo, mfma(a.hi, b.hi, c)));
 }
 
-// ---- LDS operand reads.  Row-major tiles have rows of COLS bf16 and 32 bytes
-// of padding: the 16 rows x 32 bytes that one read covers then fall on each of
-// the 64 banks exactly twice (16 bytes of padding: 1.5 times the LDS cycles).
-template <int COLS> constexpr int kStride = COLS * 2 + 32;
+// ---- LDS operand reads.  A row-major tile of 64 rows keeps every 8 bytes (4
+// channels) of a row's 128-byte blocks at place `index ^ mix(row)`: a read of
+// one place of 16 rows (rows_frag) and a transposed read of 32 bytes of 4 rows
+// (cols_frag) both touch each of the 32 banks once per 16 lanes, at 4.1 cycles
+// a read.  With rows only padded, by 16, 32 or 48 bytes, one of the two takes
+// 7 to 16 cycles, and the chain kernels are bound by LDS.
+__device__ __forceinline__ int mix(int row) { return ((row & 3) << 2) | ((row >> 2) & 3); }
+template <int COLS> constexpr int kTile = C * COLS * 2;   // bytes of a tile
+template <int COLS> __device__ __forceinline__ int place_of(int row, int col) {
+  return row * (COLS * 2) + (col >> 6) * 128 + ((((col >> 2) & 15) ^ mix(row)) << 3);
+}
 
 // Operand whose lanes are rows: lane (m, h) gets row r0 + m, the 8 columns of
 // quarter h of the 32 from c0.
 template <int COLS>
 __device__ __forceinline__ bf8 rows_frag(const char *tile, int r0, int c0, int lane) {
-  const char *p = tile + (r0 + (lane & 15)) * kStride<COLS> + (c0 + 4 * (lane >> 4)) * 2;
-  return join(*reinterpret_cast<const bf4 *>(p), *reinterpret_cast<const bf4 *>(p + 32));
+  const int m = lane & 15, at = ((lane >> 4) ^ mix(m)) << 3;
+  const char *p = tile + (r0 + m) * (COLS * 2) + (c0 >> 6) * 128;
+  const int x = at ^ ((c0 & 32) * 2);
+  return join(*reinterpret_cast<const bf4 *>(p + x), *reinterpret_cast<const bf4 *>(p + (x ^ 32)));
 }
 // ds_read_b64_tr_b16: in each group of 16 lanes, lane s gives the address of 4
 // values and lane i gets value i % 4 of lanes i / 4, 4 + i / 4, 8 + i / 4 and
@@ -115,8 +124,9 @@ __device__ __forceinline__ bf4 read_tr(const char *p) {
 // 4 rows (r0 + 4h ..) of column c0 + lane % 16.
 template <int COLS>
 __device__ __forceinline__ bf4 cols_quad(const char *tile, int r0, int c0, int lane) {
-  const int s = lane & 15, h = lane >> 4;
-  return read_tr(tile + (r0 + 4 * h + (s >> 2)) * kStride<COLS> + (c0 + 4 * (s & 3)) * 2);
+  const int s = lane & 15, h = lane >> 4, row = 4 * h + (s >> 2);
+  const int at = ((s & 3) ^ mix(row)) << 3;
+  return read_tr(tile + (r0 + row) * (COLS * 2) + (c0 >> 6) * 128 + (at ^ ((c0 & 48) * 2)));
 }
 // Operand whose lanes are columns and whose contracted index is the row.
 template <int COLS>
@@ -153,40 +163,53 @@ __device__ __forceinline__ u4 load16(const void *p, bool there) {
   return r;
 }
 
-// ---- staging of a row-major [64][COLS] bf16 tile: global -> registers -> LDS
+// ---- staging of a row-major [64][COLS] bf16 tile: global -> registers -> LDS.
+// Rows past the `valid` (>= 1) ones are loaded from the last of them and
+// stored as zeros: loads without branches, so that waiting for them does not
+// wait for everything else in flight.
 template <int COLS> struct Stage {
   static constexpr int kLanes = COLS / 8, kRows = kThreads / kLanes, kPasses = C / kRows;
   u4 r[kPasses];
   __device__ __forceinline__ void load(const __hip_bfloat16 *p, size_t ld, int valid, int t) {
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
-      const int row = t / kLanes + i * kRows;
-      r[i] = load16(p + row * ld + (t % kLanes) * 8, row < valid);
+      const int row = min(t / kLanes + i * kRows, valid - 1);
+      r[i] = *reinterpret_cast<const u4 *>(p + row * ld + (t % kLanes) * 8);
     }
   }
-  __device__ __forceinline__ void store(char *tile, int t) const {
+  __device__ __forceinline__ void store(char *tile, int valid, int t) {
+    if (valid < C)
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i)
+        if (t / kLanes + i * kRows >= valid) r[i] = 0u;
 #pragma unroll
     for (int i = 0; i < kPasses; ++i)
-      *reinterpret_cast<u4 *>(tile + (t / kLanes + i * kRows) * kStride<COLS> +
-                                 (t % kLanes) * 16) = r[i];
+    {
+      const int row = t / kLanes + i * kRows, k = mix(row);
+      char *p = tile + row * (COLS * 2) + (t % kLanes) / 8 * 128 +
+                ((((t % kLanes) % 8 * 2) ^ (k & ~1)) << 3);
+      const u4 x = r[i];
+      *reinterpret_cast<u4 *>(p) = k & 1 ? u4{x[2], x[3], x[0], x[1]} : x;
+    }
   }
 };
 // Linear bytes: global -> registers -> LDS.
 template <int BYTES> struct Linear {
   static constexpr int kPasses = (BYTES + kThreads * 16 - 1) / (kThreads * 16);
+  static constexpr bool kWhole = BYTES % (kThreads * 16) == 0;
   u4 r[kPasses];
   __device__ __forceinline__ void load(const char *p, int t) {
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
       const int at = (t + i * kThreads) * 16;
-      r[i] = load16(p + at, BYTES % (kThreads * 16) == 0 || at < BYTES);
+      r[i] = *reinterpret_cast<const u4 *>(p + (kWhole ? at : min(at, BYTES - 16)));
     }
   }
   __device__ __forceinline__ void store(char *dst, int t) const {
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
       const int at = (t + i * kThreads) * 16;
-      if (BYTES % (kThreads * 16) == 0 || at < BYTES) *reinterpret_cast<u4 *>(dst + at) = r[i];
+      if (kWhole || at < BYTES) *reinterpret_cast<u4 *>(dst + at) = r[i];
     }
   }
 };
@@ -196,6 +219,12 @@ template <int BYTES> struct Linear {
 __device__ __forceinline__ void lds_barrier() {
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
+
+// The scheduler keeps instructions on their side of this: operands are read in
+// batches well ahead of the products that use them.  Left alone it reads each
+// fragment right before its product, and the wave waits an LDS latency (over
+// 100 cycles) per product.
+__device__ __forceinline__ void fence_schedule() { __builtin_amdgcn_sched_barrier(0); }
 
 // Orders this wave's LDS writes before its later reads (the hardware runs a
 // wave's LDS operations in order; this keeps the compiler to it).

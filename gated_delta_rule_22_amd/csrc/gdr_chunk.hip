@@ -3,16 +3,16 @@
 // With a = exp(g), G_i the running sum of g in a 64-token chunk, r_ij =
 // e^(G_i - G_j), gam_i = e^(G_i) and S the state that enters the chunk:
 //
-//   Ah_ij = r_ij k_i.k_j (i > j)      P_ij = r_ij q_i.k_j (i >= j)
-//   T' = (I + Ah diag(beta))^-1       E = T' (V - gam K S)
-//   U = beta E                        O = gam Q S + P U
+//   Ah_ij = r_ij k_i.k_j (i > j)          P_ij = r_ij q_i.k_j (i >= j)
+//   T = diag(beta) (I + Ah diag(beta))^-1
+//   U = T (V - gam K S)                   O = gam Q S + P U
 //   S <- gam_n S + K^T (gam_n / gam U)
 //
 // The gate is one number per token and head, so decays scale rows and columns
 // of products of the bf16 inputs themselves: k and q stay exact bf16 operands
 // (per-channel gates would have to be multiplied into them).
 //
-// prepare_kernel makes T', P and the gate factors of every chunk in parallel;
+// prepare_kernel makes T, P and the gate factors of every chunk in parallel;
 // chain_kernel runs the chunks of a (sequence, head) in order.
 #include "gdr_chunk.h"
 
@@ -80,7 +80,6 @@ __global__ __launch_bounds__(kThreads) void prepare_kernel(
   gate[kGam * C + lane] = gam;
   gate[kLast * C + lane] = last;
   gate[kBeta * C + lane] = b;
-  gate[kLastBeta * C + lane] = last * b;
   gate[kGhi * C + lane] = ghi;
   gate[kGlo * C + lane] = glo;
 
@@ -175,8 +174,9 @@ __global__ __launch_bounds__(kThreads) void prepare_kernel(
 #pragma unroll
     for (int ks = 0; ks <= it / 2; ++ks) {
       const float *p = M + (16 * it + m) * kMStride + 32 * ks + 4 * h;
-      const Split s = split8(*reinterpret_cast<const f4 *>(p),
-                             *reinterpret_cast<const f4 *>(p + 16));
+      const float bi = s_b[16 * it + m];
+      const Split s = split8(*reinterpret_cast<const f4 *>(p) * bi,
+                             *reinterpret_cast<const f4 *>(p + 16) * bi);
       *reinterpret_cast<bf8 *>(rec + kRecTh + frag_at(it, ks) + lane * 16) = s.hi;
       *reinterpret_cast<bf8 *>(rec + kRecTl + frag_at(it, ks) + lane * 16) = s.lo;
     }
@@ -194,20 +194,20 @@ __device__ __forceinline__ bool chain_block(int nblk, int pairs, int &pair, int 
 // -------------------------------------------------------------------- chain
 // A workgroup runs 64 of the state's DV columns of one (sequence, head) over
 // its chunks.  Four chain waves own 16 columns each for the whole sequence, so
-// the chain S -> K S -> E -> S of a column never leaves its wave: S is 4 DK /
+// the chain S -> K S -> U -> S of a column never leaves its wave: S is 4 DK /
 // 16 accumulator registers, and each product's result tiles are the next one's
 // operand.  Four helper waves (one more on each SIMD) do what the chain does
 // not wait for: they load the next chunk and make the output of this one.
 // Two barriers a chunk, A when the chunk's operands and S's terms are in LDS,
 // B when the chain has read all of them but K and has written U; what the next
 // chunk overwrites between B and the next A is only K's other buffer and those.
-// STORE: for the backward, keeps the state before each chunk and E (two bf16
+// STORE: for the backward, keeps the state before each chunk and U (two bf16
 // terms each) and makes no output.
 template <int DK, int DV, bool STORE> struct ChainLds {
-  static constexpr int kBufK = C * kStride<DK>;
-  static constexpr int kK = 0, kV = 2 * kBufK, kRec = kV + C * kStride<64>;
+  static constexpr int kBufK = gdr::kTile<DK>;
+  static constexpr int kK = 0, kV = 2 * kBufK, kRec = kV + gdr::kTile<64>;
   static constexpr int kQ = kRec + kRecFwd;                      // the rest: !STORE
-  static constexpr int kS = kQ + C * kStride<DK>, kSWave = 2 * (DK / 32) * kFrag;
+  static constexpr int kS = kQ + gdr::kTile<DK>, kSWave = 2 * (DK / 32) * kFrag;
   static constexpr int kU = kS + 4 * kSWave;
   static constexpr int kBytes = STORE ? kQ : kU + 4 * 2 * kFrag;
 };
@@ -217,7 +217,7 @@ __global__ __launch_bounds__(2 * kThreads, 2) void chain_kernel(
     const __hip_bfloat16 *__restrict__ q, const __hip_bfloat16 *__restrict__ k,
     const __hip_bfloat16 *__restrict__ v, const float *__restrict__ S0, SeqTable tab, int N,
     int Hk, int Hv, const char *__restrict__ rec_base, __hip_bfloat16 *__restrict__ o,
-    float *__restrict__ S_T, char *__restrict__ S_keep, char *__restrict__ E_keep) {
+    float *__restrict__ S_T, char *__restrict__ S_keep, char *__restrict__ U_keep) {
   using L = ChainLds<DK, DV, STORE>;
   constexpr int KS = DK / 32, MT = DK / 16, BV = 64;
   constexpr int kRec = STORE ? kRecBwd : kRecFwd;
@@ -248,32 +248,43 @@ __global__ __launch_bounds__(2 * kThreads, 2) void chain_kernel(
       gv.load(v + (row * Hv + hv) * DV + blk * BV, (size_t)Hv * DV, valid, t);
       gr.load(rec_base + ((c0 + c) * Hv + hv) * kRec, t);
     };
-    auto put = [&](int c) {
-      gk.store(lds + L::kK + (c & 1) * L::kBufK, t);
-      if (!STORE) gq.store(lds + L::kQ, t);
-      gv.store(lds + L::kV, t);
+    auto put = [&](int c, int buf) {
+      const int valid = min(C, len - c * C);
+      gk.store(lds + L::kK + (buf & 1) * L::kBufK, valid, t);
+      if (!STORE) gq.store(lds + L::kQ, valid, t);
+      gv.store(lds + L::kV, valid, t);
       gr.store(lds + L::kRec, t);
     };
     if (chunks > 0) {
       fetch(0);
-      put(0);
+      put(0, 0);
     }
     for (int c = 0; c < chunks; ++c) {
       lds_barrier();                     // A
-      if (c + 1 < chunks) fetch(c + 1);
+      const int next = min(c + 1, chunks - 1);   // the last one again: read by nobody
+      fetch(next);
       f4 a[4];
       bf8 p[6];
       if (!STORE) {
         // O, transposed: lane = token, 4 columns a lane.
+        Split s[KS];
+        bf8 qf[KS][4];
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          s[ks] = {*reinterpret_cast<const bf8 *>(s_S + ks * kFrag),
+                   *reinterpret_cast<const bf8 *>(s_S + (KS + ks) * kFrag)};
+#pragma unroll
+          for (int it = 0; it < 4; ++it) qf[ks][it] = rows_frag<DK>(Q, 16 * it, 32 * ks, lane);
+        }
+        fence_schedule();
 #pragma unroll
         for (int it = 0; it < 4; ++it) a[it] = 0.f;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-          const Split s = {*reinterpret_cast<const bf8 *>(s_S + ks * kFrag),
-                           *reinterpret_cast<const bf8 *>(s_S + (KS + ks) * kFrag)};
 #pragma unroll
-          for (int it = 0; it < 4; ++it)
-            a[it] = dot2(s, rows_frag<DK>(Q, 16 * it, 32 * ks, lane), a[it]);
+          for (int it = 0; it < 4; ++it) a[it] = mfma(s[ks].hi, qf[ks][it], a[it]);
+#pragma unroll
+          for (int it = 0; it < 4; ++it) a[it] = mfma(s[ks].lo, qf[ks][it], a[it]);
         }
 #pragma unroll
         for (int it = 0; it < 4; ++it) {
@@ -284,6 +295,7 @@ __global__ __launch_bounds__(2 * kThreads, 2) void chain_kernel(
         }
       }
       lds_barrier();                     // B
+      put(next, c + 1);                  // before the stores, which loads' waits count too
       if (!STORE) {
         // One term of P and of U: each is within 2^-9 of its value, and so is
         // the bf16 output itself.
@@ -300,7 +312,6 @@ __global__ __launch_bounds__(2 * kThreads, 2) void chain_kernel(
                 round4(a[it]);
         }
       }
-      if (c + 1 < chunks) put(c + 1);
     }
     return;
   }
@@ -315,6 +326,21 @@ __global__ __launch_bounds__(2 * kThreads, 2) void chain_kernel(
 #pragma unroll
       for (int r = 0; r < 4; ++r) S[i][r] = S0[sbase + (size_t)(16 * i + 4 * h + r) * DV];
 
+  // The gate factors of a lane's tokens come from memory a chunk ahead: read
+  // from LDS they would be 9 cycles of its time each for 64 bytes.
+  f4 gam[4], last[4];
+  float gn = 0.f;
+  auto fetch_gates = [&](int c) {
+    const float *g = reinterpret_cast<const float *>(rec_base + ((c0 + c) * Hv + hv) * kRec +
+                                                     kRecGate);
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      gam[it] = *reinterpret_cast<const f4 *>(g + kGam * C + 16 * it + 4 * h);
+      last[it] = *reinterpret_cast<const f4 *>(g + kLast * C + 16 * it + 4 * h);
+    }
+    gn = g[kGam * C + C - 1];
+  };
+  if (chunks > 0) fetch_gates(0);
   for (int c = 0; c < chunks; ++c) {
     const char *K = lds + L::kK + (c & 1) * L::kBufK;
     Split sf[KS];
@@ -337,54 +363,88 @@ __global__ __launch_bounds__(2 * kThreads, 2) void chain_kernel(
       }
     }
     // X = V - gam K S, as the operand of T' X
+    bf8 kf[KS][4];
     f4 X[4];
+    auto read_k = [&](int ks) {
 #pragma unroll
-    for (int it = 0; it < 4; ++it) {
-      f4 y = 0.f;
+      for (int it = 0; it < 4; ++it) kf[ks][it] = rows_frag<DK>(K, 16 * it, 32 * ks, lane);
+    };
+    auto times_s = [&](int ks) {
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks)
-        y = dot2(rows_frag<DK>(K, 16 * it, 32 * ks, lane), sf[ks], y);
-      const f4 gam = *reinterpret_cast<const f4 *>(gate + kGam * C + 16 * it + 4 * h);
-      X[it] = widen4(cols_quad<BV>(V, 16 * it, 16 * wave, lane)) - gam * y;
+      for (int it = 0; it < 4; ++it) X[it] = mfma(kf[ks][it], sf[ks].hi, ks ? X[it] : f4(0.f));
+#pragma unroll
+      for (int it = 0; it < 4; ++it) X[it] = mfma(kf[ks][it], sf[ks].lo, X[it]);
+    };
+    read_k(0);
+    read_k(1);
+    fence_schedule();
+    if (KS > 2) {
+      read_k(KS - 2);
+      read_k(KS - 1);
     }
+    times_s(0);
+    fence_schedule();
+    bf4 vq[4];
+    Split T[6];
+#pragma unroll
+    for (int it = 0; it < 4; ++it) vq[it] = cols_quad<BV>(V, 16 * it, 16 * wave, lane);
+#pragma unroll
+    for (int f = 0; f < 6; ++f)
+      T[f] = {*reinterpret_cast<const bf8 *>(R + kRecTh + f * kFrag + lane * 16),
+              *reinterpret_cast<const bf8 *>(R + kRecTl + f * kFrag + lane * 16)};
+#pragma unroll
+    for (int ks = 1; ks < KS; ++ks) times_s(ks);
+    fence_schedule();
+    bf8 kt[2][MT];                       // K^T for the update, read meanwhile
+#pragma unroll
+    for (int i = 0; i < MT; ++i) kt[0][i] = cols_frag<DK>(K, 0, 16 * i, lane);
+#pragma unroll
+    for (int it = 0; it < 4; ++it) X[it] = widen4(vq[it]) - gam[it] * X[it];
     const Split x0 = split8(X[0], X[1]), x1 = split8(X[2], X[3]);
-    f4 E[4];
+    fence_schedule();
+    f4 U[4];
 #pragma unroll
-    for (int it = 0; it < 4; ++it) {
-      E[it] = 0.f;
+    for (int it = 0; it < 4; ++it) U[it] = 0.f;
+    // the four tiles' products turn by turn: each waits for its own last one
 #pragma unroll
-      for (int ks = 0; ks <= it / 2; ++ks) {
-        const Split T = {tri_frag(R + kRecTh, it, ks, lane), tri_frag(R + kRecTl, it, ks, lane)};
-        E[it] = dot3(T, ks ? x1 : x0, E[it]);
-      }
-    }
-    f4 W[4];                             // gam_n / gam U
+    for (int term = 0; term < 3; ++term)
 #pragma unroll
-    for (int it = 0; it < 4; ++it)
-      W[it] = E[it] * *reinterpret_cast<const f4 *>(gate + kLastBeta * C + 16 * it + 4 * h);
-    const float gn = gate[kGam * C + C - 1];
+      for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int it = 2 * ks; it < 4; ++it) {
+          const Split &t = T[frag_at(it, ks) / kFrag];
+          const Split &x = ks ? x1 : x0;
+          U[it] = mfma(term == 2 ? t.lo : t.hi, term == 1 ? x.lo : x.hi, U[it]);
+        }
+#pragma unroll
+    for (int i = 0; i < MT; ++i) S[i] *= gn;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) kt[1][i] = cols_frag<DK>(K, 32, 16 * i, lane);
     if (STORE) {
-      char *p = E_keep + (((c0 + c) * Hv + hv) * (4 * (DV / 16)) + col / 16) * kFrag + lane * 16;
-      const Split e0 = split8(E[0], E[1]), e1 = split8(E[2], E[3]);
-      *reinterpret_cast<bf8 *>(p) = e0.hi;
-      *reinterpret_cast<bf8 *>(p + (DV / 16) * kFrag) = e1.hi;
-      *reinterpret_cast<bf8 *>(p + 2 * (DV / 16) * kFrag) = e0.lo;
-      *reinterpret_cast<bf8 *>(p + 3 * (DV / 16) * kFrag) = e1.lo;
+      char *p = U_keep + (((c0 + c) * Hv + hv) * (4 * (DV / 16)) + col / 16) * kFrag + lane * 16;
+      const Split u0 = split8(U[0], U[1]), u1 = split8(U[2], U[3]);
+      *reinterpret_cast<bf8 *>(p) = u0.hi;
+      *reinterpret_cast<bf8 *>(p + (DV / 16) * kFrag) = u1.hi;
+      *reinterpret_cast<bf8 *>(p + 2 * (DV / 16) * kFrag) = u0.lo;
+      *reinterpret_cast<bf8 *>(p + 3 * (DV / 16) * kFrag) = u1.lo;
     } else {
-#pragma unroll
-      for (int it = 0; it < 4; ++it)
-        E[it] *= *reinterpret_cast<const f4 *>(gate + kBeta * C + 16 * it + 4 * h);
-      *reinterpret_cast<bf8 *>(s_U) = join(round4(E[0]), round4(E[1]));
-      *reinterpret_cast<bf8 *>(s_U + kFrag) = join(round4(E[2]), round4(E[3]));
+      *reinterpret_cast<bf8 *>(s_U) = join(round4(U[0]), round4(U[1]));
+      *reinterpret_cast<bf8 *>(s_U + kFrag) = join(round4(U[2]), round4(U[3]));
     }
     lds_barrier();                       // B
-    const Split w0 = split8(W[0], W[1]), w1 = split8(W[2], W[3]);
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      S[i] *= gn;
-      S[i] = dot2(cols_frag<DK>(K, 0, 16 * i, lane), w0, S[i]);
-      S[i] = dot2(cols_frag<DK>(K, 32, 16 * i, lane), w1, S[i]);
-    }
+    for (int it = 0; it < 4; ++it) U[it] *= last[it];
+    fetch_gates(min(c + 1, chunks - 1));
+    const Split w0 = split8(U[0], U[1]), w1 = split8(U[2], U[3]);
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+      for (int term = 0; term < 2; ++term)
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          const Split &w = ks ? w1 : w0;
+          S[i] = mfma(kt[ks][i], term ? w.lo : w.hi, S[i]);
+        }
   }
   if (S_T)
 #pragma unroll
