@@ -39,10 +39,10 @@ __device__ __forceinline__ bool chain_block(int nblk, int pairs, int &pair, int 
 // compute the chain's inputs that do not depend on dS, P^T dO and
 // Q^T (gam dO), which the chain takes from LDS as result tiles.
 // Barrier A: the chunk's operands and those tiles are in LDS; barrier B: the
-// chain has read all of them but K.
+// chain has read all of them into registers.
 template <int DK> struct ReverseLds {
-  static constexpr int kBufK = kTile<DK>, kWave = (4 + DK / 16) * 1024;   // a wave's tiles
-  static constexpr int kK = 0, kT = 2 * kBufK, kQ = kT + 2 * kTri, kD = kQ + kTile<DK>;
+  static constexpr int kWave = (4 + DK / 16) * 1024;   // a wave's tiles
+  static constexpr int kK = 0, kT = kTile<DK>, kQ = kT + 2 * kTri, kD = kQ + kTile<DK>;
   static constexpr int kP = kD + kTile<64>, kGam = kP + 2 * kTri;
   static constexpr int kTiles = kGam + C * 4, kBytes = kTiles + 4 * kWave;
 };
@@ -64,6 +64,7 @@ __global__ __launch_bounds__(2 * kThreads, 2) void reverse_kernel(
   const size_t row0 = tab.seq_start[seq];
   const size_t c0 = tab.chunk_off[seq];
   const int col = blk * BV + 16 * wave;
+  const char *K = lds + L::kK, *T = lds + L::kT;
   char *tiles = lds + L::kTiles + wave * L::kWave + lane * 16;
 
   if (threadIdx.x >= kThreads) {         // helper waves
@@ -81,9 +82,9 @@ __global__ __launch_bounds__(2 * kThreads, 2) void reverse_kernel(
       gk.load(k + (row * Hk + hk) * DK, (size_t)Hk * DK, min(C, len - c * C), t);
       gt.load(rec + kRecTh, t);
     };
-    auto put_chain = [&](int c, int buf) {
-      gk.store(lds + L::kK + (buf & 1) * L::kBufK, min(C, len - c * C), t);
-      gt.store(lds + L::kT, t);
+    auto put_chain = [&](int c) {
+      gk.store(lds + L::kK, min(C, len - c * C), t);
+      gt.store_mixed(lds + L::kT, t);
     };
     auto fetch_own = [&](int c) {
       const int valid = min(C, len - c * C);
@@ -103,31 +104,53 @@ __global__ __launch_bounds__(2 * kThreads, 2) void reverse_kernel(
       const int valid = min(C, len - c * C);
       gq.store(lds + L::kQ, valid, t);
       gd.store(lds + L::kD, valid, t);
-      gp.store(lds + L::kP, t);
+      gp.store_mixed(lds + L::kP, t);
       if (t < C) reinterpret_cast<float *>(lds + L::kGam)[t] = gam;
     };
     f4 pd[4], qd[MT];
     auto ahead = [&]() {
       f4 d[4];                           // dO: lane = column, 4 tokens a tile
       bf4 r[4];
+      Split pf[4][2];
 #pragma unroll
       for (int it = 0; it < 4; ++it) r[it] = cols_quad<BV>(D, 16 * it, 16 * wave, lane);
+#pragma unroll
+      for (int jt = 0; jt < 4; ++jt) {
+        d[jt] = *reinterpret_cast<const f4 *>(s_gam + 16 * jt + 4 * h);
+#pragma unroll
+        for (int ks = jt / 2; ks < 2; ++ks)
+          pf[jt][ks] = {tri_frag_t(P, jt, ks, lane), tri_frag_t(P + kTri, jt, ks, lane)};
+      }
+      fence_schedule();
+      bf8 qf[2][MT];
+#pragma unroll
+      for (int i = 0; i < MT; ++i) qf[0][i] = cols_frag<DK>(Q, 0, 16 * i, lane);
       const bf8 d0 = join(r[0], r[1]), d1 = join(r[2], r[3]);
 #pragma unroll
       for (int jt = 0; jt < 4; ++jt) {
         pd[jt] = 0.f;
-#pragma unroll
-        for (int ks = jt / 2; ks < 2; ++ks) {
-          const Split p = {tri_frag_t(P, jt, ks, lane), tri_frag_t(P + kTri, jt, ks, lane)};
-          pd[jt] = dot2(p, ks ? d1 : d0, pd[jt]);
-        }
-        d[jt] = widen4(r[jt]) * *reinterpret_cast<const f4 *>(s_gam + 16 * jt + 4 * h);
+        d[jt] *= widen4(r[jt]);
       }
+#pragma unroll
+      for (int term = 0; term < 2; ++term)
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+          for (int jt = 0; jt < 2 * ks + 2; ++jt)
+            pd[jt] = mfma(term ? pf[jt][ks].lo : pf[jt][ks].hi, ks ? d1 : d0, pd[jt]);
+      fence_schedule();
+#pragma unroll
+      for (int i = 0; i < MT; ++i) qf[1][i] = cols_frag<DK>(Q, 32, 16 * i, lane);
       const Split e0 = split8(d[0], d[1]), e1 = split8(d[2], d[3]);
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
-        qd[i] = dot2(cols_frag<DK>(Q, 32, 16 * i, lane), e1,
-                     dot2(cols_frag<DK>(Q, 0, 16 * i, lane), e0, f4(0.f)));
+      for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int term = 0; term < 2; ++term)
+#pragma unroll
+          for (int i = 0; i < MT; ++i) {
+            const Split &e = ks ? e1 : e0;
+            qd[i] = mfma(qf[ks][i], term ? e.lo : e.hi, ks + term ? qd[i] : f4(0.f));
+          }
     };
     auto put_tiles = [&]() {
 #pragma unroll
@@ -141,7 +164,7 @@ __global__ __launch_bounds__(2 * kThreads, 2) void reverse_kernel(
       fetch_own(last);
       fetch_chain(last);
       put_own(last);
-      put_chain(last, last);
+      put_chain(last);
     }
     lds_barrier();                       // the helpers' operands of the last chunk
     if (chunks > 0) {
@@ -159,7 +182,7 @@ __global__ __launch_bounds__(2 * kThreads, 2) void reverse_kernel(
       ahead();
       lds_barrier();                     // B
       put_tiles();
-      put_chain(c1, c - 1);
+      put_chain(c1);
       put_own(c2);
     }
     return;
@@ -190,8 +213,8 @@ __global__ __launch_bounds__(2 * kThreads, 2) void reverse_kernel(
   if (chunks > 0) fetch_gates(chunks - 1);
   lds_barrier();                         // the helpers' two, before the loop
   lds_barrier();
+  __builtin_amdgcn_s_setprio(2);         // the chain before the helper on its SIMD
   for (int c = chunks - 1; c >= 0; --c) {
-    const char *K = lds + L::kK + (c & 1) * L::kBufK, *T = lds + L::kT;
     Split sf[KS];
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) sf[ks] = split8(S[2 * ks], S[2 * ks + 1]);
@@ -261,7 +284,9 @@ __global__ __launch_bounds__(2 * kThreads, 2) void reverse_kernel(
     for (int i = 0; i < MT; ++i) S[i] = S[i] * gn + qd[i];
 #pragma unroll
     for (int i = 0; i < MT; ++i) kt[1][i] = cols_frag<DK>(K, 32, 16 * i, lane);
+    fence_schedule();
     lds_barrier();                       // B
+    fence_schedule();
     p = F_keep + (((c0 + c) * Hv + hv) * (4 * (DV / 16)) + col / 16) * kFrag + lane * 16;
     const Split f0 = split8(F[0], F[1]), f1 = split8(F[2], F[3]);
     *reinterpret_cast<bf8 *>(p) = f0.hi;
@@ -293,15 +318,22 @@ __global__ __launch_bounds__(2 * kThreads, 2) void reverse_kernel(
 // ---------------------------------------------------------------- gradients
 // One workgroup per (chunk, query/key head); it goes over the group's value
 // heads one after another, so dQ and dK of a shared head are summed in
-// registers, in a fixed order.  Wave w owns tokens 16 w .. 16 w + 15: as rows
-// i it needs the tiles j <= w of the triangular products, as columns j the
-// tiles i >= w, five tiles for every wave.  Results have lane = token and 4
-// key channels a lane, so stores are 8 bytes and q.dq needs two exchanges.
+// registers, in a fixed order.  Eight waves, two on each SIMD: wave (w, e) owns
+// tokens 16 w .. 16 w + 15 and half e of the key channels.  As rows i its
+// tokens need the tiles j <= w of the triangular products, as columns j the
+// tiles i >= w, five tiles for every wave; e = 0 makes those of dP, e = 1 those
+// of dA, and they are exchanged through LDS.  The states are loaded while the
+// products before them run, into the place of what those have read.  Results
+// have lane = token and 4 key channels a lane, so stores are 8 bytes and q.dq
+// needs two exchanges.
+constexpr int kGradThreads = 512;
 template <int DK, int DV> struct GradLds {
   static constexpr int kK = 0, kQ = kK + kTile<DK>, kGate = kQ + kTile<DK>;
-  static constexpr int kSum = kGate + kGateBytes, kX = kSum + 512;
+  static constexpr int kSum = kGate + kGateBytes, kX = kSum + 1024;
   static constexpr int kD = kX, kU = kD + kTile<DV>, kF = kU + 4 * C * DV;
-  static constexpr int kEnd1 = kF + 4 * C * DV, kEnd2 = kX + 4 * DK * DV;
+  static constexpr int kEnd1 = kF + 4 * C * DV;
+  static constexpr int kTriX = kX + 4 * DK * DV;                 // 6 fragments a wave
+  static constexpr int kEnd2 = kTriX + 8 * 6 * kFrag;
   static constexpr int kBytes = kEnd1 > kEnd2 ? kEnd1 : kEnd2;
 };
 
@@ -312,7 +344,7 @@ __device__ __forceinline__ float over_quarters(float x) {
 }
 
 template <int DK, int DV>
-__global__ __launch_bounds__(kThreads, 1) void grad_kernel(
+__global__ __launch_bounds__(kGradThreads, 2) void grad_kernel(
     const __hip_bfloat16 *__restrict__ q, const __hip_bfloat16 *__restrict__ k,
     const float *__restrict__ g, const float *__restrict__ beta,
     const __hip_bfloat16 *__restrict__ d_o, SeqTable tab, int N, int Hk, int Hv,
@@ -322,7 +354,7 @@ __global__ __launch_bounds__(kThreads, 1) void grad_kernel(
     __hip_bfloat16 *__restrict__ dk_out, __hip_bfloat16 *__restrict__ dv_out,
     float *__restrict__ dg, float *__restrict__ dbeta) {
   using L = GradLds<DK, DV>;
-  constexpr int MT = DK / 16, NT = DV / 16, KV = DV / 32;
+  constexpr int MT = DK / 16, HT = MT / 2, NT = DV / 16, KV = DV / 32, NTH = kGradThreads;
   constexpr int kPlane = DK * DV * 2;    // bytes of one term of a state
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const int chunk = blockIdx.x / Hk, hk = blockIdx.x % Hk, rep = Hv / Hk;
@@ -331,242 +363,308 @@ __global__ __launch_bounds__(kThreads, 1) void grad_kernel(
   const int at = (chunk - tab.chunk_off[seq]) * C;
   const int valid = min(C, tab.seq_len[seq] - at);
   const size_t row0 = (size_t)tab.seq_start[seq] + at;
-  const int t = threadIdx.x, w = t >> 6, lane = t & 63, m = lane & 15, h = lane >> 4;
+  int t = threadIdx.x, lane = t & 63;
+  const int m = lane & 15, h = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6), w = wave & 3, e = wave >> 2;
   const int tok = 16 * w + m;            // this lane's token
-  const char *K = lds + L::kK, *Q = lds + L::kQ;
+  const char *K = lds + L::kK, *Q = lds + L::kQ, *D = lds + L::kD;
   float *gate = reinterpret_cast<float *>(lds + L::kGate);
-  float *s_dG = reinterpret_cast<float *>(lds + L::kSum), *s_n = s_dG + C;
+  float *s_dG = reinterpret_cast<float *>(lds + L::kSum), *s_n = s_dG + 2 * C;
 
-  {
-    Stage<DK> a, b;
-    a.load(k + (row0 * Hk + hk) * DK, (size_t)Hk * DK, valid, t);
-    b.load(q + (row0 * Hk + hk) * DK, (size_t)Hk * DK, valid, t);
-    a.store(lds + L::kK, valid, t);
-    b.store(lds + L::kQ, valid, t);
-  }
-  f4 dQ[MT], dK[MT];
+  Stage<DK, NTH> gk, gq;
+  gk.load(k + (row0 * Hk + hk) * DK, (size_t)Hk * DK, valid, t);
+  gq.load(q + (row0 * Hk + hk) * DK, (size_t)Hk * DK, valid, t);
+  f4 dQ[HT], dK[HT];
 #pragma unroll
-  for (int i = 0; i < MT; ++i) dQ[i] = dK[i] = 0.f;
+  for (int i = 0; i < HT; ++i) dQ[i] = dK[i] = 0.f;
+
+  // Operand from pair order: lanes are rows of tile `row`, contracted over the
+  // 32 columns of pairs 2 ks and 2 ks + 1.
+  auto turned = [&](const char *base, int row, int rows, int ks) {
+    const char *a = base + ((row >> 1) * NT + 2 * ks) * kFrag;
+    const char *b = a + (rows / 2) * NT * kFrag;
+    const int half = row & 1;
+    return Split{join(frag_quad_t(a, half, lane), frag_quad_t(a + kFrag, half, lane)),
+                 join(frag_quad_t(b, half, lane), frag_quad_t(b + kFrag, half, lane))};
+  };
+  auto Uf = [&](int tile, int ks) { return turned(lds + L::kU, tile, 4, ks); };
+  auto Ff = [&](int tile, int ks) { return turned(lds + L::kF, tile, 4, ks); };
+  auto Sf = [&](int mt, int ks) { return turned(lds + L::kX, mt, MT, ks); };
 
   for (int u = 0; u < rep; ++u) {
     const int hv = hk * rep + u;
     const size_t ch = (size_t)chunk * Hv + hv;
+    t = renewed(t);
+    lane = t & 63;
     {
-      Stage<DV> a;
-      Linear<4 * C * DV> e, f;
+      Stage<DV, NTH> a;
+      Linear<4 * C * DV, NTH> x, y;
       a.load(d_o + (row0 * Hv + hv) * DV, (size_t)Hv * DV, valid, t);
-      e.load(U_keep + ch * (4 * C * DV), t);
-      f.load(F_keep + ch * (4 * C * DV), t);
+      x.load(U_keep + ch * (4 * C * DV), t);
+      y.load(F_keep + ch * (4 * C * DV), t);
       const float *rg = reinterpret_cast<const float *>(rec_base + ch * kRecBwd + kRecGate);
-      float ga = rg[t], gb = t < C ? rg[kThreads + t] : 0.f;
+      const float ga = rg[min(t, 5 * C - 1)];
+      if (u == 0) {
+        gk.store(lds + L::kK, valid, t);
+        gq.store(lds + L::kQ, valid, t);
+      }
       a.store(lds + L::kD, valid, t);
-      e.store(lds + L::kU, t);
-      f.store(lds + L::kF, t);
-      gate[t] = ga;
-      if (t < C) gate[kThreads + t] = gb;
+      x.store_mixed(lds + L::kU, t);
+      y.store_mixed(lds + L::kF, t);
+      if (t < 5 * C) gate[t] = ga;
     }
     __syncthreads();
-    const char *D = lds + L::kD;
-    auto tile_split = [&](const char *base, int row, int rows, int ks) {
-      const char *a = base + ((row >> 1) * NT + 2 * ks) * kFrag;
-      const char *b = a + (rows / 2) * NT * kFrag;
-      const int half = row & 1;
-      return Split{join(pair_quad_t(a, half, lane), pair_quad_t(a + kFrag, half, lane)),
-                   join(pair_quad_t(b, half, lane), pair_quad_t(b + kFrag, half, lane))};
-    };
-    auto Uf = [&](int tile, int ks) { return tile_split(lds + L::kU, tile, 4, ks); };
-    auto Ff = [&](int tile, int ks) { return tile_split(lds + L::kF, tile, 4, ks); };
+    Linear<2 * kPlane, NTH> state;       // S, on its way while the first products run
+    state.load(S_keep + ch * (2 * kPlane), t);
     bf8 d[KV];
-    Split u_[KV], f[KV];
+    Split uo[KV], f[KV];                 // own rows of dO, U, F
 #pragma unroll
     for (int ks = 0; ks < KV; ++ks) {
       d[ks] = rows_frag<DV>(D, 16 * w, 32 * ks, lane);
-      u_[ks] = Uf(w, ks);
+      uo[ks] = Uf(w, ks);
       f[ks] = Ff(w, ks);
     }
     const float ghi = gate[kGhi * C + tok], glo = gate[kGlo * C + tok];
     const float bet = gate[kBeta * C + tok], gam = gate[kGam * C + tok];
+    const float last = gate[kLast * C + tok], gn = gate[kGam * C + C - 1];
 
-    // The triangular products, as operands: [lane i, over j] and [lane j, over i].
-    Split pt[2], at_[2], pn[2], an[2];
-    {
-      f4 p[4], a[4];
+    // The triangular products as operands: x[lane i, over j] from tiles j <= w
+    // and y[lane j, over i] from tiles i >= w.
+    f4 x[4], y[4];
 #pragma unroll
-      for (int jt = 0; jt < 4; ++jt) {
-        p[jt] = a[jt] = 0.f;
-        if (jt <= w) {
+    for (int jt = 0; jt < 4; ++jt) {
+      fence_schedule();                  // one tile's operands at a time in registers
+      x[jt] = 0.f;
+      if (jt <= w) {
+        f4 a = 0.f, b = 0.f;
+        Split z[KV];
 #pragma unroll
-          for (int ks = 0; ks < KV; ++ks) {
-            const Split x = Uf(jt, ks);
-            p[jt] = dot2(x, d[ks], p[jt]);
-            a[jt] = dot3(x, f[ks], a[jt]);
-          }
-          const f4 hj = *reinterpret_cast<const f4 *>(gate + kGhi * C + 16 * jt + 4 * h);
-          const f4 lj = *reinterpret_cast<const f4 *>(gate + kGlo * C + 16 * jt + 4 * h);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int j = 16 * jt + 4 * h + r;
-            const float x = exp2f((ghi - hj[r]) + (glo - lj[r]));
-            p[jt][r] = tok >= j ? p[jt][r] * x : 0.f;
-            a[jt][r] = tok > j ? -a[jt][r] * x : 0.f;
-          }
-        }
-      }
-      pt[0] = split8(p[0], p[1]); pt[1] = split8(p[2], p[3]);
-      at_[0] = split8(a[0], a[1]); at_[1] = split8(a[2], a[3]);
-#pragma unroll
-      for (int it = 0; it < 4; ++it) {
-        p[it] = a[it] = 0.f;
-        if (it >= w) {
+        for (int ks = 0; ks < KV; ++ks) z[ks] = Uf(jt, ks);
+        if (e == 0)
 #pragma unroll
           for (int ks = 0; ks < KV; ++ks) {
-            p[it] = dot2(rows_frag<DV>(D, 16 * it, 32 * ks, lane), u_[ks], p[it]);
-            a[it] = dot3(Ff(it, ks), u_[ks], a[it]);
+            a = mfma(z[ks].hi, d[ks], a);
+            b = mfma(z[ks].lo, d[ks], b);
           }
-          const f4 hi = *reinterpret_cast<const f4 *>(gate + kGhi * C + 16 * it + 4 * h);
-          const f4 li = *reinterpret_cast<const f4 *>(gate + kGlo * C + 16 * it + 4 * h);
+        else
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int i = 16 * it + 4 * h + r;
-            const float x = exp2f((hi[r] - ghi) + (li[r] - glo));
-            p[it][r] = i >= tok ? p[it][r] * x : 0.f;
-            a[it][r] = i > tok ? -a[it][r] * x : 0.f;
+          for (int ks = 0; ks < KV; ++ks) {
+            a = mfma(z[ks].hi, f[ks].hi, a);
+            b = mfma(z[ks].hi, f[ks].lo, mfma(z[ks].lo, f[ks].hi, b));
           }
+        a += b;
+        const f4 hj = *reinterpret_cast<const f4 *>(gate + kGhi * C + 16 * jt + 4 * h);
+        const f4 lj = *reinterpret_cast<const f4 *>(gate + kGlo * C + 16 * jt + 4 * h);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float z2 = a[r] * pow2((ghi - hj[r]) + (glo - lj[r]));
+          const int j = 16 * jt + 4 * h + r;
+          x[jt][r] = e == 0 ? (tok >= j ? z2 : 0.f) : (tok > j ? -z2 : 0.f);
         }
       }
-      pn[0] = split8(p[0], p[1]); pn[1] = split8(p[2], p[3]);
-      an[0] = split8(a[0], a[1]); an[1] = split8(a[2], a[3]);
     }
-    // dV and dbeta from the wave's own rows.
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      fence_schedule();
+      y[it] = 0.f;
+      if (it >= w) {
+        f4 a = 0.f, b = 0.f;
+        if (e == 0) {
+          bf8 z[KV];
+#pragma unroll
+          for (int ks = 0; ks < KV; ++ks) z[ks] = rows_frag<DV>(D, 16 * it, 32 * ks, lane);
+#pragma unroll
+          for (int ks = 0; ks < KV; ++ks) {
+            a = mfma(z[ks], uo[ks].hi, a);
+            b = mfma(z[ks], uo[ks].lo, b);
+          }
+        } else {
+          Split z[KV];
+#pragma unroll
+          for (int ks = 0; ks < KV; ++ks) z[ks] = Ff(it, ks);
+#pragma unroll
+          for (int ks = 0; ks < KV; ++ks) {
+            a = mfma(z[ks].hi, uo[ks].hi, a);
+            b = mfma(z[ks].hi, uo[ks].lo, mfma(z[ks].lo, uo[ks].hi, b));
+          }
+        }
+        a += b;
+        const f4 hi = *reinterpret_cast<const f4 *>(gate + kGhi * C + 16 * it + 4 * h);
+        const f4 li = *reinterpret_cast<const f4 *>(gate + kGlo * C + 16 * it + 4 * h);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float z2 = a[r] * pow2((hi[r] - ghi) + (li[r] - glo));
+          const int i = 16 * it + 4 * h + r;
+          y[it][r] = e == 0 ? (i >= tok ? z2 : 0.f) : (i > tok ? -z2 : 0.f);
+        }
+      }
+    }
+    // dV and dbeta from the wave's own rows, half of the channels each.
     {
       float s = 0.f;
       const float own = tok < valid ? beta[(row0 + tok) * Hv + hv] : 0.f;
       const float back = own / bet;      // 1, or below 1 where beta was raised
       __hip_bfloat16 *o = dv_out + ((row0 + tok) * Hv + hv) * DV;
+      auto part = [&](const Split &z, int half) {
+        const bf4 a = half ? __builtin_shufflevector(z.hi, z.hi, 4, 5, 6, 7)
+                           : __builtin_shufflevector(z.hi, z.hi, 0, 1, 2, 3);
+        const bf4 b = half ? __builtin_shufflevector(z.lo, z.lo, 4, 5, 6, 7)
+                           : __builtin_shufflevector(z.lo, z.lo, 0, 1, 2, 3);
+        return widen4(a) + widen4(b);
+      };
 #pragma unroll
       for (int ks = 0; ks < KV; ++ks)
+        if ((ks & 1) == e)
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          auto part = [&](const Split &x) {
-            const bf4 a = half ? __builtin_shufflevector(x.hi, x.hi, 4, 5, 6, 7)
-                               : __builtin_shufflevector(x.hi, x.hi, 0, 1, 2, 3);
-            const bf4 b = half ? __builtin_shufflevector(x.lo, x.lo, 4, 5, 6, 7)
-                               : __builtin_shufflevector(x.lo, x.lo, 0, 1, 2, 3);
-            return widen4(a) + widen4(b);
-          };
-          const f4 x = part(f[ks]);
-          s += sum4(x * part(u_[ks]));
-          if (tok < valid)
-            *reinterpret_cast<bf4 *>(o + 32 * ks + 16 * half + 4 * h) = round4(x * back);
-        }
+          for (int half = 0; half < 2; ++half) {
+            const f4 z = part(f[ks], half);
+            s += sum4(z * part(uo[ks], half));
+            if (tok < valid)
+              *reinterpret_cast<bf4 *>(o + 32 * ks + 16 * half + 4 * h) = round4(z * back);
+          }
       s = over_quarters(s);
-      if (h == 0 && tok < valid) dbeta[(row0 + tok) * Hv + hv] = s / (bet * bet);
+      if (h == 0) s_dG[e * C + tok] = s;
     }
-    __syncthreads();
+    __syncthreads();                     // dO, U and F have been read
+    t = renewed(t);
+    lane = t & 63;
+    if (t < valid) dbeta[(row0 + t) * Hv + hv] =
+        (s_dG[t] + s_dG[C + t]) / (gate[kBeta * C + t] * gate[kBeta * C + t]);
+    state.store_mixed(lds + L::kX, t);
+    // x of tiles 0-1, then x of tiles 2-3 (w >= 2) or y of tiles 0-1 (w < 2,
+    // the others are zero), then y of tiles 2-3
+    char *ex = lds + L::kTriX + lane * 16;
     {
-      Linear<2 * kPlane> s;
-      s.load(S_keep + ch * (2 * kPlane), t);
-      s.store(lds + L::kX, t);
+      char *p = ex + (w * 2 + e) * 6 * kFrag;
+      const Split x0 = split8(x[0], x[1]), y1 = split8(y[2], y[3]);
+      const Split z = w >= 2 ? split8(x[2], x[3]) : split8(y[0], y[1]);
+      const bf8 all[6] = {x0.hi, x0.lo, z.hi, z.lo, y1.hi, y1.lo};
+#pragma unroll
+      for (int i = 0; i < 6; ++i) *reinterpret_cast<bf8 *>(p + i * kFrag) = all[i];
     }
     __syncthreads();
-    auto Sf = [&](int mt, int ks) { return tile_split(lds + L::kX, mt, MT, ks); };
+    state.load(dS_keep + ch * (2 * kPlane), t);
+    // read where they are used, not kept: 48 registers otherwise
+    const char *px = ex + w * 12 * kFrag;
+    auto tp = [&](int i) {
+      return Split{*reinterpret_cast<const bf8 *>(px + 2 * i * kFrag),
+                   *reinterpret_cast<const bf8 *>(px + (2 * i + 1) * kFrag)};
+    };
+    auto ta = [&](int i) {
+      return Split{*reinterpret_cast<const bf8 *>(px + (6 + 2 * i) * kFrag),
+                   *reinterpret_cast<const bf8 *>(px + (7 + 2 * i) * kFrag)};
+    };
     float dG = 0.f;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      f4 a = 0.f, b = 0.f;
+    for (int i = 0; i < HT; ++i) {
+      fence_schedule();
+      lane = renewed(lane);
+      const int mt = e * HT + i;
+      f4 a = 0.f, b = 0.f, a2 = 0.f, b2 = 0.f;
+      Split s[KV];
 #pragma unroll
-      for (int ks = 0; ks < KV; ++ks) {
-        const Split s = Sf(mt, ks);
-        a = dot2(s, d[ks], a);
-        b = dot3(s, f[ks], b);
-      }
-      a *= gam;
-      b *= -gam;
+      for (int ks = 0; ks < KV; ++ks) s[ks] = Sf(mt, ks);
       const bf8 k0 = cols_frag<DK>(K, 0, 16 * mt, lane), k1 = cols_frag<DK>(K, 32, 16 * mt, lane);
       const bf8 q0 = cols_frag<DK>(Q, 0, 16 * mt, lane), q1 = cols_frag<DK>(Q, 32, 16 * mt, lane);
-      a = dot2(k0, pt[0], a);
-      b = dot2(k0, at_[0], b);
-      if (w >= 2) {                      // tiles j >= 32 lie above the diagonal for w < 2
-        a = dot2(k1, pt[1], a);
-        b = dot2(k1, at_[1], b);
-      }
-      f4 c = 0.f;
-      if (w < 2) {
-        c = dot2(q0, pn[0], c);
-        c = dot2(k0, an[0], c);
-      }
-      c = dot2(q1, pn[1], c);
-      c = dot2(k1, an[1], c);
       const int off = place_of<DK>(tok, 16 * mt + 4 * h);
       const f4 qv = widen4(*reinterpret_cast<const bf4 *>(Q + off));
       const f4 kv = widen4(*reinterpret_cast<const bf4 *>(K + off));
+#pragma unroll
+      for (int ks = 0; ks < KV; ++ks) {
+        a = mfma(s[ks].hi, d[ks], a);
+        b = mfma(s[ks].hi, f[ks].hi, b);
+        a2 = mfma(s[ks].lo, d[ks], a2);
+        b2 = mfma(s[ks].lo, f[ks].hi, b2);
+        b = mfma(s[ks].hi, f[ks].lo, b);
+      }
+      a = (a + a2) * gam;
+      b = (b + b2) * -gam;
+      a = dot2(k0, tp(0), a);
+      b = dot2(k0, ta(0), b);
+      f4 c = dot2(q1, tp(2), f4(0.f));
+      c = dot2(k1, ta(2), c);
+      if (w >= 2) {
+        a = dot2(k1, tp(1), a);
+        b = dot2(k1, ta(1), b);
+      } else {
+        c = dot2(q0, tp(1), c);
+        c = dot2(k0, ta(1), c);
+      }
       dG += sum4(qv * a) + sum4(kv * (b - c));
-      dQ[mt] += a;
-      dK[mt] += b + c;
+      dQ[i] += a;
+      dK[i] += b + c;
     }
     // <S, dS'>, then dS' in place of S.
     float dot = 0.f;
     {
-      Linear<2 * kPlane> s;
-      s.load(dS_keep + ch * (2 * kPlane), t);
-      constexpr int kHalf = kPlane / (kThreads * 16);
+      constexpr int kHalf = kPlane / (NTH * 16);
 #pragma unroll
       for (int i = 0; i < kHalf; ++i) {
-        const char *p = lds + L::kX + (t + i * kThreads) * 16;
-        const u4 x = *reinterpret_cast<const u4 *>(p);
-        const u4 y = *reinterpret_cast<const u4 *>(p + kPlane);
-        const u4 z = s.r[i], v = s.r[i + kHalf];
-        auto low = [](uint32_t a) { return __uint_as_float(a << 16); };
-        auto high = [](uint32_t a) { return __uint_as_float(a & 0xFFFF0000u); };
+        using Lin = Linear<2 * kPlane, NTH>;
+        const char *p = lds + L::kX + (Lin::mixed(t) + i * NTH) * 16;
+        const u4 z = Lin::halves(state.r[i], t), v = Lin::halves(state.r[i + kHalf], t);
+        const u4 a = *reinterpret_cast<const u4 *>(p), b = *reinterpret_cast<const u4 *>(p + kPlane);
+        auto low = [](uint32_t q) { return __uint_as_float(q << 16); };
+        auto high = [](uint32_t q) { return __uint_as_float(q & 0xFFFF0000u); };
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          dot += (low(x[j]) + low(y[j])) * (low(z[j]) + low(v[j])) +
-                 (high(x[j]) + high(y[j])) * (high(z[j]) + high(v[j]));
+          dot += (low(a[j]) + low(b[j])) * (low(z[j]) + low(v[j])) +
+                 (high(a[j]) + high(b[j])) * (high(z[j]) + high(v[j]));
       }
-      __syncthreads();
-      s.store(lds + L::kX, t);
     }
     __syncthreads();
-    const float last = gate[kLast * C + tok];
+    t = renewed(t);
+    lane = t & 63;
+    state.store_mixed(lds + L::kX, t);
+    __syncthreads();
     float ws = 0.f;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      f4 c = 0.f;
+    for (int i = 0; i < HT; ++i) {
+      fence_schedule();
+      lane = renewed(lane);
+      const int mt = e * HT + i;
+      f4 c = 0.f, c2 = 0.f;
+      Split s[KV];
 #pragma unroll
-      for (int ks = 0; ks < KV; ++ks) c = dot3(Sf(mt, ks), u_[ks], c);
-      c *= last;
-      const f4 kv = widen4(*reinterpret_cast<const bf4 *>(K + place_of<DK>(tok, 16 * mt + 4 * h)));
-      ws += sum4(kv * c);
-      dK[mt] += c;
+      for (int ks = 0; ks < KV; ++ks) s[ks] = Sf(mt, ks);
+#pragma unroll
+      for (int ks = 0; ks < KV; ++ks) {
+        c = mfma(s[ks].hi, uo[ks].hi, c);
+        c2 = mfma(s[ks].lo, uo[ks].hi, c2);
+        c = mfma(s[ks].hi, uo[ks].lo, c);
+      }
+      c = (c + c2) * last;
+      ws += sum4(c * widen4(*reinterpret_cast<const bf4 *>(K + place_of<DK>(tok, 16 * mt + 4 * h))));
+      dK[i] += c;
     }
     dG = over_quarters(dG - ws);
-    if (h == 0) s_dG[tok] = dG;
+    if (h == 0) s_dG[e * C + tok] = dG;
     // sum_j w_j + gam_n <S, dS'> over the workgroup
-    float n = ws + gate[kGam * C + C - 1] * dot;
+    float n = ws + gn * dot;
     for (int o = 32; o > 0; o >>= 1) n += __shfl_xor(n, o);
-    if (lane == 0) s_n[w] = n;
+    if (lane == 0) s_n[wave] = n;
     __syncthreads();
-    if (w == 0) {
-      float x = s_dG[lane];
+    if (wave == 0) {
+      float z = s_dG[lane] + s_dG[C + lane];
 #pragma unroll
       for (int o = 1; o < 64; o <<= 1) {
-        const float y = __shfl_down(x, o);
-        if (lane + o < 64) x += y;
+        const float v = __shfl_down(z, o);
+        if (lane + o < 64) z += v;
       }
-      x += (s_n[0] + s_n[1]) + (s_n[2] + s_n[3]);
+      z += ((s_n[0] + s_n[1]) + (s_n[2] + s_n[3])) + ((s_n[4] + s_n[5]) + (s_n[6] + s_n[7]));
       if (lane < valid) {
         const size_t gi = (row0 + lane) * Hv + hv;
-        dg[gi] = g[gi] < (float)kGateFloor ? 0.f : x;   // a floored gate is constant
+        dg[gi] = g[gi] < (float)kGateFloor ? 0.f : z;   // a floored gate is constant
       }
     }
-    __syncthreads();
+    if (u + 1 < rep) __syncthreads();
   }
   if (tok < valid) {
-    const size_t o = ((row0 + tok) * Hk + hk) * DK + 4 * h;
+    const size_t o = ((row0 + tok) * Hk + hk) * DK + 16 * e * HT + 4 * h;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      *reinterpret_cast<bf4 *>(dq + o + 16 * mt) = round4(dQ[mt]);
-      *reinterpret_cast<bf4 *>(dk_out + o + 16 * mt) = round4(dK[mt]);
+    for (int i = 0; i < HT; ++i) {
+      *reinterpret_cast<bf4 *>(dq + o + 16 * i) = round4(dQ[i]);
+      *reinterpret_cast<bf4 *>(dk_out + o + 16 * i) = round4(dK[i]);
     }
   }
 }
@@ -595,7 +693,7 @@ template <int DK, int DV> hipError_t backward_typed(const GdrBwdArgs &a, hipStre
   e = hipFuncSetAttribute(reinterpret_cast<const void *>(gr),
                           hipFuncAttributeMaxDynamicSharedMemorySize, gl);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(gr, dim3((unsigned)(f.n_chunks_ub * f.Hk)), dim3(kThreads), gl, st, q, k, f.g,
+  hipLaunchKernelGGL(gr, dim3((unsigned)(f.n_chunks_ub * f.Hk)), dim3(kGradThreads), gl, st, q, k, f.g,
                      f.beta, d_o, f.tab, f.N, f.Hk, f.Hv, rec, S, U, dS, F,
                      static_cast<__hip_bfloat16 *>(a.dq), static_cast<__hip_bfloat16 *>(a.dk),
                      static_cast<__hip_bfloat16 *>(a.dv), a.dg, a.dbeta);

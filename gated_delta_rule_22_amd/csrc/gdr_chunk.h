@@ -57,6 +57,8 @@ constexpr float kBetaFloor = 9.09494702e-13f;
 // log-gates below this count as this (e^-10000 is 0 in every product).
 constexpr double kGateFloor = -1e4;
 
+// 2^x; results below 2^-126 are 0.
+__device__ __forceinline__ float pow2(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ f4 mfma(bf8 a, bf8 b, f4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
@@ -99,9 +101,10 @@ __device__ __forceinline__ f4 dot3(const Split &a, const Split &b, f4 c) {
 // a read.  With rows only padded, by 16, 32 or 48 bytes, one of the two takes
 // 7 to 16 cycles, and the chain kernels are bound by LDS.
 __device__ __forceinline__ int mix(int row) { return ((row & 3) << 2) | ((row >> 2) & 3); }
-template <int COLS> constexpr int kTile = C * COLS * 2;   // bytes of a tile
+template <int COLS> constexpr int kRow = (COLS < 64 ? 64 : COLS) * 2;   // bytes of a row
+template <int COLS> constexpr int kTile = C * kRow<COLS>;
 template <int COLS> __device__ __forceinline__ int place_of(int row, int col) {
-  return row * (COLS * 2) + (col >> 6) * 128 + ((((col >> 2) & 15) ^ mix(row)) << 3);
+  return row * kRow<COLS> + (col >> 6) * 128 + ((((col >> 2) & 15) ^ mix(row)) << 3);
 }
 
 // Operand whose lanes are rows: lane (m, h) gets row r0 + m, the 8 columns of
@@ -109,7 +112,7 @@ template <int COLS> __device__ __forceinline__ int place_of(int row, int col) {
 template <int COLS>
 __device__ __forceinline__ bf8 rows_frag(const char *tile, int r0, int c0, int lane) {
   const int m = lane & 15, at = ((lane >> 4) ^ mix(m)) << 3;
-  const char *p = tile + (r0 + m) * (COLS * 2) + (c0 >> 6) * 128;
+  const char *p = tile + (r0 + m) * kRow<COLS> + (c0 >> 6) * 128;
   const int x = at ^ ((c0 & 32) * 2);
   return join(*reinterpret_cast<const bf4 *>(p + x), *reinterpret_cast<const bf4 *>(p + (x ^ 32)));
 }
@@ -126,7 +129,7 @@ template <int COLS>
 __device__ __forceinline__ bf4 cols_quad(const char *tile, int r0, int c0, int lane) {
   const int s = lane & 15, h = lane >> 4, row = 4 * h + (s >> 2);
   const int at = ((s & 3) ^ mix(row)) << 3;
-  return read_tr(tile + (r0 + row) * (COLS * 2) + (c0 >> 6) * 128 + (at ^ ((c0 & 48) * 2)));
+  return read_tr(tile + (r0 + row) * kRow<COLS> + (c0 >> 6) * 128 + (at ^ ((c0 & 48) * 2)));
 }
 // Operand whose lanes are columns and whose contracted index is the row.
 template <int COLS>
@@ -136,26 +139,26 @@ __device__ __forceinline__ bf8 cols_frag(const char *tile, int r0, int c0, int l
 __device__ __forceinline__ bf8 tri_frag(const char *mat, int it, int ks, int lane) {
   return *reinterpret_cast<const bf8 *>(mat + frag_at(it, ks) + lane * 16);
 }
-// The same matrix transposed: lanes are its columns 16 jt + m, contracted over
-// the rows of tiles 2 ks and 2 ks + 1 (tiles above the diagonal are zero).
-__device__ __forceinline__ bf4 tri_quad_t(const char *mat, int it, int jt, int lane) {
+// Fragments that are read transposed keep lane (m, h)'s 16 bytes at slot
+// (m ^ 4 (h & 1), h), with the two 8-byte halves exchanged for h >= 2: the 16
+// pieces that such a read collects then lie in different banks (7 cycles a
+// read without, 4.1 with).  Linear::store_mixed writes them so.
+__device__ __forceinline__ bf4 frag_quad_t(const char *frag, int half, int lane) {
   const int s = lane & 15, h = lane >> 4;
-  return read_tr(mat + frag_at(it, jt >> 1) + ((s & 3) * 16 + 4 * h + (s >> 2)) * 16 +
-                 (jt & 1) * 8);
+  const int at = ((s & 3) * 16 + ((4 * h + (s >> 2)) ^ (4 * (s & 1)))) * 16 + ((s >> 1) & 1) * 8;
+  return read_tr(frag + (at ^ (half * 8)));
 }
+// A triangular matrix transposed: lanes are its columns 16 jt + m, contracted
+// over the rows of tiles 2 ks and 2 ks + 1.  it = 2 ks < jt only where jt =
+// 2 ks + 1: that tile lies above the diagonal and is stored as zeros.
 __device__ __forceinline__ bf8 tri_frag_t(const char *mat, int jt, int ks, int lane) {
-  // it = 2 ks < jt only where jt = 2 ks + 1: that tile lies above the diagonal
-  // and is stored as zeros.
-  return join(tri_quad_t(mat, 2 * ks, jt, lane), tri_quad_t(mat, 2 * ks + 1, jt, lane));
+  return join(frag_quad_t(mat + frag_at(2 * ks, jt >> 1), jt & 1, lane),
+              frag_quad_t(mat + frag_at(2 * ks + 1, jt >> 1), jt & 1, lane));
 }
-// Pair order, used for states and E, F in the workspace: two 16 x 16 result
+// Pair order, used for states and U, F in the workspace: two 16 x 16 result
 // tiles, one above the other, as their 64 lanes x 8 values (16 bytes a lane),
-// which is the operand they make.  Transposed read of tile `half`: lane i gets
-// the 4 columns 4h .. of row i (a result's lane is its column).
-__device__ __forceinline__ bf4 pair_quad_t(const char *pair, int half, int lane) {
-  const int s = lane & 15, h = lane >> 4;
-  return read_tr(pair + ((s & 3) * 16 + 4 * h + (s >> 2)) * 16 + half * 8);
-}
+// which is the operand they make.  frag_quad_t of tile `half` gives lane i the
+// 4 columns 4h .. of its row i (a result's lane is its column).
 
 __device__ __forceinline__ u4 load16(const void *p, bool there) {
   u4 r = 0u;
@@ -167,8 +170,9 @@ __device__ __forceinline__ u4 load16(const void *p, bool there) {
 // Rows past the `valid` (>= 1) ones are loaded from the last of them and
 // stored as zeros: loads without branches, so that waiting for them does not
 // wait for everything else in flight.
-template <int COLS> struct Stage {
-  static constexpr int kLanes = COLS / 8, kRows = kThreads / kLanes, kPasses = C / kRows;
+template <int COLS, int THREADS = kThreads> struct Stage {
+  static constexpr int kLanes = COLS / 8, kRows = THREADS / kLanes, kPasses = C / kRows;
+  static_assert(kRows * kPasses == C, "whole passes");
   u4 r[kPasses];
   __device__ __forceinline__ void load(const __hip_bfloat16 *p, size_t ld, int valid, int t) {
 #pragma unroll
@@ -186,7 +190,7 @@ template <int COLS> struct Stage {
     for (int i = 0; i < kPasses; ++i)
     {
       const int row = t / kLanes + i * kRows, k = mix(row);
-      char *p = tile + row * (COLS * 2) + (t % kLanes) / 8 * 128 +
+      char *p = tile + row * kRow<COLS> + (t % kLanes) / 8 * 128 +
                 ((((t % kLanes) % 8 * 2) ^ (k & ~1)) << 3);
       const u4 x = r[i];
       *reinterpret_cast<u4 *>(p) = k & 1 ? u4{x[2], x[3], x[0], x[1]} : x;
@@ -194,22 +198,35 @@ template <int COLS> struct Stage {
   }
 };
 // Linear bytes: global -> registers -> LDS.
-template <int BYTES> struct Linear {
-  static constexpr int kPasses = (BYTES + kThreads * 16 - 1) / (kThreads * 16);
-  static constexpr bool kWhole = BYTES % (kThreads * 16) == 0;
+template <int BYTES, int THREADS = kThreads> struct Linear {
+  static constexpr int kPasses = (BYTES + THREADS * 16 - 1) / (THREADS * 16);
+  static constexpr bool kWhole = BYTES % (THREADS * 16) == 0;
   u4 r[kPasses];
   __device__ __forceinline__ void load(const char *p, int t) {
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
-      const int at = (t + i * kThreads) * 16;
+      const int at = (t + i * THREADS) * 16;
       r[i] = *reinterpret_cast<const u4 *>(p + (kWhole ? at : min(at, BYTES - 16)));
     }
   }
   __device__ __forceinline__ void store(char *dst, int t) const {
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
-      const int at = (t + i * kThreads) * 16;
+      const int at = (t + i * THREADS) * 16;
       if (kWhole || at < BYTES) *reinterpret_cast<u4 *>(dst + at) = r[i];
+    }
+  }
+  // Fragments for transposed reads (frag_quad_t); whole fragments a wave.
+  static __device__ __forceinline__ int mixed(int t) { return t ^ (((t >> 4) & 1) * 4); }
+  static __device__ __forceinline__ u4 halves(u4 x, int t) {
+    return t & 32 ? u4{x[2], x[3], x[0], x[1]} : x;
+  }
+  __device__ __forceinline__ void store_mixed(char *dst, int t) const {
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const int at = (mixed(t) + i * THREADS) * 16;
+      if (kWhole || (t + i * THREADS) * 16 < BYTES)
+        *reinterpret_cast<u4 *>(dst + at) = halves(r[i], t);
     }
   }
 };
@@ -225,6 +242,13 @@ __device__ __forceinline__ void lds_barrier() {
 // fragment right before its product, and the wave waits an LDS latency (over
 // 100 cycles) per product.
 __device__ __forceinline__ void fence_schedule() { __builtin_amdgcn_sched_barrier(0); }
+
+// The same number, as a new one: addresses made from it are computed where
+// they are used instead of being kept in registers from the kernel's start.
+__device__ __forceinline__ int renewed(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
 
 // Orders this wave's LDS writes before its later reads (the hardware runs a
 // wave's LDS operations in order; this keeps the compiler to it).

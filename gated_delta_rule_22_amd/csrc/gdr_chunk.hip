@@ -15,6 +15,7 @@
 // prepare_kernel makes T, P and the gate factors of every chunk in parallel;
 // chain_kernel runs the chunks of a (sequence, head) in order.
 #include "gdr_chunk.h"
+#include <stdlib.h>
 
 namespace ckda {
 using namespace gdr;
@@ -67,11 +68,11 @@ __global__ __launch_bounds__(kThreads) void prepare_kernel(
     if (lane >= o) G += y;
   }
   const double Gn = __shfl(G, 63);
-  auto pow2 = [](double x) {             // 2^x; whole and fractional part apart
+  auto pow2d = [](double x) {             // 2^x; whole and fractional part apart
     const double w = rint(x);
     return ldexpf(exp2f((float)(x - w)), (int)fmin(fmax(w, -3e4), 3e4));
   };
-  const float gam = pow2(G), last = pow2(Gn - G);
+  const float gam = pow2d(G), last = pow2d(Gn - G);
   const float ghi = (float)G, glo = (float)(G - (double)ghi);
   s_hi[lane] = ghi;
   s_lo[lane] = glo;
@@ -110,7 +111,7 @@ __global__ __launch_bounds__(kThreads) void prepare_kernel(
       for (int r = 0; r < 4; ++r) {
         const int i = 16 * it + 4 * h + r;
         const float e = (hi_i[r] - hj) + (lo_i[r] - lj);
-        M[i * kMStride + j] = i > j ? a[r] * exp2f(e) * bj : 0.f;
+        M[i * kMStride + j] = i > j ? a[r] * pow2(e) * bj : 0.f;
       }
     }
   }
@@ -137,7 +138,7 @@ __global__ __launch_bounds__(kThreads) void prepare_kernel(
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const float x = (hi_i - hj[r]) + (lo_i - lj[r]);
-          p[r] = i >= 16 * jt + 4 * h + r ? p[r] * exp2f(x) : 0.f;
+          p[r] = i >= 16 * jt + 4 * h + r ? p[r] * pow2(x) : 0.f;
         }
         return p;
       };
@@ -192,54 +193,53 @@ __device__ __forceinline__ bool chain_block(int nblk, int pairs, int &pair, int 
 }
 
 // -------------------------------------------------------------------- chain
-// A workgroup runs 64 of the state's DV columns of one (sequence, head) over
-// its chunks.  Four chain waves own 16 columns each for the whole sequence, so
+// A workgroup runs BV of the state's DV columns of one (sequence, head) over
+// its chunks.  Its chain waves own 16 columns each for the whole sequence, so
 // the chain S -> K S -> U -> S of a column never leaves its wave: S is 4 DK /
 // 16 accumulator registers, and each product's result tiles are the next one's
-// operand.  Four helper waves (one more on each SIMD) do what the chain does
-// not wait for: they load the next chunk and make the output of this one.
-// Two barriers a chunk, A when the chunk's operands and S's terms are in LDS,
-// B when the chain has read all of them but K and has written U; what the next
-// chunk overwrites between B and the next A is only K's other buffer and those.
+// operand.  As many helper waves do what the chain does not wait for: they
+// load the next chunk and make the output of this one.  Two barriers a chunk:
+// A, when the chunk's operands and S's terms are in LDS, and B, when the chain
+// has read all of them into registers and has written U; the next chunk's
+// operands take their places between B and the next A.
 // STORE: for the backward, keeps the state before each chunk and U (two bf16
 // terms each) and makes no output.
-template <int DK, int DV, bool STORE> struct ChainLds {
-  static constexpr int kBufK = gdr::kTile<DK>;
-  static constexpr int kK = 0, kV = 2 * kBufK, kRec = kV + gdr::kTile<64>;
+template <int DK, int BV, bool STORE> struct ChainLds {
+  static constexpr int kK = 0, kV = gdr::kTile<DK>, kRec = kV + gdr::kTile<BV>;
   static constexpr int kQ = kRec + kRecFwd;                      // the rest: !STORE
   static constexpr int kS = kQ + gdr::kTile<DK>, kSWave = 2 * (DK / 32) * kFrag;
-  static constexpr int kU = kS + 4 * kSWave;
-  static constexpr int kBytes = STORE ? kQ : kU + 4 * 2 * kFrag;
+  static constexpr int kU = kS + BV / 16 * kSWave;
+  static constexpr int kBytes = STORE ? kQ : kU + BV / 16 * 2 * kFrag;
 };
 
-template <int DK, int DV, bool STORE>
-__global__ __launch_bounds__(2 * kThreads, 2) void chain_kernel(
+template <int DK, int DV, int BV, bool STORE>
+__global__ __launch_bounds__(8 * BV, 2) void chain_kernel(
     const __hip_bfloat16 *__restrict__ q, const __hip_bfloat16 *__restrict__ k,
     const __hip_bfloat16 *__restrict__ v, const float *__restrict__ S0, SeqTable tab, int N,
     int Hk, int Hv, const char *__restrict__ rec_base, __hip_bfloat16 *__restrict__ o,
     float *__restrict__ S_T, char *__restrict__ S_keep, char *__restrict__ U_keep) {
-  using L = ChainLds<DK, DV, STORE>;
-  constexpr int KS = DK / 32, MT = DK / 16, BV = 64;
+  using L = ChainLds<DK, BV, STORE>;
+  constexpr int KS = DK / 32, MT = DK / 16, kWaves = BV / 16, kHelp = 64 * kWaves;
   constexpr int kRec = STORE ? kRecBwd : kRecFwd;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   int pair, blk;
   if (!chain_block(DV / BV, N * Hv, pair, blk)) return;
   const int seq = tab.order[pair / Hv], hv = pair % Hv, hk = hv / (Hv / Hk);
-  const int wave = (threadIdx.x >> 6) & 3, lane = threadIdx.x & 63, m = lane & 15, h = lane >> 4;
+  const int wave = (threadIdx.x >> 6) % kWaves, lane = threadIdx.x & 63, m = lane & 15, h = lane >> 4;
   const int len = tab.seq_len[seq], chunks = (len + C - 1) / C;
   const size_t row0 = tab.seq_start[seq];
   const size_t c0 = tab.chunk_off[seq];
   const int col = blk * BV + 16 * wave;  // of the head's DV
-  const char *V = lds + L::kV, *R = lds + L::kRec, *Q = lds + L::kQ;
+  const char *K = lds + L::kK, *V = lds + L::kV, *R = lds + L::kRec, *Q = lds + L::kQ;
   const float *gate = reinterpret_cast<const float *>(R + kRecGate);
   char *s_S = lds + L::kS + wave * L::kSWave + lane * 16;
   char *s_U = lds + L::kU + wave * 2 * kFrag + lane * 16;
 
-  if (threadIdx.x >= kThreads) {         // helper waves
-    const int t = threadIdx.x - kThreads;
-    Stage<DK> gk, gq;
-    Stage<BV> gv;
-    Linear<kRecFwd> gr;
+  if (threadIdx.x >= kHelp) {            // helper waves
+    const int t = threadIdx.x - kHelp;
+    Stage<DK, kHelp> gk, gq;
+    Stage<BV, kHelp> gv;
+    Linear<kRecFwd, kHelp> gr;
     auto fetch = [&](int c) {
       const int valid = min(C, len - c * C);
       const size_t row = row0 + (size_t)c * C;
@@ -248,16 +248,16 @@ __global__ __launch_bounds__(2 * kThreads, 2) void chain_kernel(
       gv.load(v + (row * Hv + hv) * DV + blk * BV, (size_t)Hv * DV, valid, t);
       gr.load(rec_base + ((c0 + c) * Hv + hv) * kRec, t);
     };
-    auto put = [&](int c, int buf) {
+    auto put = [&](int c) {
       const int valid = min(C, len - c * C);
-      gk.store(lds + L::kK + (buf & 1) * L::kBufK, valid, t);
+      gk.store(lds + L::kK, valid, t);
       if (!STORE) gq.store(lds + L::kQ, valid, t);
       gv.store(lds + L::kV, valid, t);
       gr.store(lds + L::kRec, t);
     };
     if (chunks > 0) {
       fetch(0);
-      put(0, 0);
+      put(0);
     }
     for (int c = 0; c < chunks; ++c) {
       lds_barrier();                     // A
@@ -295,7 +295,7 @@ __global__ __launch_bounds__(2 * kThreads, 2) void chain_kernel(
         }
       }
       lds_barrier();                     // B
-      put(next, c + 1);                  // before the stores, which loads' waits count too
+      put(next);                         // before the stores, which loads' waits count too
       if (!STORE) {
         // One term of P and of U: each is within 2^-9 of its value, and so is
         // the bf16 output itself.
@@ -341,8 +341,8 @@ __global__ __launch_bounds__(2 * kThreads, 2) void chain_kernel(
     gn = g[kGam * C + C - 1];
   };
   if (chunks > 0) fetch_gates(0);
+  __builtin_amdgcn_s_setprio(2);         // the chain before the helper on its SIMD
   for (int c = 0; c < chunks; ++c) {
-    const char *K = lds + L::kK + (c & 1) * L::kBufK;
     Split sf[KS];
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
@@ -431,7 +431,9 @@ __global__ __launch_bounds__(2 * kThreads, 2) void chain_kernel(
       *reinterpret_cast<bf8 *>(s_U) = join(round4(U[0]), round4(U[1]));
       *reinterpret_cast<bf8 *>(s_U + kFrag) = join(round4(U[2]), round4(U[3]));
     }
+    fence_schedule();
     lds_barrier();                       // B
+    fence_schedule();
 #pragma unroll
     for (int it = 0; it < 4; ++it) U[it] *= last[it];
     fetch_gates(min(c + 1, chunks - 1));
@@ -461,24 +463,40 @@ template <typename F> hipError_t allow_lds(F *f, int bytes) {
                              hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
-// prepare, then the chain; with STORE it keeps S and E and makes no output.
+template <int DK, int DV, int BV, bool STORE>
+hipError_t launch_chain(const GdrArgs &a, char *rec, char *S, char *U, hipStream_t st) {
+  constexpr int lds = ChainLds<DK, BV, STORE>::kBytes;
+  auto *kernel = chain_kernel<DK, DV, BV, STORE>;
+  if (hipError_t e = allow_lds(kernel, lds); e != hipSuccess) return e;
+  hipLaunchKernelGGL(kernel, dim3(chain_grid(a.N * a.Hv, DV / BV)), dim3(8 * BV), lds, st,
+                     static_cast<const __hip_bfloat16 *>(a.q),
+                     static_cast<const __hip_bfloat16 *>(a.k),
+                     static_cast<const __hip_bfloat16 *>(a.v), a.S0, a.tab, a.N, a.Hk, a.Hv, rec,
+                     static_cast<__hip_bfloat16 *>(a.o), a.S_T, S, U);
+  return hipGetLastError();
+}
+
+// Columns of a workgroup.  64 load a chunk's operands once for twice the
+// columns; 32 halve the LDS traffic of a compute unit, which bounds the chunk,
+// and pay where half the chip would stand idle.
+int chain_columns(int pairs, int dv) {
+  return (size_t)pairs * (dv / 64) <= 128 ? 32 : 64;
+}
+
+// prepare, then the chain; with STORE it keeps S and U and makes no output.
 template <int DK, int DV, bool STORE>
-hipError_t forward_typed(const GdrArgs &a, char *rec, char *S, char *E, hipStream_t st) {
+hipError_t forward_typed(const GdrArgs &a, char *rec, char *S, char *U, hipStream_t st) {
   const auto *q = static_cast<const __hip_bfloat16 *>(a.q);
   const auto *k = static_cast<const __hip_bfloat16 *>(a.k);
-  const auto *v = static_cast<const __hip_bfloat16 *>(a.v);
   if (a.n_chunks_ub > 0) {
     hipLaunchKernelGGL((prepare_kernel<DK, STORE>),
                        dim3((unsigned)(a.n_chunks_ub * ((a.Hv + 3) / 4))), dim3(kThreads), 0, st,
                        q, k, a.g, a.beta, a.tab, a.N, a.Hk, a.Hv, rec);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }
-  constexpr int lds = ChainLds<DK, DV, STORE>::kBytes;
-  if (hipError_t e = allow_lds(chain_kernel<DK, DV, STORE>, lds); e != hipSuccess) return e;
-  hipLaunchKernelGGL((chain_kernel<DK, DV, STORE>), dim3(chain_grid(a.N * a.Hv, DV / 64)),
-                     dim3(2 * kThreads), lds, st, q, k, v, a.S0, a.tab, a.N, a.Hk, a.Hv, rec,
-                     static_cast<__hip_bfloat16 *>(a.o), a.S_T, S, E);
-  return hipGetLastError();
+  return chain_columns(a.N * a.Hv, DV) == 64
+             ? launch_chain<DK, DV, 64, STORE>(a, rec, S, U, st)
+             : launch_chain<DK, DV, 32, STORE>(a, rec, S, U, st);
 }
 
 template <bool STORE>
