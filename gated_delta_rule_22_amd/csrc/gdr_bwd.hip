@@ -316,25 +316,24 @@ __global__ __launch_bounds__(2 * kThreads, 2) void reverse_kernel(
 }
 
 // ---------------------------------------------------------------- gradients
-// One workgroup per (chunk, query/key head); it goes over the group's value
-// heads one after another, so dQ and dK of a shared head are summed in
-// registers, in a fixed order.  Eight waves, two on each SIMD: wave (w, e) owns
-// tokens 16 w .. 16 w + 15 and half e of the key channels.  As rows i its
-// tokens need the tiles j <= w of the triangular products, as columns j the
-// tiles i >= w, five tiles for every wave; e = 0 makes those of dP, e = 1 those
-// of dA, and they are exchanged through LDS.  The states are loaded while the
-// products before them run, into the place of what those have read.  Results
-// have lane = token and 4 key channels a lane, so stores are 8 bytes and q.dq
-// needs two exchanges.
-constexpr int kGradThreads = 512;
+// One workgroup of 4 waves per (chunk, query/key head); it goes over the
+// group's value heads one after another, so dQ and dK of a shared head are
+// summed in registers, in a fixed order.  Wave w owns tokens 16 w .. 16 w + 15:
+// as rows i they need the tiles j <= w of the triangular products, as columns j
+// the tiles i >= w, five tiles for every wave.  Results have lane = token and 4
+// key channels a lane, so stores are 8 bytes and q.dq needs two exchanges.
+// Everything but k and q passes through one 40 KB window of LDS, 64 value
+// columns at a time: dO, U and F, then the state, then its gradient, each
+// loaded while the one before it is used.  So two workgroups fit a compute
+// unit, and one computes while the other waits for memory, which is the bound
+// (2.4 GB on the layer); and a wave keeps only 64 columns of its own rows in
+// registers.
 template <int DK, int DV> struct GradLds {
   static constexpr int kK = 0, kQ = kK + kTile<DK>, kGate = kQ + kTile<DK>;
-  static constexpr int kSum = kGate + kGateBytes, kX = kSum + 1024;
-  static constexpr int kD = kX, kU = kD + kTile<DV>, kF = kU + 4 * C * DV;
-  static constexpr int kEnd1 = kF + 4 * C * DV;
-  static constexpr int kTriX = kX + 4 * DK * DV;                 // 6 fragments a wave
-  static constexpr int kEnd2 = kTriX + 8 * 6 * kFrag;
-  static constexpr int kBytes = kEnd1 > kEnd2 ? kEnd1 : kEnd2;
+  static constexpr int kSum = kGate + kGateBytes, kX = kSum + 256 + 64;
+  static constexpr int kD = kX, kU = kD + kTile<64>, kF = kU + 16 * kFrag;
+  static constexpr int kBytes = kF + 16 * kFrag;
+  static_assert(kX + 256 * DK <= kBytes, "a state's 64 columns fit the window");
 };
 
 __device__ __forceinline__ float sum4(f4 a) { return (a[0] + a[1]) + (a[2] + a[3]); }
@@ -343,8 +342,28 @@ __device__ __forceinline__ float over_quarters(float x) {
   return x + __shfl_xor(x, 32);
 }
 
+// SEGMENTS runs of BYTES from `step` bytes to `step` bytes, to LDS one behind
+// the other, mixed for transposed reads.
+template <int SEGMENTS, int BYTES> struct Segments {
+  static constexpr int kPer = BYTES / (kThreads * 16), kPasses = SEGMENTS * kPer;
+  static_assert(kPer * kThreads * 16 == BYTES, "whole passes");
+  using Lin = Linear<BYTES>;
+  u4 r[kPasses];
+  __device__ __forceinline__ void load(const char *p, size_t step, int t) {
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i)
+      r[i] = *reinterpret_cast<const u4 *>(p + (i / kPer) * step +
+                                           (t + (i % kPer) * kThreads) * 16);
+  }
+  __device__ __forceinline__ void store(char *dst, int t) const {
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i)
+      *reinterpret_cast<u4 *>(dst + (Lin::mixed(t) + i * kThreads) * 16) = Lin::halves(r[i], t);
+  }
+};
+
 template <int DK, int DV>
-__global__ __launch_bounds__(kGradThreads, 2) void grad_kernel(
+__global__ __launch_bounds__(kThreads, 2) void grad_kernel(
     const __hip_bfloat16 *__restrict__ q, const __hip_bfloat16 *__restrict__ k,
     const float *__restrict__ g, const float *__restrict__ beta,
     const __hip_bfloat16 *__restrict__ d_o, SeqTable tab, int N, int Hk, int Hv,
@@ -354,8 +373,7 @@ __global__ __launch_bounds__(kGradThreads, 2) void grad_kernel(
     __hip_bfloat16 *__restrict__ dk_out, __hip_bfloat16 *__restrict__ dv_out,
     float *__restrict__ dg, float *__restrict__ dbeta) {
   using L = GradLds<DK, DV>;
-  constexpr int MT = DK / 16, HT = MT / 2, NT = DV / 16, KV = DV / 32, NTH = kGradThreads;
-  constexpr int kPlane = DK * DV * 2;    // bytes of one term of a state
+  constexpr int MT = DK / 16, NT = DV / 16, kParts = DV / 64;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const int chunk = blockIdx.x / Hk, hk = blockIdx.x % Hk, rep = Hv / Hk;
   if (chunk >= tab.chunk_off[N]) return;
@@ -365,293 +383,293 @@ __global__ __launch_bounds__(kGradThreads, 2) void grad_kernel(
   const size_t row0 = (size_t)tab.seq_start[seq] + at;
   int t = threadIdx.x, lane = t & 63;
   const int m = lane & 15, h = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(t >> 6), w = wave & 3, e = wave >> 2;
+  const int w = __builtin_amdgcn_readfirstlane(t >> 6);
   const int tok = 16 * w + m;            // this lane's token
   const char *K = lds + L::kK, *Q = lds + L::kQ, *D = lds + L::kD;
   float *gate = reinterpret_cast<float *>(lds + L::kGate);
-  float *s_dG = reinterpret_cast<float *>(lds + L::kSum), *s_n = s_dG + 2 * C;
+  float *s_dG = reinterpret_cast<float *>(lds + L::kSum), *s_n = s_dG + C;
 
-  Stage<DK, NTH> gk, gq;
-  gk.load(k + (row0 * Hk + hk) * DK, (size_t)Hk * DK, valid, t);
-  gq.load(q + (row0 * Hk + hk) * DK, (size_t)Hk * DK, valid, t);
-  f4 dQ[HT], dK[HT];
+  {
+    Stage<DK> gk, gq;
+    gk.load(k + (row0 * Hk + hk) * DK, (size_t)Hk * DK, valid, t);
+    gq.load(q + (row0 * Hk + hk) * DK, (size_t)Hk * DK, valid, t);
+    gk.store(lds + L::kK, valid, t);
+    gq.store(lds + L::kQ, valid, t);
+  }
+  f4 dQ[MT], dK[MT];
 #pragma unroll
-  for (int i = 0; i < HT; ++i) dQ[i] = dK[i] = 0.f;
+  for (int i = 0; i < MT; ++i) dQ[i] = dK[i] = 0.f;
 
-  // Operand from pair order: lanes are rows of tile `row`, contracted over the
-  // 32 columns of pairs 2 ks and 2 ks + 1.
-  auto turned = [&](const char *base, int row, int rows, int ks) {
-    const char *a = base + ((row >> 1) * NT + 2 * ks) * kFrag;
-    const char *b = a + (rows / 2) * NT * kFrag;
+  // Operand from pair order in the window (4 pairs of 64 columns a row of
+  // pairs, `plane` bytes from hi to lo): lanes are rows of tile `row`,
+  // contracted over pairs 2 ks, 2 ks + 1.
+  auto turned = [&](const char *base, int row, int plane, int ks) {
+    const char *a = base + ((row >> 1) * 4 + 2 * ks) * kFrag, *b = a + plane;
     const int half = row & 1;
     return Split{join(frag_quad_t(a, half, lane), frag_quad_t(a + kFrag, half, lane)),
                  join(frag_quad_t(b, half, lane), frag_quad_t(b + kFrag, half, lane))};
   };
-  auto Uf = [&](int tile, int ks) { return turned(lds + L::kU, tile, 4, ks); };
-  auto Ff = [&](int tile, int ks) { return turned(lds + L::kF, tile, 4, ks); };
-  auto Sf = [&](int mt, int ks) { return turned(lds + L::kX, mt, MT, ks); };
+  auto Sf = [&](int mt, int ks) { return turned(lds + L::kX, mt, MT * 2 * kFrag, ks); };
 
   for (int u = 0; u < rep; ++u) {
     const int hv = hk * rep + u;
     const size_t ch = (size_t)chunk * Hv + hv;
     t = renewed(t);
     lane = t & 63;
+    Stage<64> gd;
+    Segments<4, 4 * kFrag> gu, gf;       // hi and lo of the two row pairs, 4 pairs of columns
+    auto fetch_rows = [&](int part) {
+      gd.load(d_o + (row0 * Hv + hv) * DV + 64 * part, (size_t)Hv * DV, valid, t);
+      gu.load(U_keep + ch * (4 * C * DV) + part * 4 * kFrag, NT * kFrag, t);
+      gf.load(F_keep + ch * (4 * C * DV) + part * 4 * kFrag, NT * kFrag, t);
+    };
+    auto put_rows = [&]() {
+      gd.store(lds + L::kD, valid, t);
+      gu.store(lds + L::kU, t);
+      gf.store(lds + L::kF, t);
+    };
+    fetch_rows(0);
     {
-      Stage<DV, NTH> a;
-      Linear<4 * C * DV, NTH> x, y;
-      a.load(d_o + (row0 * Hv + hv) * DV, (size_t)Hv * DV, valid, t);
-      x.load(U_keep + ch * (4 * C * DV), t);
-      y.load(F_keep + ch * (4 * C * DV), t);
       const float *rg = reinterpret_cast<const float *>(rec_base + ch * kRecBwd + kRecGate);
-      const float ga = rg[min(t, 5 * C - 1)];
-      if (u == 0) {
-        gk.store(lds + L::kK, valid, t);
-        gq.store(lds + L::kQ, valid, t);
-      }
-      a.store(lds + L::kD, valid, t);
-      x.store_mixed(lds + L::kU, t);
-      y.store_mixed(lds + L::kF, t);
-      if (t < 5 * C) gate[t] = ga;
+      const float ga = rg[t], gb = rg[kThreads + t % C];
+      gate[t] = ga;
+      if (t < C) gate[kThreads + t] = gb;
     }
+    put_rows();
     __syncthreads();
-    Linear<2 * kPlane, NTH> state;       // S, on its way while the first products run
-    state.load(S_keep + ch * (2 * kPlane), t);
-    bf8 d[KV];
-    Split uo[KV], f[KV];                 // own rows of dO, U, F
-#pragma unroll
-    for (int ks = 0; ks < KV; ++ks) {
-      d[ks] = rows_frag<DV>(D, 16 * w, 32 * ks, lane);
-      uo[ks] = Uf(w, ks);
-      f[ks] = Ff(w, ks);
-    }
+    Segments<MT, 4 * kFrag> state;       // hi and lo of the row pairs, 4 pairs of columns
+    auto fetch_state = [&](const char *base, int part) {
+      state.load(base + ch * (4 * DK * DV) + part * 4 * kFrag, NT * kFrag, t);
+    };
     const float ghi = gate[kGhi * C + tok], glo = gate[kGlo * C + tok];
     const float bet = gate[kBeta * C + tok], gam = gate[kGam * C + tok];
     const float last = gate[kLast * C + tok], gn = gate[kGam * C + C - 1];
+    const float own_beta = tok < valid ? beta[(row0 + tok) * Hv + hv] : 0.f;
 
-    // The triangular products as operands: x[lane i, over j] from tiles j <= w
-    // and y[lane j, over i] from tiles i >= w.
-    f4 x[4], y[4];
+    // Triangular products, five tiles: slot s is tile j = s of the row block
+    // [lane i, over j] while s <= w, then tile i = s - 1 of the column block
+    // [lane j, over i].  Both take the same operands in other places (a wave
+    // reads its own rows again rather than choosing between registers).
+    f4 pp[5], xx[5];                     // of dP and dA
 #pragma unroll
-    for (int jt = 0; jt < 4; ++jt) {
-      fence_schedule();                  // one tile's operands at a time in registers
-      x[jt] = 0.f;
-      if (jt <= w) {
-        f4 a = 0.f, b = 0.f;
-        Split z[KV];
+    for (int s = 0; s < 5; ++s) pp[s] = xx[s] = 0.f;
+    float dG = 0.f, ws = 0.f, dot = 0.f, db = 0.f;
 #pragma unroll
-        for (int ks = 0; ks < KV; ++ks) z[ks] = Uf(jt, ks);
-        if (e == 0)
-#pragma unroll
-          for (int ks = 0; ks < KV; ++ks) {
-            a = mfma(z[ks].hi, d[ks], a);
-            b = mfma(z[ks].lo, d[ks], b);
-          }
-        else
-#pragma unroll
-          for (int ks = 0; ks < KV; ++ks) {
-            a = mfma(z[ks].hi, f[ks].hi, a);
-            b = mfma(z[ks].hi, f[ks].lo, mfma(z[ks].lo, f[ks].hi, b));
-          }
-        a += b;
-        const f4 hj = *reinterpret_cast<const f4 *>(gate + kGhi * C + 16 * jt + 4 * h);
-        const f4 lj = *reinterpret_cast<const f4 *>(gate + kGlo * C + 16 * jt + 4 * h);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float z2 = a[r] * pow2((ghi - hj[r]) + (glo - lj[r]));
-          const int j = 16 * jt + 4 * h + r;
-          x[jt][r] = e == 0 ? (tok >= j ? z2 : 0.f) : (tok > j ? -z2 : 0.f);
-        }
+    for (int part = 0; part < kParts; ++part) {
+      if (part) {
+        __syncthreads();                 // the window has been read
+        put_rows();
+        __syncthreads();
       }
-    }
+      fetch_state(S_keep, part);
 #pragma unroll
-    for (int it = 0; it < 4; ++it) {
-      fence_schedule();
-      y[it] = 0.f;
-      if (it >= w) {
+      for (int s = 0; s < 5; ++s) {
+        fence_schedule();                // one tile's operands at a time in registers
+        lane = renewed(lane);
+        const bool rows = s <= w;
+        const int tile = rows ? s : s - 1;
+        const char *zb = lds + (rows ? L::kU : L::kF), *wb = lds + (rows ? L::kF : L::kU);
         f4 a = 0.f, b = 0.f;
-        if (e == 0) {
-          bf8 z[KV];
 #pragma unroll
-          for (int ks = 0; ks < KV; ++ks) z[ks] = rows_frag<DV>(D, 16 * it, 32 * ks, lane);
-#pragma unroll
-          for (int ks = 0; ks < KV; ++ks) {
-            a = mfma(z[ks], uo[ks].hi, a);
-            b = mfma(z[ks], uo[ks].lo, b);
-          }
-        } else {
-          Split z[KV];
-#pragma unroll
-          for (int ks = 0; ks < KV; ++ks) z[ks] = Ff(it, ks);
-#pragma unroll
-          for (int ks = 0; ks < KV; ++ks) {
-            a = mfma(z[ks].hi, uo[ks].hi, a);
-            b = mfma(z[ks].hi, uo[ks].lo, mfma(z[ks].lo, uo[ks].hi, b));
+        for (int c = 0; c < 2; ++c) {
+          const Split z = turned(zb, tile, 8 * kFrag, c), v = turned(wb, w, 8 * kFrag, c);
+          const bf8 y = rows_frag<64>(D, 16 * (rows ? w : tile), 32 * c, lane);
+          xx[s] = mfma(z.hi, v.hi, xx[s]);
+          a = mfma(z.lo, v.hi, a);
+          xx[s] = mfma(z.hi, v.lo, xx[s]);
+          if (rows) {
+            pp[s] = mfma(z.hi, y, pp[s]);
+            b = mfma(z.lo, y, b);
+          } else {
+            pp[s] = mfma(y, v.hi, pp[s]);
+            b = mfma(y, v.lo, b);
           }
         }
-        a += b;
-        const f4 hi = *reinterpret_cast<const f4 *>(gate + kGhi * C + 16 * it + 4 * h);
-        const f4 li = *reinterpret_cast<const f4 *>(gate + kGlo * C + 16 * it + 4 * h);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float z2 = a[r] * pow2((hi[r] - ghi) + (li[r] - glo));
-          const int i = 16 * it + 4 * h + r;
-          y[it][r] = e == 0 ? (i >= tok ? z2 : 0.f) : (i > tok ? -z2 : 0.f);
-        }
+        xx[s] += a;
+        pp[s] += b;
+        computed(xx[s]);
+        computed(pp[s]);
       }
-    }
-    // dV and dbeta from the wave's own rows, half of the channels each.
-    {
-      float s = 0.f;
-      const float own = tok < valid ? beta[(row0 + tok) * Hv + hv] : 0.f;
-      const float back = own / bet;      // 1, or below 1 where beta was raised
-      __hip_bfloat16 *o = dv_out + ((row0 + tok) * Hv + hv) * DV;
-      auto part = [&](const Split &z, int half) {
-        const bf4 a = half ? __builtin_shufflevector(z.hi, z.hi, 4, 5, 6, 7)
-                           : __builtin_shufflevector(z.hi, z.hi, 0, 1, 2, 3);
-        const bf4 b = half ? __builtin_shufflevector(z.lo, z.lo, 4, 5, 6, 7)
-                           : __builtin_shufflevector(z.lo, z.lo, 0, 1, 2, 3);
-        return widen4(a) + widen4(b);
-      };
-#pragma unroll
-      for (int ks = 0; ks < KV; ++ks)
-        if ((ks & 1) == e)
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const f4 z = part(f[ks], half);
-            s += sum4(z * part(uo[ks], half));
-            if (tok < valid)
-              *reinterpret_cast<bf4 *>(o + 32 * ks + 16 * half + 4 * h) = round4(z * back);
-          }
-      s = over_quarters(s);
-      if (h == 0) s_dG[e * C + tok] = s;
-    }
-    __syncthreads();                     // dO, U and F have been read
-    t = renewed(t);
-    lane = t & 63;
-    if (t < valid) dbeta[(row0 + t) * Hv + hv] =
-        (s_dG[t] + s_dG[C + t]) / (gate[kBeta * C + t] * gate[kBeta * C + t]);
-    state.store_mixed(lds + L::kX, t);
-    // x of tiles 0-1, then x of tiles 2-3 (w >= 2) or y of tiles 0-1 (w < 2,
-    // the others are zero), then y of tiles 2-3
-    char *ex = lds + L::kTriX + lane * 16;
-    {
-      char *p = ex + (w * 2 + e) * 6 * kFrag;
-      const Split x0 = split8(x[0], x[1]), y1 = split8(y[2], y[3]);
-      const Split z = w >= 2 ? split8(x[2], x[3]) : split8(y[0], y[1]);
-      const bf8 all[6] = {x0.hi, x0.lo, z.hi, z.lo, y1.hi, y1.lo};
-#pragma unroll
-      for (int i = 0; i < 6; ++i) *reinterpret_cast<bf8 *>(p + i * kFrag) = all[i];
-    }
-    __syncthreads();
-    state.load(dS_keep + ch * (2 * kPlane), t);
-    // read where they are used, not kept: 48 registers otherwise
-    const char *px = ex + w * 12 * kFrag;
-    auto tp = [&](int i) {
-      return Split{*reinterpret_cast<const bf8 *>(px + 2 * i * kFrag),
-                   *reinterpret_cast<const bf8 *>(px + (2 * i + 1) * kFrag)};
-    };
-    auto ta = [&](int i) {
-      return Split{*reinterpret_cast<const bf8 *>(px + (6 + 2 * i) * kFrag),
-                   *reinterpret_cast<const bf8 *>(px + (7 + 2 * i) * kFrag)};
-    };
-    float dG = 0.f;
-#pragma unroll
-    for (int i = 0; i < HT; ++i) {
       fence_schedule();
       lane = renewed(lane);
-      const int mt = e * HT + i;
-      f4 a = 0.f, b = 0.f, a2 = 0.f, b2 = 0.f;
-      Split s[KV];
+      bf8 d[2];
+      Split uo[2], f[2];                 // own rows of dO, U, F
 #pragma unroll
-      for (int ks = 0; ks < KV; ++ks) s[ks] = Sf(mt, ks);
-      const bf8 k0 = cols_frag<DK>(K, 0, 16 * mt, lane), k1 = cols_frag<DK>(K, 32, 16 * mt, lane);
-      const bf8 q0 = cols_frag<DK>(Q, 0, 16 * mt, lane), q1 = cols_frag<DK>(Q, 32, 16 * mt, lane);
-      const int off = place_of<DK>(tok, 16 * mt + 4 * h);
-      const f4 qv = widen4(*reinterpret_cast<const bf4 *>(Q + off));
-      const f4 kv = widen4(*reinterpret_cast<const bf4 *>(K + off));
-#pragma unroll
-      for (int ks = 0; ks < KV; ++ks) {
-        a = mfma(s[ks].hi, d[ks], a);
-        b = mfma(s[ks].hi, f[ks].hi, b);
-        a2 = mfma(s[ks].lo, d[ks], a2);
-        b2 = mfma(s[ks].lo, f[ks].hi, b2);
-        b = mfma(s[ks].hi, f[ks].lo, b);
+      for (int c = 0; c < 2; ++c) {
+        d[c] = rows_frag<64>(D, 16 * w, 32 * c, lane);
+        uo[c] = turned(lds + L::kU, w, 8 * kFrag, c);
+        f[c] = turned(lds + L::kF, w, 8 * kFrag, c);
       }
-      a = (a + a2) * gam;
-      b = (b + b2) * -gam;
-      a = dot2(k0, tp(0), a);
-      b = dot2(k0, ta(0), b);
-      f4 c = dot2(q1, tp(2), f4(0.f));
-      c = dot2(k1, ta(2), c);
-      if (w >= 2) {
-        a = dot2(k1, tp(1), a);
-        b = dot2(k1, ta(1), b);
-      } else {
-        c = dot2(q0, tp(1), c);
-        c = dot2(k0, ta(1), c);
-      }
-      dG += sum4(qv * a) + sum4(kv * (b - c));
-      dQ[i] += a;
-      dK[i] += b + c;
-    }
-    // <S, dS'>, then dS' in place of S.
-    float dot = 0.f;
-    {
-      constexpr int kHalf = kPlane / (NTH * 16);
+      {
+        // dV, and F.U for dbeta
+        const float back = own_beta / bet;   // 1, or below 1 where beta was raised
+        __hip_bfloat16 *o = dv_out + ((row0 + tok) * Hv + hv) * DV + 64 * part;
+        auto whole = [&](const Split &z, int half) {
+          const bf4 a = half ? __builtin_shufflevector(z.hi, z.hi, 4, 5, 6, 7)
+                             : __builtin_shufflevector(z.hi, z.hi, 0, 1, 2, 3);
+          const bf4 b = half ? __builtin_shufflevector(z.lo, z.lo, 4, 5, 6, 7)
+                             : __builtin_shufflevector(z.lo, z.lo, 0, 1, 2, 3);
+          return widen4(a) + widen4(b);
+        };
 #pragma unroll
-      for (int i = 0; i < kHalf; ++i) {
-        using Lin = Linear<2 * kPlane, NTH>;
-        const char *p = lds + L::kX + (Lin::mixed(t) + i * NTH) * 16;
-        const u4 z = Lin::halves(state.r[i], t), v = Lin::halves(state.r[i + kHalf], t);
-        const u4 a = *reinterpret_cast<const u4 *>(p), b = *reinterpret_cast<const u4 *>(p + kPlane);
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const f4 z = whole(f[c], half);
+            db += sum4(z * whole(uo[c], half));
+            computed(db);
+            if (tok < valid)
+              *reinterpret_cast<bf4 *>(o + 32 * c + 16 * half + 4 * h) = round4(z * back);
+          }
+      }
+      __syncthreads();
+      t = renewed(t);
+      lane = t & 63;
+      state.store(lds + L::kX, t);
+      __syncthreads();
+      fetch_state(dS_keep, part);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        fence_schedule();
+        lane = renewed(lane);
+        f4 a = 0.f, b = 0.f, a2 = 0.f, b2 = 0.f;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const Split s = Sf(i, c);
+          a = mfma(s.hi, d[c], a);
+          b = mfma(s.hi, f[c].hi, b);
+          a2 = mfma(s.lo, d[c], a2);
+          b2 = mfma(s.lo, f[c].hi, b2);
+          b = mfma(s.hi, f[c].lo, b);
+        }
+        const int off = place_of<DK>(16 * w + (lane & 15), 16 * i + 4 * (lane >> 4));
+        const f4 qv = widen4(*reinterpret_cast<const bf4 *>(Q + off));
+        const f4 kv = widen4(*reinterpret_cast<const bf4 *>(K + off));
+        a = (a + a2) * gam;
+        b = (b + b2) * -gam;
+        dG += sum4(qv * a) + sum4(kv * b);
+        dQ[i] += a;
+        dK[i] += b;
+        computed(dQ[i]);
+        computed(dK[i]);
+        computed(dG);
+      }
+      // <S, dS'>, then dS' in place of S.
+      t = renewed(t);
+      lane = t & 63;
+      using St = Segments<MT, 4 * kFrag>;
+      constexpr int kLo = St::kPasses / 2;
+#pragma unroll
+      for (int i = 0; i < kLo; ++i) {
+        const char *p = lds + L::kX + (St::Lin::mixed(t) + i * kThreads) * 16;
+        const u4 z = St::Lin::halves(state.r[i], t), v = St::Lin::halves(state.r[i + kLo], t);
+        const u4 a = *reinterpret_cast<const u4 *>(p);
+        const u4 b = *reinterpret_cast<const u4 *>(p + kLo * kThreads * 16);
         auto low = [](uint32_t q) { return __uint_as_float(q << 16); };
         auto high = [](uint32_t q) { return __uint_as_float(q & 0xFFFF0000u); };
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           dot += (low(a[j]) + low(b[j])) * (low(z[j]) + low(v[j])) +
                  (high(a[j]) + high(b[j])) * (high(z[j]) + high(v[j]));
+        computed(dot);
+      }
+      __syncthreads();
+      state.store(lds + L::kX, t);
+      __syncthreads();
+      if (part + 1 < kParts) fetch_rows(part + 1);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        fence_schedule();
+        lane = renewed(lane);
+        f4 c0 = 0.f, c1 = 0.f;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const Split s = Sf(i, c);
+          c0 = mfma(s.hi, uo[c].hi, c0);
+          c1 = mfma(s.lo, uo[c].hi, c1);
+          c0 = mfma(s.hi, uo[c].lo, c0);
+        }
+        c0 = (c0 + c1) * last;
+        const int off = place_of<DK>(16 * w + (lane & 15), 16 * i + 4 * (lane >> 4));
+        ws += sum4(c0 * widen4(*reinterpret_cast<const bf4 *>(K + off)));
+        dK[i] += c0;
+        computed(dK[i]);
+        computed(ws);
       }
     }
-    __syncthreads();
-    t = renewed(t);
-    lane = t & 63;
-    state.store_mixed(lds + L::kX, t);
-    __syncthreads();
-    float ws = 0.f;
+    db = over_quarters(db);
+    if (h == 0 && tok < valid) dbeta[(row0 + tok) * Hv + hv] = db / (bet * bet);
+
+    // Decays and masks, then dQ and dK from the triangular products.
 #pragma unroll
-    for (int i = 0; i < HT; ++i) {
-      fence_schedule();
-      lane = renewed(lane);
-      const int mt = e * HT + i;
-      f4 c = 0.f, c2 = 0.f;
-      Split s[KV];
+    for (int s = 0; s < 5; ++s) {
+      const bool rows = s <= w;
+      const int first = 16 * (rows ? s : s - 1) + 4 * h;
+      const f4 go = *reinterpret_cast<const f4 *>(gate + kGhi * C + first);
+      const f4 lo = *reinterpret_cast<const f4 *>(gate + kGlo * C + first);
+      const float sign = rows ? 1.f : -1.f;
 #pragma unroll
-      for (int ks = 0; ks < KV; ++ks) s[ks] = Sf(mt, ks);
-#pragma unroll
-      for (int ks = 0; ks < KV; ++ks) {
-        c = mfma(s[ks].hi, uo[ks].hi, c);
-        c2 = mfma(s[ks].lo, uo[ks].hi, c2);
-        c = mfma(s[ks].hi, uo[ks].lo, c);
+      for (int r = 0; r < 4; ++r) {
+        const float z = pow2(sign * ((ghi - go[r]) + (glo - lo[r])));
+        const int behind = rows ? tok - first - r : first + r - tok;   // i - j
+        pp[s][r] = behind >= 0 ? pp[s][r] * z : 0.f;
+        xx[s][r] = behind > 0 ? -xx[s][r] * z : 0.f;
       }
-      c = (c + c2) * last;
-      ws += sum4(c * widen4(*reinterpret_cast<const bf4 *>(K + place_of<DK>(tok, 16 * mt + 4 * h))));
-      dK[i] += c;
+    }
+    {
+      // As operands: row block over tiles 0-1; over tiles 2-3 for w >= 2 (zero
+      // for w < 2) or column block over tiles 0-1 for w < 2 (zero for w >= 2);
+      // column block over tiles 2-3.
+      const f4 none = 0.f;
+      auto first = [&](const f4 *x) { return split8(x[0], w == 0 ? none : x[1]); };
+      auto middle = [&](const f4 *x) {
+        return split8(w == 0 ? x[1] : w == 1 ? none : x[2], w < 2 ? x[2] : w == 2 ? none : x[3]);
+      };
+      auto behind = [&](const f4 *x) { return split8(w == 3 ? none : x[3], x[4]); };
+      const Split p0 = first(pp), p1 = middle(pp), p2 = behind(pp);
+      const Split a0 = first(xx), a1 = middle(xx), a2 = behind(xx);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        fence_schedule();
+        lane = renewed(lane);
+        const bf8 k0 = cols_frag<DK>(K, 0, 16 * i, lane), k1 = cols_frag<DK>(K, 32, 16 * i, lane);
+        const bf8 q1 = cols_frag<DK>(Q, 32, 16 * i, lane);
+        // with the middle operands: K of tokens 32 .. for the row block, Q and
+        // K of tokens 0 .. for the column block
+        const bf8 m1 = cols_frag<DK>(w >= 2 ? K : Q, w >= 2 ? 32 : 0, 16 * i, lane);
+        const bf8 m2 = cols_frag<DK>(K, w >= 2 ? 32 : 0, 16 * i, lane);
+        const int off = place_of<DK>(16 * w + (lane & 15), 16 * i + 4 * (lane >> 4));
+        const f4 qv = widen4(*reinterpret_cast<const bf4 *>(Q + off));
+        const f4 kv = widen4(*reinterpret_cast<const bf4 *>(K + off));
+        f4 a = dot2(k0, p0, f4(0.f)), b = dot2(k0, a0, f4(0.f));
+        f4 c = dot2(k1, a2, dot2(q1, p2, f4(0.f)));
+        const f4 r1 = dot2(m1, p1, f4(0.f)), r2 = dot2(m2, a1, f4(0.f));
+        a += w >= 2 ? r1 : none;
+        b += w >= 2 ? r2 : none;
+        c += w >= 2 ? none : r1 + r2;
+        dG += sum4(qv * a) + sum4(kv * (b - c));
+        dQ[i] += a;
+        dK[i] += b + c;
+        computed(dQ[i]);
+        computed(dK[i]);
+        computed(dG);
+      }
     }
     dG = over_quarters(dG - ws);
-    if (h == 0) s_dG[e * C + tok] = dG;
+    if (h == 0) s_dG[tok] = dG;
     // sum_j w_j + gam_n <S, dS'> over the workgroup
     float n = ws + gn * dot;
     for (int o = 32; o > 0; o >>= 1) n += __shfl_xor(n, o);
-    if (lane == 0) s_n[wave] = n;
+    if (lane == 0) s_n[w] = n;
     __syncthreads();
-    if (wave == 0) {
-      float z = s_dG[lane] + s_dG[C + lane];
+    if (w == 0) {
+      float z = s_dG[lane];
 #pragma unroll
       for (int o = 1; o < 64; o <<= 1) {
         const float v = __shfl_down(z, o);
         if (lane + o < 64) z += v;
       }
-      z += ((s_n[0] + s_n[1]) + (s_n[2] + s_n[3])) + ((s_n[4] + s_n[5]) + (s_n[6] + s_n[7]));
+      z += (s_n[0] + s_n[1]) + (s_n[2] + s_n[3]);
       if (lane < valid) {
         const size_t gi = (row0 + lane) * Hv + hv;
         dg[gi] = g[gi] < (float)kGateFloor ? 0.f : z;   // a floored gate is constant
@@ -660,9 +678,9 @@ __global__ __launch_bounds__(kGradThreads, 2) void grad_kernel(
     if (u + 1 < rep) __syncthreads();
   }
   if (tok < valid) {
-    const size_t o = ((row0 + tok) * Hk + hk) * DK + 16 * e * HT + 4 * h;
+    const size_t o = ((row0 + tok) * Hk + hk) * DK + 4 * h;
 #pragma unroll
-    for (int i = 0; i < HT; ++i) {
+    for (int i = 0; i < MT; ++i) {
       *reinterpret_cast<bf4 *>(dq + o + 16 * i) = round4(dQ[i]);
       *reinterpret_cast<bf4 *>(dk_out + o + 16 * i) = round4(dK[i]);
     }
@@ -693,7 +711,7 @@ template <int DK, int DV> hipError_t backward_typed(const GdrBwdArgs &a, hipStre
   e = hipFuncSetAttribute(reinterpret_cast<const void *>(gr),
                           hipFuncAttributeMaxDynamicSharedMemorySize, gl);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(gr, dim3((unsigned)(f.n_chunks_ub * f.Hk)), dim3(kGradThreads), gl, st, q, k, f.g,
+  hipLaunchKernelGGL(gr, dim3((unsigned)(f.n_chunks_ub * f.Hk)), dim3(kThreads), gl, st, q, k, f.g,
                      f.beta, d_o, f.tab, f.N, f.Hk, f.Hv, rec, S, U, dS, F,
                      static_cast<__hip_bfloat16 *>(a.dq), static_cast<__hip_bfloat16 *>(a.dk),
                      static_cast<__hip_bfloat16 *>(a.dv), a.dg, a.dbeta);

@@ -243,6 +243,11 @@ __device__ __forceinline__ void lds_barrier() {
 // 100 cycles) per product.
 __device__ __forceinline__ void fence_schedule() { __builtin_amdgcn_sched_barrier(0); }
 
+// Has the value computed by here: arithmetic alone is not held by
+// fence_schedule, and one tile's operands would wait in registers for another's.
+__device__ __forceinline__ void computed(f4 &x) { asm volatile("" : "+v"(x)); }
+__device__ __forceinline__ void computed(float &x) { asm volatile("" : "+v"(x)); }
+
 // The same number, as a new one: addresses made from it are computed where
 // they are used instead of being kept in registers from the kernel's start.
 __device__ __forceinline__ int renewed(int x) {
