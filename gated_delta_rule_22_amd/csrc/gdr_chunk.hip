@@ -23,10 +23,9 @@ namespace {
 
 // ------------------------------------------------------------------ prepare
 // One wave per (chunk, value head), four to a workgroup, no barriers.  The
-// 64 x 64 unit lower triangular inverse is taken by forward substitution in
-// fp32, one column a lane: row i of Ah diag(beta) is read from LDS at one
-// address for all lanes (a broadcast) and the column's earlier entries are
-// registers.
+// 64 x 64 unit lower triangular inverse is taken in fp32: its 16 x 16 diagonal
+// blocks by substitution, what is below them by matrix products (substitution
+// over all 64 rows takes 2016 steps a wave and as many LDS broadcasts).
 constexpr int kMStride = C + 4;          // floats; keeps rows 16-byte aligned
 
 template <int DK, bool BWD>
@@ -152,23 +151,71 @@ __global__ __launch_bounds__(kThreads) void prepare_kernel(
   }
   wave_sync();
 
-  // Column `lane` of the inverse.
-  float x[C];
+  // The inverse, in place.  Diagonal 16 x 16 blocks by forward substitution,
+  // one column of one block a lane.
+  {
+    float x[16];
+    float *D = M + (16 * h) * kMStride + 16 * h;
 #pragma unroll
-  for (int i = 0; i < C; ++i) {
-    f4 s = 0.f;
+    for (int i = 0; i < 16; ++i) {
+      f4 s = 0.f;
 #pragma unroll
-    for (int j = 0; j < i; j += 4) {
-      const f4 a = *reinterpret_cast<const f4 *>(M + i * kMStride + j);
+      for (int j = 0; j < i; j += 4) {
+        const f4 a = *reinterpret_cast<const f4 *>(D + i * kMStride + j);
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (j + e < i) s[e] += a[e] * x[j + e];
+        for (int e = 0; e < 4; ++e)
+          if (j + e < i) s[e] += a[e] * x[j + e];
+      }
+      x[i] = (i == m ? 1.f : 0.f) - ((s[0] + s[1]) + (s[2] + s[3]));
     }
-    x[i] = (i == lane ? 1.f : 0.f) - ((s[0] + s[1]) + (s[2] + s[3]));
-  }
-  wave_sync();
+    wave_sync();
 #pragma unroll
-  for (int i = 0; i < C; ++i) M[i * kMStride + lane] = x[i];
+    for (int i = 0; i < 16; ++i) D[i * kMStride + m] = x[i];
+    wave_sync();
+  }
+  // The blocks below them, T21 = -T22 (A21 T11), on fp32 matrix products.  A
+  // product's left operand is read as rows; its right one has the layout of a
+  // result (column m, rows 4h ..), so products follow each other in registers.
+  auto block = [&](int i, int j) {
+    return *reinterpret_cast<const f4 *>(M + (16 * i + m) * kMStride + 16 * j + 4 * h);
+  };
+  auto times = [](f4 a, f4 b, f4 c) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[r], b[r], c, 0, 0, 0);
+    return c;
+  };
+  auto keep = [&](int i, int j, f4 x) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) M[(16 * i + 4 * h + r) * kMStride + 16 * j + m] = x[r];
+  };
+  {
+    f4 t[4];                             // diagonal blocks as right operands
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) t[d][r] = M[(16 * d + 4 * h + r) * kMStride + 16 * d + m];
+    const f4 none = 0.f;
+    const f4 t10 = -times(block(1, 1), times(block(1, 0), t[0], none), none);
+    const f4 t32 = -times(block(3, 3), times(block(3, 2), t[2], none), none);
+    wave_sync();
+    keep(1, 0, t10);
+    keep(3, 2, t32);
+    wave_sync();
+    f4 x[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const f4 a0 = block(2 + i, 0), a1 = block(2 + i, 1);
+      x[i][0] = times(a1, t10, times(a0, t[0], none));
+      x[i][1] = times(a1, t[1], none);
+    }
+    const f4 b22 = block(2, 2), b32 = block(3, 2), b33 = block(3, 3);
+    wave_sync();
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      keep(2, j, -times(b22, x[0][j], none));
+      keep(3, j, -times(b33, x[1][j], times(b32, x[0][j], none)));
+    }
+  }
   wave_sync();
 #pragma unroll
   for (int it = 0; it < 4; ++it)
@@ -176,8 +223,10 @@ __global__ __launch_bounds__(kThreads) void prepare_kernel(
     for (int ks = 0; ks <= it / 2; ++ks) {
       const float *p = M + (16 * it + m) * kMStride + 32 * ks + 4 * h;
       const float bi = s_b[16 * it + m];
-      const Split s = split8(*reinterpret_cast<const f4 *>(p) * bi,
-                             *reinterpret_cast<const f4 *>(p + 16) * bi);
+      // the tile right of an even diagonal one lies above the diagonal
+      f4 right = 0.f;
+      if (2 * ks + 1 <= it) right = *reinterpret_cast<const f4 *>(p + 16) * bi;
+      const Split s = split8(*reinterpret_cast<const f4 *>(p) * bi, right);
       *reinterpret_cast<bf8 *>(rec + kRecTh + frag_at(it, ks) + lane * 16) = s.hi;
       *reinterpret_cast<bf8 *>(rec + kRecTl + frag_at(it, ks) + lane * 16) = s.lo;
     }
