@@ -102,11 +102,12 @@ extern "C" int gdr_forward(const void *q, const void *k, const void *v, const fl
   if (int s = debug_prologue(cu_seqlens, N, T, workspace, L.total, st)) return s;
   GdrArgs a{};
   a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.S0 = S0;
-  a.tab = seq_table(workspace, N);
+  a.seqs = Seqs{seq_table(workspace, N), packed ? -1 : T};
   a.n_chunks_ub = L.n_chunks;
   a.N = N; a.Hk = Hk; a.Hv = Hv; a.dk = dk; a.dv = dv;
   a.o = o; a.S_T = S_T;
-  if (launch_seq_table(cu_seqlens, B, T, N, a.tab, st) != hipSuccess) return CKDA_ERR_LAUNCH;
+  if (packed && launch_seq_table(cu_seqlens, B, T, N, a.seqs.tab, st) != hipSuccess)
+    return CKDA_ERR_LAUNCH;
   const hipError_t r = in_dtype == CKDA_BF16
                            ? launch_gdr_forward(a, static_cast<char *>(workspace) + L.rec, st)
                            : launch_gdr_token(a, in_dtype, st);
@@ -219,12 +220,13 @@ extern "C" int gdr_backward(const void *q, const void *k, const void *v, const f
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (int s = debug_prologue(cu_seqlens, N, T, workspace, L.total, st)) return s;
   char *w = static_cast<char *>(workspace);
-  const SeqTable tab = seq_table(workspace, N);
-  if (launch_seq_table(cu_seqlens, B, T, N, tab, st) != hipSuccess) return CKDA_ERR_LAUNCH;
+  const Seqs seqs{seq_table(workspace, N), packed ? -1 : T};
+  if (packed && launch_seq_table(cu_seqlens, B, T, N, seqs.tab, st) != hipSuccess)
+    return CKDA_ERR_LAUNCH;
   if (in_dtype == CKDA_BF16) {
     GdrBwdArgs a{};
     a.fwd.q = q; a.fwd.k = k; a.fwd.v = v; a.fwd.g = g; a.fwd.beta = beta; a.fwd.S0 = S0;
-    a.fwd.tab = tab; a.fwd.n_chunks_ub = L.n_chunks;
+    a.fwd.seqs = seqs; a.fwd.n_chunks_ub = L.n_chunks;
     a.fwd.N = N; a.fwd.Hk = Hk; a.fwd.Hv = Hv; a.fwd.dk = dk; a.fwd.dv = dv;
     a.d_o = d_o; a.dS_T = dS_T;
     a.rec = w + L.rec; a.S = w + L.S; a.U = w + L.U; a.dS = w + L.dS; a.F = w + L.F;
@@ -244,7 +246,7 @@ extern "C" int gdr_backward(const void *q, const void *k, const void *v, const f
                            L.total - L.inner, stream))
     return s;
   if (rows > 0 &&
-      launch_gdr_collect(x[3], x[4], x[5], g, tab, N, rows, Hk, Hv, dk, static_cast<float *>(dq),
+      launch_gdr_collect(x[3], x[4], x[5], g, seqs, N, rows, Hk, Hv, dk, static_cast<float *>(dq),
                          static_cast<float *>(d_k), dg, st) != hipSuccess)
     return CKDA_ERR_LAUNCH;
   return CKDA_OK;

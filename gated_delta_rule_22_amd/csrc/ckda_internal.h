@@ -39,6 +39,30 @@ struct SeqTable {
     int32_t *order;
 };
 
+// The sequences of a call: the table, or for uniform rows of T tokens (T >= 0)
+// plain arithmetic, which spares the table's launch.
+struct Seqs {
+    SeqTable tab;
+    int T;                               // -1: packed
+    __device__ int start(int n) const { return T >= 0 ? n * T : tab.seq_start[n]; }
+    __device__ int len(int n) const { return T >= 0 ? T : tab.seq_len[n]; }
+    __device__ int first_chunk(int n) const {      // n = N: the number of chunks
+        return T >= 0 ? n * ((T + kChunk - 1) / kChunk) : tab.chunk_off[n];
+    }
+    __device__ int order(int r) const { return T >= 0 ? r : tab.order[r]; }
+    // Sequence of a flat chunk index below first_chunk(N).
+    __device__ int of_chunk(int chunk, int N) const {
+        if (T >= 0) return chunk / ((T + kChunk - 1) / kChunk);
+        int lo = 0, hi = N;              // first_chunk(lo) <= chunk < first_chunk(hi)
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (tab.chunk_off[mid] <= chunk) lo = mid;
+            else hi = mid;
+        }
+        return lo;
+    }
+};
+
 // Workspace layout for a forward call (host-side arithmetic only).
 struct FwdLayout {
     size_t table_bytes;      // the SeqTable arrays, 256-byte aligned
@@ -106,7 +130,7 @@ hipError_t launch_bwd_f64(const void *q, const void *k, const void *v, const flo
 struct GdrArgs {
     const void *q, *k, *v;
     const float *g, *beta, *S0;
-    SeqTable tab;
+    Seqs seqs;
     size_t n_chunks_ub;
     int N, Hk, Hv, dk, dv;
     void *o;
@@ -140,7 +164,7 @@ hipError_t launch_gdr_backward(const GdrBwdArgs &a, hipStream_t stream);
 hipError_t launch_gdr_expand(const float *q, const float *k, const float *g, size_t rows, int Hk,
                              int Hv, int dk, float *qx, float *kx, float *gx, hipStream_t stream);
 hipError_t launch_gdr_collect(const float *dqx, const float *dkx, const float *dgx,
-                              const float *g, SeqTable tab, int N, size_t rows, int Hk, int Hv,
+                              const float *g, Seqs seqs, int N, size_t rows, int Hk, int Hv,
                               int dk, float *dq, float *dk_out, float *dg, hipStream_t stream);
 
 // ---------------------------------------------------------------- norm and rotation

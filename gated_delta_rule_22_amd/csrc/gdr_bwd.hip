@@ -50,7 +50,7 @@ template <int DK> struct ReverseLds {
 template <int DK, int DV>
 __global__ __launch_bounds__(2 * kThreads, 2) void reverse_kernel(
     const __hip_bfloat16 *__restrict__ q, const __hip_bfloat16 *__restrict__ k,
-    const __hip_bfloat16 *__restrict__ d_o, const float *__restrict__ dS_T, SeqTable tab, int N,
+    const __hip_bfloat16 *__restrict__ d_o, const float *__restrict__ dS_T, Seqs seqs, int N,
     int Hk, int Hv, const char *__restrict__ rec_base, char *__restrict__ dS_keep,
     char *__restrict__ F_keep, float *__restrict__ dS0) {
   using L = ReverseLds<DK>;
@@ -58,11 +58,11 @@ __global__ __launch_bounds__(2 * kThreads, 2) void reverse_kernel(
   extern __shared__ __attribute__((aligned(16))) char lds[];
   int pair, blk;
   if (!chain_block(DV / BV, N * Hv, pair, blk)) return;
-  const int seq = tab.order[pair / Hv], hv = pair % Hv, hk = hv / (Hv / Hk);
+  const int seq = seqs.order(pair / Hv), hv = pair % Hv, hk = hv / (Hv / Hk);
   const int wave = (threadIdx.x >> 6) & 3, lane = threadIdx.x & 63, m = lane & 15, h = lane >> 4;
-  const int len = tab.seq_len[seq], chunks = (len + C - 1) / C;
-  const size_t row0 = tab.seq_start[seq];
-  const size_t c0 = tab.chunk_off[seq];
+  const int len = seqs.len(seq), chunks = (len + C - 1) / C;
+  const size_t row0 = seqs.start(seq);
+  const size_t c0 = seqs.first_chunk(seq);
   const int col = blk * BV + 16 * wave;
   const char *K = lds + L::kK, *T = lds + L::kT;
   char *tiles = lds + L::kTiles + wave * L::kWave + lane * 16;
@@ -366,7 +366,7 @@ template <int DK, int DV>
 __global__ __launch_bounds__(kThreads, 2) void grad_kernel(
     const __hip_bfloat16 *__restrict__ q, const __hip_bfloat16 *__restrict__ k,
     const float *__restrict__ g, const float *__restrict__ beta,
-    const __hip_bfloat16 *__restrict__ d_o, SeqTable tab, int N, int Hk, int Hv,
+    const __hip_bfloat16 *__restrict__ d_o, Seqs seqs, int N, int Hk, int Hv,
     const char *__restrict__ rec_base, const char *__restrict__ S_keep,
     const char *__restrict__ U_keep, const char *__restrict__ dS_keep,
     const char *__restrict__ F_keep, __hip_bfloat16 *__restrict__ dq,
@@ -376,11 +376,11 @@ __global__ __launch_bounds__(kThreads, 2) void grad_kernel(
   constexpr int MT = DK / 16, NT = DV / 16, kParts = DV / 64;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const int chunk = blockIdx.x / Hk, hk = blockIdx.x % Hk, rep = Hv / Hk;
-  if (chunk >= tab.chunk_off[N]) return;
-  const int seq = find_seq(tab, N, chunk);
-  const int at = (chunk - tab.chunk_off[seq]) * C;
-  const int valid = min(C, tab.seq_len[seq] - at);
-  const size_t row0 = (size_t)tab.seq_start[seq] + at;
+  if (chunk >= seqs.first_chunk(N)) return;
+  const int seq = seqs.of_chunk(chunk, N);
+  const int at = (chunk - seqs.first_chunk(seq)) * C;
+  const int valid = min(C, seqs.len(seq) - at);
+  const size_t row0 = (size_t)seqs.start(seq) + at;
   int t = threadIdx.x, lane = t & 63;
   const int m = lane & 15, h = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(t >> 6);
@@ -703,7 +703,7 @@ template <int DK, int DV> hipError_t backward_typed(const GdrBwdArgs &a, hipStre
   if (e != hipSuccess) return e;
   const unsigned pairs = (unsigned)((f.N * f.Hv + 7) / 8 * 8);
   hipLaunchKernelGGL(rev, dim3(pairs * (DV / 64)), dim3(2 * kThreads), lds, st, q, k, d_o, a.dS_T,
-                     f.tab, f.N, f.Hk, f.Hv, rec, dS, F, a.dS0);
+                     f.seqs, f.N, f.Hk, f.Hv, rec, dS, F, a.dS0);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   if (f.n_chunks_ub == 0) return hipSuccess;
   auto *gr = grad_kernel<DK, DV>;
@@ -712,7 +712,7 @@ template <int DK, int DV> hipError_t backward_typed(const GdrBwdArgs &a, hipStre
                           hipFuncAttributeMaxDynamicSharedMemorySize, gl);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(gr, dim3((unsigned)(f.n_chunks_ub * f.Hk)), dim3(kThreads), gl, st, q, k, f.g,
-                     f.beta, d_o, f.tab, f.N, f.Hk, f.Hv, rec, S, U, dS, F,
+                     f.beta, d_o, f.seqs, f.N, f.Hk, f.Hv, rec, S, U, dS, F,
                      static_cast<__hip_bfloat16 *>(a.dq), static_cast<__hip_bfloat16 *>(a.dk),
                      static_cast<__hip_bfloat16 *>(a.dv), a.dg, a.dbeta);
   return hipGetLastError();

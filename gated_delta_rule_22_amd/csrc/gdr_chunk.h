@@ -262,16 +262,5 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_wave_barrier();
 }
 
-// Sequence of a flat chunk index (the last whose first chunk is not behind it).
-__device__ __forceinline__ int find_seq(const SeqTable &tab, int N, int chunk) {
-  int lo = 0, hi = N;                    // chunk_off[lo] <= chunk < chunk_off[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (tab.chunk_off[mid] <= chunk) lo = mid;
-    else hi = mid;
-  }
-  return lo;
-}
-
 }  // namespace gdr
 }  // namespace ckda

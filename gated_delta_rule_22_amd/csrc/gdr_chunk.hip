@@ -31,7 +31,7 @@ constexpr int kMStride = C + 4;          // floats; keeps rows 16-byte aligned
 template <int DK, bool BWD>
 __global__ __launch_bounds__(kThreads) void prepare_kernel(
     const __hip_bfloat16 *__restrict__ q, const __hip_bfloat16 *__restrict__ k,
-    const float *__restrict__ g, const float *__restrict__ beta, SeqTable tab, int N, int Hk,
+    const float *__restrict__ g, const float *__restrict__ beta, Seqs seqs, int N, int Hk,
     int Hv, char *__restrict__ rec_base) {
   constexpr int KS = DK / 32;
   constexpr int kRec = BWD ? kRecBwd : kRecFwd;
@@ -41,11 +41,11 @@ __global__ __launch_bounds__(kThreads) void prepare_kernel(
   const int m = lane & 15, h = lane >> 4;
   const int per = (Hv + 3) / 4;
   const int chunk = blockIdx.x / per, hv = (blockIdx.x % per) * 4 + wave;
-  if (hv >= Hv || chunk >= tab.chunk_off[N]) return;   // waves share nothing
-  const int seq = find_seq(tab, N, chunk);
-  const int at = (chunk - tab.chunk_off[seq]) * C;
-  const int valid = min(C, tab.seq_len[seq] - at);
-  const size_t row0 = (size_t)tab.seq_start[seq] + at;
+  if (hv >= Hv || chunk >= seqs.first_chunk(N)) return;   // waves share nothing
+  const int seq = seqs.of_chunk(chunk, N);
+  const int at = (chunk - seqs.first_chunk(seq)) * C;
+  const int valid = min(C, seqs.len(seq) - at);
+  const size_t row0 = (size_t)seqs.start(seq) + at;
   const int hk = hv / (Hv / Hk);
   char *rec = rec_base + ((size_t)chunk * Hv + hv) * kRec;
   float *M = s_M[wave], *s_hi = s_g[wave][0], *s_lo = s_g[wave][1], *s_b = s_g[wave][2];
@@ -264,7 +264,7 @@ template <int DK, int BV, bool STORE> struct ChainLds {
 template <int DK, int DV, int BV, bool STORE>
 __global__ __launch_bounds__(8 * BV, 2) void chain_kernel(
     const __hip_bfloat16 *__restrict__ q, const __hip_bfloat16 *__restrict__ k,
-    const __hip_bfloat16 *__restrict__ v, const float *__restrict__ S0, SeqTable tab, int N,
+    const __hip_bfloat16 *__restrict__ v, const float *__restrict__ S0, Seqs seqs, int N,
     int Hk, int Hv, const char *__restrict__ rec_base, __hip_bfloat16 *__restrict__ o,
     float *__restrict__ S_T, char *__restrict__ S_keep, char *__restrict__ U_keep) {
   using L = ChainLds<DK, BV, STORE>;
@@ -273,11 +273,11 @@ __global__ __launch_bounds__(8 * BV, 2) void chain_kernel(
   extern __shared__ __attribute__((aligned(16))) char lds[];
   int pair, blk;
   if (!chain_block(DV / BV, N * Hv, pair, blk)) return;
-  const int seq = tab.order[pair / Hv], hv = pair % Hv, hk = hv / (Hv / Hk);
+  const int seq = seqs.order(pair / Hv), hv = pair % Hv, hk = hv / (Hv / Hk);
   const int wave = (threadIdx.x >> 6) % kWaves, lane = threadIdx.x & 63, m = lane & 15, h = lane >> 4;
-  const int len = tab.seq_len[seq], chunks = (len + C - 1) / C;
-  const size_t row0 = tab.seq_start[seq];
-  const size_t c0 = tab.chunk_off[seq];
+  const int len = seqs.len(seq), chunks = (len + C - 1) / C;
+  const size_t row0 = seqs.start(seq);
+  const size_t c0 = seqs.first_chunk(seq);
   const int col = blk * BV + 16 * wave;  // of the head's DV
   const char *K = lds + L::kK, *V = lds + L::kV, *R = lds + L::kRec, *Q = lds + L::kQ;
   const float *gate = reinterpret_cast<const float *>(R + kRecGate);
@@ -520,7 +520,7 @@ hipError_t launch_chain(const GdrArgs &a, char *rec, char *S, char *U, hipStream
   hipLaunchKernelGGL(kernel, dim3(chain_grid(a.N * a.Hv, DV / BV)), dim3(8 * BV), lds, st,
                      static_cast<const __hip_bfloat16 *>(a.q),
                      static_cast<const __hip_bfloat16 *>(a.k),
-                     static_cast<const __hip_bfloat16 *>(a.v), a.S0, a.tab, a.N, a.Hk, a.Hv, rec,
+                     static_cast<const __hip_bfloat16 *>(a.v), a.S0, a.seqs, a.N, a.Hk, a.Hv, rec,
                      static_cast<__hip_bfloat16 *>(a.o), a.S_T, S, U);
   return hipGetLastError();
 }
@@ -540,7 +540,7 @@ hipError_t forward_typed(const GdrArgs &a, char *rec, char *S, char *U, hipStrea
   if (a.n_chunks_ub > 0) {
     hipLaunchKernelGGL((prepare_kernel<DK, STORE>),
                        dim3((unsigned)(a.n_chunks_ub * ((a.Hv + 3) / 4))), dim3(kThreads), 0, st,
-                       q, k, a.g, a.beta, a.tab, a.N, a.Hk, a.Hv, rec);
+                       q, k, a.g, a.beta, a.seqs, a.N, a.Hk, a.Hv, rec);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }
   return chain_columns(a.N * a.Hv, DV) == 64

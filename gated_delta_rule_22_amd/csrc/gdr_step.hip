@@ -117,19 +117,19 @@ template <typename TIn, int DK, int DV>
 __global__ __launch_bounds__(kThreads) void gdr_token_kernel(
     const TIn *__restrict__ q, const TIn *__restrict__ k, const TIn *__restrict__ v,
     const float *__restrict__ g, const float *__restrict__ beta, const float *__restrict__ S0,
-    SeqTable tab, int Hk, int Hv, TIn *__restrict__ o, float *__restrict__ S_T) {
+    Seqs seqs, int Hk, int Hv, TIn *__restrict__ o, float *__restrict__ S_T) {
   constexpr int kCols = 64;              // columns of a workgroup: 4 waves of 16
   constexpr int kBlocks = DV / kCols;
   constexpr int kRows = DK / 4;
   __shared__ float s_k[kStage][DK], s_q[kStage][DK], s_v[kStage][kCols];
   __shared__ float s_a[kStage], s_b[kStage];
   const int blk = blockIdx.x % kBlocks, nh = blockIdx.x / kBlocks;
-  const int n = tab.order[nh / Hv], h = nh % Hv, hk = h / (Hv / Hk);
+  const int n = seqs.order(nh / Hv), h = nh % Hv, hk = h / (Hv / Hk);
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
   const int rr = lane >> 4, c = lane & 15;
   const int col = wave * 16 + c;
-  const size_t first = tab.seq_start[n];
-  const int len = tab.seq_len[n];
+  const size_t first = seqs.start(n);
+  const int len = seqs.len(n);
   const size_t sbase = ((size_t)n * Hv + h) * DK * DV + (size_t)blk * kCols + col;
 
   float S[kRows];
@@ -219,7 +219,7 @@ __global__ __launch_bounds__(kThreads) void gdr_collect_kernel(
     const float *__restrict__ dqx, const float *__restrict__ dkx, const float *__restrict__ dgx,
     const float *__restrict__ g, int N, size_t rows, int Hk,
     int Hv, int dk, float *__restrict__ dq, float *__restrict__ dk_out, float *__restrict__ dg,
-    SeqTable tab) {
+    Seqs seqs) {
   // One wave per (token, query/key head).  Rows outside every sequence are
   // left alone, as everywhere: a row belongs to the last sequence that starts
   // at or before it, if that sequence reaches it.
@@ -232,10 +232,10 @@ __global__ __launch_bounds__(kThreads) void gdr_collect_kernel(
     int lo = 0, hi = N;                  // first sequence that starts behind `row`
     while (lo < hi) {
       const int mid = (lo + hi) / 2;
-      if ((size_t)tab.seq_start[mid] <= row) lo = mid + 1;
+      if ((size_t)seqs.start(mid) <= row) lo = mid + 1;
       else hi = mid;
     }
-    if (lo == 0 || row >= (size_t)tab.seq_start[lo - 1] + tab.seq_len[lo - 1]) continue;
+    if (lo == 0 || row >= (size_t)seqs.start(lo - 1) + seqs.len(lo - 1)) continue;
     for (int c = lane; c < dk; c += 64) {
       float a = 0.f, b = 0.f;
       for (int r = 0; r < rep; ++r) {
@@ -285,7 +285,7 @@ hipError_t token_typed(const GdrArgs &a, hipStream_t stream) {
   if (a.dk == DK_ && a.dv == DV_) {                                                          \
     hipLaunchKernelGGL((gdr_token_kernel<TIn, DK_, DV_>), grid, block, 0, stream,            \
                        static_cast<const TIn *>(a.q), static_cast<const TIn *>(a.k),         \
-                       static_cast<const TIn *>(a.v), a.g, a.beta, a.S0, a.tab, a.Hk, a.Hv,  \
+                       static_cast<const TIn *>(a.v), a.g, a.beta, a.S0, a.seqs, a.Hk, a.Hv,  \
                        static_cast<TIn *>(a.o), a.S_T);                                      \
     return hipGetLastError();                                                                \
   }
@@ -328,11 +328,11 @@ hipError_t launch_gdr_expand(const float *q, const float *k, const float *g, siz
 }
 
 hipError_t launch_gdr_collect(const float *dqx, const float *dkx, const float *dgx,
-                              const float *g, SeqTable tab, int N, size_t rows, int Hk, int Hv,
+                              const float *g, Seqs seqs, int N, size_t rows, int Hk, int Hv,
                               int dk, float *dq, float *dk_out, float *dg, hipStream_t stream) {
   hipLaunchKernelGGL(gdr_collect_kernel, dim3(blocks_for(rows * Hk * 64)), dim3(kThreads), 0,
                      stream, dqx, dkx, dgx, g, N, rows, Hk, Hv, dk, dq,
-                     dk_out, dg, tab);
+                     dk_out, dg, seqs);
   return hipGetLastError();
 }
 

@@ -14,11 +14,12 @@
 // Everything here reads its rows once and writes them once, so HBM traffic is
 // the bound.  One thread holds 2V channels that are V whole pairs, so nothing
 // but the row's sum crosses lanes: G = d / 2V lanes (rounded up to a power of
-// two) share a row.  A workgroup takes kTok tokens at a time and computes the
-// tokens' cosines and sines once into LDS for all of their heads: an angle
-// costs an fp64 product (pos * f in turns, reduced exactly, so that positions
-// of a million and more lose nothing) and an fp32 sincospi, about as much work
-// as the rest of a pair.
+// two) share a row.  A workgroup takes the query or the key heads of kTok
+// tokens at a time (one weight to keep, not two), loads a row ahead, and
+// computes the tokens' cosines and sines once into LDS for all of their heads:
+// an angle costs an fp64 product (pos * f in turns, reduced exactly, so that
+// positions of a million and more lose nothing) and an fp32 sincospi, about as
+// much work as the rest of a pair.
 #include "ckda_internal.h"
 
 namespace ckda {
@@ -26,39 +27,56 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxPairs = 128;          // rd <= 256
+constexpr int kRotaryTile = 8;          // tokens of a workgroup's tile where there are many
+
+// V elements of T as they lie in memory.
+template <int BYTES> struct RawOf { struct Type { uint4 a[BYTES / 16]; }; };
+template <> struct RawOf<8> { using Type = uint2; };
+template <> struct RawOf<4> { using Type = uint32_t; };
+template <> struct RawOf<2> { using Type = uint16_t; };
+template <typename T, int V> struct Raw {
+  typename RawOf<V * (int)sizeof(T)>::Type r[2];
+};
 
 // 2V channels of a row: V first and V second elements of its pairs.
 template <int V> struct Unit { float a[V], b[V]; };
 
-
-template <int V> __device__ __forceinline__ void load_vec(const __hip_bfloat16 *p, float *x) {
-  if constexpr (V == 8) {
-    const uint4 u = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-  } else if constexpr (V == 4) {
-    const float4 f = load4_f32(p);
-    x[0] = f.x; x[1] = f.y; x[2] = f.z; x[3] = f.w;
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = to_f32(p[i]);
-  }
+// Offsets within a row of a unit's first and second V channels in memory, and
+// whether they are rotated.  In the interleaved layout (and behind the rotated
+// part) the 2V channels are contiguous and the pairs are (even, odd).
+struct Place { int p0, p1, pair; bool rot, half; };
+template <int V> __device__ __forceinline__ Place place(int u, int rd, bool half) {
+  Place pl;
+  pl.rot = u < rd / (2 * V);
+  pl.half = half && pl.rot;
+  pl.pair = u * V;
+  pl.p0 = pl.half ? u * V : 2 * V * u;
+  pl.p1 = pl.half ? rd / 2 + u * V : 2 * V * u + V;
+  return pl;
 }
-template <int V> __device__ __forceinline__ void load_vec(const float *p, float *x) {
-  if constexpr (V >= 4) {
+
+template <int V, typename T>
+__device__ __forceinline__ Raw<T, V> load_raw(const T *row, const Place &pl) {
+  Raw<T, V> x;
+  using R = typename RawOf<V * (int)sizeof(T)>::Type;
+  x.r[0] = *reinterpret_cast<const R *>(row + pl.p0);
+  x.r[1] = *reinterpret_cast<const R *>(row + pl.p1);
+  return x;
+}
+template <int V, typename T>
+__device__ __forceinline__ Unit<V> unpack(const Raw<T, V> &raw, const Place &pl) {
+  struct Both { T v[2 * V]; };
+  const Both b = __builtin_bit_cast(Both, raw);
+  float x[2 * V];
 #pragma unroll
-    for (int i = 0; i < V; i += 4) {
-      const float4 f = load4_f32(p + i);
-      x[i] = f.x; x[i + 1] = f.y; x[i + 2] = f.z; x[i + 3] = f.w;
-    }
-  } else {
+  for (int i = 0; i < 2 * V; ++i) x[i] = to_f32(b.v[i]);
+  Unit<V> u;
 #pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = p[i];
+  for (int i = 0; i < V; ++i) {
+    u.a[i] = pl.half ? x[i] : x[2 * i];
+    u.b[i] = pl.half ? x[V + i] : x[2 * i + 1];
   }
+  return u;
 }
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   typedef __bf16 b2 __attribute__((ext_vector_type(2)));
@@ -85,51 +103,33 @@ template <int V> __device__ __forceinline__ void store_vec(float *p, const float
     for (int i = 0; i < V; ++i) p[i] = x[i];
   }
 }
-
-// Offsets within a row of a unit's first and second V channels in memory, and
-// whether they are rotated.  In the interleaved layout (and behind the rotated
-// part) the 2V channels are contiguous and the pairs are (even, odd).
-struct Place { int p0, p1, pair; bool rot; };
-template <int V> __device__ __forceinline__ Place place(int u, int rd, bool half) {
-  const int ur = rd / (2 * V);
-  Place pl;
-  pl.rot = u < ur;
-  pl.pair = u * V;
-  if (pl.rot && half) {
-    pl.p0 = u * V;
-    pl.p1 = rd / 2 + u * V;
-  } else {
-    pl.p0 = 2 * V * u;
-    pl.p1 = 2 * V * u + V;
-  }
-  return pl;
-}
-
-// Raw 2V channels to pairs: in the half layout the two vectors are the pairs'
-// first and second elements; otherwise channels alternate.
 template <int V, typename T>
-__device__ __forceinline__ Unit<V> load_unit(const T *row, const Place &pl, bool half) {
-  Unit<V> r;
-  float x[2 * V];
-  load_vec<V>(row + pl.p0, x);
-  load_vec<V>(row + pl.p1, x + V);
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    r.a[i] = half ? x[i] : x[2 * i];
-    r.b[i] = half ? x[V + i] : x[2 * i + 1];
-  }
-  return r;
-}
-template <int V, typename T>
-__device__ __forceinline__ void store_unit(T *row, const Place &pl, bool half, const Unit<V> &r) {
+__device__ __forceinline__ void store_unit(T *row, const Place &pl, const Unit<V> &r) {
   float x[2 * V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    x[half ? i : 2 * i] = r.a[i];
-    x[half ? V + i : 2 * i + 1] = r.b[i];
+    x[2 * i] = pl.half ? 0.f : r.a[i];
+    x[2 * i + 1] = pl.half ? 0.f : r.b[i];
+  }
+  if (pl.half) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      x[i] = r.a[i];
+      x[V + i] = r.b[i];
+    }
   }
   store_vec<V>(row + pl.p0, x);
   store_vec<V>(row + pl.p1, x + V);
+}
+template <int V>
+__device__ __forceinline__ Unit<V> load_weight(const float *w, const Place &pl) {
+  Unit<V> u;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    u.a[i] = w ? w[pl.half ? pl.p0 + i : pl.p0 + 2 * i] : 1.f;
+    u.b[i] = w ? w[pl.half ? pl.p1 + i : pl.p0 + 2 * i + 1] : 1.f;
+  }
+  return u;
 }
 
 template <int V>
@@ -146,7 +146,7 @@ __device__ __forceinline__ void rotate(Unit<V> &x, const float2 *cs, const Place
   }
 }
 
-// cos and sin (times `scale`) of kTok tokens' angles into LDS.
+// cos and sin (times `scale`) of nt tokens' angles into LDS.
 __device__ __forceinline__ void angles(float2 (*s_cs)[kMaxPairs], const int32_t *pos,
                                        const double *freqs, int t0, int nt, int pairs,
                                        float scale) {
@@ -161,171 +161,181 @@ __device__ __forceinline__ void angles(float2 (*s_cs)[kMaxPairs], const int32_t 
   }
 }
 
-// kTok: 4 tokens share a workgroup where there are many (fewer, fuller
+// The rows of a workgroup's tile that a lane group goes through: (token, head)
+// `groups` apart, without a division a row.
+struct Rows {
+  int t, h, step_t, step_h, H, nt;
+  __device__ Rows(int group, int groups, int H_, int nt_) : H(H_), nt(nt_) {
+    step_t = groups / H;
+    step_h = groups - step_t * H;
+    t = group / H;
+    h = group - t * H;
+  }
+  __device__ bool inside() const { return t < nt; }
+  __device__ void next() {
+    t += step_t;
+    h += step_h;
+    if (h >= H) {
+      h -= H;
+      ++t;
+    }
+  }
+};
+
+// kTok: 8 tokens share a workgroup where there are many (fewer, fuller
 // workgroups); 1 where there are few, so that they spread over the chip.
 template <typename T, int V, bool kNorm, int kTok>
 __global__ __launch_bounds__(kThreads) void rotary_fwd_kernel(RotaryArgs a) {
   constexpr int kU = V == 1 ? 2 : 1;     // units a lane holds (V = 1: up to 128 pairs a row)
   __shared__ float2 s_cs[kTok][kMaxPairs];
-  const int t0 = blockIdx.x * kTok;
-  const int nt = min(kTok, a.tokens - t0);
-  if (a.rd) angles(s_cs, a.pos, a.freqs, t0, nt, a.rd / 2, a.rotary_scale);
-  __syncthreads();
+  const bool isq = blockIdx.y == 0 && a.Hq > 0;
+  const int H = isq ? a.Hq : a.Hk;
+  const size_t ldi = isq ? a.ldq : a.ldk, ldo = isq ? a.ldqo : a.ldko;
+  const int t0 = blockIdx.x * kTok, nt = min(kTok, a.tokens - t0);
+  const T *in = static_cast<const T *>(isq ? a.q : a.k) + (size_t)t0 * ldi;
+  T *out = static_cast<T *>(isq ? a.qo : a.ko) + (size_t)t0 * ldo;
+  const float scale = isq ? a.q_scale : 1.f;
 
   const int G = a.lanes, units = a.d / (2 * V);
-  const int lane = threadIdx.x % G, group = threadIdx.x / G, groups = kThreads / G;
-  const int heads = a.Hq + a.Hk;
+  const int lane = threadIdx.x % G;
   Place pl[kU];
-  bool on[kU], half[kU];
-  Unit<V> wq[kU], wk[kU];
+  bool on[kU];
+  Raw<T, V> raw[kU];
+  Unit<V> w[kU];
+  Rows at(threadIdx.x / G, kThreads / G, H, nt);
 #pragma unroll
   for (int j = 0; j < kU; ++j) {
     const int u = lane + j * G;
     on[j] = u < units;
     pl[j] = place<V>(on[j] ? u : 0, a.rd, a.half);
-    half[j] = a.half && pl[j].rot;
-    if (on[j] && a.wq) wq[j] = load_unit<V>(a.wq, pl[j], half[j]);
-    if (on[j] && a.wk) wk[j] = load_unit<V>(a.wk, pl[j], half[j]);
+    if (on[j] && at.inside())
+      raw[j] = load_raw<V>(in + (size_t)at.t * ldi + (size_t)at.h * a.d, pl[j]);
+    w[j] = load_weight<V>(isq ? a.wq : a.wk, pl[j]);
   }
-  for (int r = group; r < nt * heads; r += groups) {
-    const int t = r / heads, h = r - t * heads;
-    const bool isq = h < a.Hq;
-    const size_t tok = (size_t)(t0 + t);
-    const T *row = isq ? static_cast<const T *>(a.q) + tok * a.ldq + (size_t)h * a.d
-                       : static_cast<const T *>(a.k) + tok * a.ldk + (size_t)(h - a.Hq) * a.d;
-    T *dst = isq ? static_cast<T *>(a.qo) + tok * a.ldqo + (size_t)h * a.d
-                 : static_cast<T *>(a.ko) + tok * a.ldko + (size_t)(h - a.Hq) * a.d;
+  if (a.rd) angles(s_cs, a.pos, a.freqs, t0, nt, a.rd / 2, a.rotary_scale);
+  __syncthreads();
+  while (at.inside()) {
+    const int t = at.t;
+    T *dst = out + (size_t)t * ldo + (size_t)at.h * a.d;
     Unit<V> x[kU];
     float ss = 0.f;
 #pragma unroll
     for (int j = 0; j < kU; ++j)
       if (on[j]) {
-        x[j] = load_unit<V>(row, pl[j], half[j]);
+        x[j] = unpack<V, T>(raw[j], pl[j]);
         if (kNorm)
 #pragma unroll
           for (int i = 0; i < V; ++i) ss += x[j].a[i] * x[j].a[i] + x[j].b[i] * x[j].b[i];
       }
-    float f = isq ? a.q_scale : 1.f;
+    at.next();
+#pragma unroll
+    for (int j = 0; j < kU; ++j)         // the next row, on its way meanwhile
+      if (on[j] && at.inside())
+        raw[j] = load_raw<V>(in + (size_t)at.t * ldi + (size_t)at.h * a.d, pl[j]);
+    float f = scale;
     if (kNorm) {
       for (int o = G >> 1; o > 0; o >>= 1) ss += __shfl_xor(ss, o);
       f *= 1.f / sqrtf(ss * a.norm_scale + a.eps);
     }
-    const bool has_w = isq ? a.wq != nullptr : a.wk != nullptr;
 #pragma unroll
     for (int j = 0; j < kU; ++j)
       if (on[j]) {
-        const Unit<V> &w = isq ? wq[j] : wk[j];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          x[j].a[i] *= has_w ? f * w.a[i] : f;
-          x[j].b[i] *= has_w ? f * w.b[i] : f;
+          x[j].a[i] *= f * w[j].a[i];
+          x[j].b[i] *= f * w[j].b[i];
         }
         rotate<V>(x[j], s_cs[t], pl[j], a.inverse);
-        store_unit<V>(dst, pl[j], half[j], x[j]);
+        store_unit<V>(dst, pl[j], x[j]);
       }
   }
 }
 
-// Sums over a workgroup's row groups, in a fixed order, of each lane's 2V
-// weight-gradient terms; one row of d per workgroup goes to the workspace.
-template <int V, int kU>
-__device__ __forceinline__ void write_partial(const Unit<V> *acc, const Place *pl, const bool *on,
-                                              const bool *half, float *s_red, int group,
-                                              int groups, int d, float *dst) {
-  // Row groups write their terms in turn into kSlots rows of LDS, then add up.
-  for (int g = 0; g < groups; ++g) {
-    if (group == g)
-#pragma unroll
-      for (int j = 0; j < kU; ++j)
-        if (on[j])
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const int ca = half[j] ? pl[j].p0 + i : pl[j].p0 + 2 * i;
-            const int cb = half[j] ? pl[j].p1 + i : pl[j].p0 + 2 * i + 1;
-            s_red[ca] = (g ? s_red[ca] : 0.f) + acc[j].a[i];
-            s_red[cb] = (g ? s_red[cb] : 0.f) + acc[j].b[i];
-          }
-    __syncthreads();
-  }
-  for (int c = threadIdx.x; c < d; c += kThreads) dst[c] = s_red[c];
-  __syncthreads();
-}
-
+// Workgroups go over tiles of 8 tokens, a fixed set each, and keep the weight
+// gradient's terms of their rows in registers.
 template <typename T, int V, bool kNorm>
-__global__ __launch_bounds__(kThreads) void rotary_bwd_kernel(RotaryArgs a) {
-  constexpr int kU = V == 1 ? 2 : 1, kTok = 4;
+__global__ __launch_bounds__(kThreads, 4) void rotary_bwd_kernel(RotaryArgs a) {
+  constexpr int kU = V == 1 ? 2 : 1, kTok = kRotaryTile;
   __shared__ float2 s_cs[kTok][kMaxPairs];
-  __shared__ float s_red[2 * kMaxPairs];
+  __shared__ float s_red[2 * V * kU * kThreads];   // a row of d (<= 2 V kU G) for every lane group
+  const bool isq = blockIdx.y == 0 && a.Hq > 0;
+  const int H = isq ? a.Hq : a.Hk;
+  const size_t ldi = isq ? a.ldq : a.ldk, ldu = isq ? a.lddq : a.lddk;
+  const size_t ldo = isq ? a.ldqo : a.ldko;
+  const T *in = static_cast<const T *>(isq ? a.q : a.k);
+  const T *up = static_cast<const T *>(isq ? a.dq : a.dk);
+  T *out = static_cast<T *>(isq ? a.qo : a.ko);
+  const float scale = isq ? a.q_scale : 1.f;
+  const bool has_w = (isq ? a.wq : a.wk) != nullptr;
+
   const int G = a.lanes, units = a.d / (2 * V);
   const int lane = threadIdx.x % G, group = threadIdx.x / G, groups = kThreads / G;
-  const int heads = a.Hq + a.Hk;
   Place pl[kU];
-  bool on[kU], half[kU];
-  Unit<V> wq[kU], wk[kU], dwq[kU], dwk[kU];
+  bool on[kU];
+  Unit<V> w[kU], dw[kU];
 #pragma unroll
   for (int j = 0; j < kU; ++j) {
     const int u = lane + j * G;
     on[j] = u < units;
     pl[j] = place<V>(on[j] ? u : 0, a.rd, a.half);
-    half[j] = a.half && pl[j].rot;
-    if (on[j] && a.wq) wq[j] = load_unit<V>(a.wq, pl[j], half[j]);
-    if (on[j] && a.wk) wk[j] = load_unit<V>(a.wk, pl[j], half[j]);
+    w[j] = load_weight<V>(isq ? a.wq : a.wk, pl[j]);
 #pragma unroll
-    for (int i = 0; i < V; ++i) dwq[j].a[i] = dwq[j].b[i] = dwk[j].a[i] = dwk[j].b[i] = 0.f;
+    for (int i = 0; i < V; ++i) dw[j].a[i] = dw[j].b[i] = 0.f;
   }
   const int tiles = (a.tokens + kTok - 1) / kTok;
   for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
     const int t0 = tile * kTok, nt = min(kTok, a.tokens - t0);
+    Rows at(group, groups, H, nt);
+    Raw<T, V> rx[kU], ry[kU];
+    auto fetch = [&]() {
+      if (!at.inside()) return;
+      const size_t t = (size_t)(t0 + at.t), hh = (size_t)at.h * a.d;
+#pragma unroll
+      for (int j = 0; j < kU; ++j)
+        if (on[j]) {
+          rx[j] = load_raw<V>(in + t * ldi + hh, pl[j]);
+          ry[j] = load_raw<V>(up + t * ldu + hh, pl[j]);
+        }
+    };
+    fetch();
     if (a.rd) angles(s_cs, a.pos, a.freqs, t0, nt, a.rd / 2, a.rotary_scale);
     __syncthreads();
-    for (int r = group; r < nt * heads; r += groups) {
-      const int t = r / heads, h = r - t * heads;
-      const bool isq = h < a.Hq;
-      const size_t tok = (size_t)(t0 + t);
-      const size_t hh = (size_t)(isq ? h : h - a.Hq) * a.d;
-      const T *row = static_cast<const T *>(isq ? a.q : a.k) + tok * (isq ? a.ldq : a.ldk) + hh;
-      const T *up = static_cast<const T *>(isq ? a.dq : a.dk) + tok * (isq ? a.lddq : a.lddk) + hh;
-      T *dst = static_cast<T *>(isq ? a.qo : a.ko) + tok * (isq ? a.ldqo : a.ldko) + hh;
+    while (at.inside()) {
+      const int t = at.t;
+      T *dst = out + (size_t)(t0 + t) * ldo + (size_t)at.h * a.d;
       Unit<V> x[kU], y[kU];
       float ss = 0.f;
 #pragma unroll
       for (int j = 0; j < kU; ++j)
         if (on[j]) {
-          x[j] = load_unit<V>(row, pl[j], half[j]);
-          y[j] = load_unit<V>(up, pl[j], half[j]);
+          x[j] = unpack<V, T>(rx[j], pl[j]);
+          y[j] = unpack<V, T>(ry[j], pl[j]);
           if (kNorm)
 #pragma unroll
             for (int i = 0; i < V; ++i) ss += x[j].a[i] * x[j].a[i] + x[j].b[i] * x[j].b[i];
         }
+      at.next();
+      fetch();                           // the next row, on its way meanwhile
       float rs = 1.f;
       if (kNorm) {
         for (int o = G >> 1; o > 0; o >>= 1) ss += __shfl_xor(ss, o);
         rs = 1.f / sqrtf(ss * a.norm_scale + a.eps);
       }
-      const float f = isq ? a.q_scale : 1.f;
-      const bool has_w = isq ? a.wq != nullptr : a.wk != nullptr;
       float m = 0.f;
 #pragma unroll
       for (int j = 0; j < kU; ++j)
         if (on[j]) {
           rotate<V>(y[j], s_cs[t], pl[j], true);
-          const Unit<V> &w = isq ? wq[j] : wk[j];
 #pragma unroll
           for (int i = 0; i < V; ++i) {
             x[j].a[i] *= rs;
             x[j].b[i] *= rs;
-            y[j].a[i] *= f;
-            y[j].b[i] *= f;
-            const float ta = y[j].a[i] * x[j].a[i], tb = y[j].b[i] * x[j].b[i];
-            if (has_w) {
-              // selects, not a branch: the sums stay in registers
-              dwq[j].a[i] += isq ? ta : 0.f;
-              dwq[j].b[i] += isq ? tb : 0.f;
-              dwk[j].a[i] += isq ? 0.f : ta;
-              dwk[j].b[i] += isq ? 0.f : tb;
-              y[j].a[i] *= w.a[i];
-              y[j].b[i] *= w.b[i];
-            }
+            y[j].a[i] *= scale;
+            y[j].b[i] *= scale;
+            dw[j].a[i] += y[j].a[i] * x[j].a[i];
+            dw[j].b[i] += y[j].b[i] * x[j].b[i];
+            y[j].a[i] *= w[j].a[i];
+            y[j].b[i] *= w[j].b[i];
             if (kNorm) m += y[j].a[i] * x[j].a[i] + y[j].b[i] * x[j].b[i];
           }
         }
@@ -342,34 +352,53 @@ __global__ __launch_bounds__(kThreads) void rotary_bwd_kernel(RotaryArgs a) {
               y[j].a[i] = rs * (y[j].a[i] - x[j].a[i] * m);
               y[j].b[i] = rs * (y[j].b[i] - x[j].b[i] * m);
             }
-          store_unit<V>(dst, pl[j], half[j], y[j]);
+          store_unit<V>(dst, pl[j], y[j]);
         }
     }
     __syncthreads();                     // s_cs is rewritten for the next tile
   }
-  float *part = a.partial + (size_t)blockIdx.x * 2 * a.d;
-  if (a.wq) write_partial<V, kU>(dwq, pl, on, half, s_red, group, groups, a.d, part);
-  if (a.wk) write_partial<V, kU>(dwk, pl, on, half, s_red, group, groups, a.d, part + a.d);
+  if (!has_w) return;
+  // The groups' rows of terms, then their sum in a fixed order.
+  float *mine = s_red + group * a.d;
+#pragma unroll
+  for (int j = 0; j < kU; ++j)
+    if (on[j])
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        mine[pl[j].half ? pl[j].p0 + i : pl[j].p0 + 2 * i] = dw[j].a[i];
+        mine[pl[j].half ? pl[j].p1 + i : pl[j].p0 + 2 * i + 1] = dw[j].b[i];
+      }
+  __syncthreads();
+  float *part = a.partial + ((size_t)blockIdx.x * 2 + (isq ? 0 : 1)) * a.d;
+  for (int c = threadIdx.x; c < a.d; c += kThreads) {
+    float s = 0.f;
+    for (int g = 0; g < groups; ++g) s += s_red[g * a.d + c];
+    part[c] = s;
+  }
 }
 
-// dw[c] = the sum of the workgroups' rows, always in the same order: 16
-// threads a column, each over every 16th row, then their 16 sums.
+// dw[c] = the sum of the workgroups' rows, always in the same order: 64
+// threads a column, each over every 64th row, then their sums.
 __global__ __launch_bounds__(kThreads) void weight_sum_kernel(const float *part, int rows, int d,
-                                                              float *dwq, float *dwk) {
-  __shared__ float s[16][17];
-  const int cx = threadIdx.x % 16, ry = threadIdx.x / 16;
-  const int c = blockIdx.x * 16 + cx;    // column of the pair of rows [dwq | dwk]
+                                                              float *dwq, float *dwk, int Hq,
+                                                              int Hk) {
+  __shared__ float s[64][5];
+  const int cx = threadIdx.x % 4, ry = threadIdx.x / 4;
+  const int c = blockIdx.x * 4 + cx;     // column of the pair of rows [dwq | dwk]
+  const bool isq = c < d;
+  const bool want = c < 2 * d && (isq ? dwq : dwk) != nullptr;
   float sum = 0.f;
-  const bool want = c < 2 * d && (c < d ? dwq : dwk) != nullptr;
-  if (want)
-    for (int r = ry; r < rows; r += 16) sum += part[(size_t)r * 2 * d + c];
+  if (want && (isq ? Hq : Hk) > 0) {     // without heads there are no rows
+#pragma unroll 8
+    for (int r = ry; r < rows; r += 64) sum += part[(size_t)r * 2 * d + c];
+  }
   s[ry][cx] = sum;
   __syncthreads();
   if (ry == 0 && want) {
     float t = 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) t += s[i][cx];
-    (c < d ? dwq : dwk)[c < d ? c : c - d] = t;
+#pragma unroll 8
+    for (int i = 0; i < 64; ++i) t += s[i][cx];
+    (isq ? dwq : dwk)[isq ? c : c - d] = t;
   }
 }
 
@@ -384,8 +413,6 @@ template <typename T> int unit_width(const RotaryArgs &a) {
     const void *ps[] = {a.q, a.k, a.qo, a.ko, a.dq, a.dk};
     const size_t bytes = V * sizeof(T) < 16 ? V * sizeof(T) : 16;
     for (const void *p : ps) ok = ok && reinterpret_cast<uintptr_t>(p) % bytes == 0;
-    ok = ok && reinterpret_cast<uintptr_t>(a.wq) % 16 == 0 &&
-         reinterpret_cast<uintptr_t>(a.wk) % 16 == 0;
     if (ok) return V;
   }
   return 1;
@@ -396,23 +423,25 @@ template <typename T, int V> hipError_t launch_v(RotaryArgs a, bool backward, hi
   int G = 1;
   while (G < units && G < 64) G *= 2;
   a.lanes = G;
+  const unsigned both = a.Hq > 0 && a.Hk > 0 ? 2 : 1;   // query heads, key heads
   if (backward) {
-    const dim3 grid(rotary_bwd_groups(a.tokens));
+    const dim3 grid(rotary_bwd_groups(a.tokens), both);
     if (a.norm) hipLaunchKernelGGL((rotary_bwd_kernel<T, V, true>), grid, dim3(kThreads), 0, st, a);
     else hipLaunchKernelGGL((rotary_bwd_kernel<T, V, false>), grid, dim3(kThreads), 0, st, a);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-    if (a.dwq || a.dwk) {
-      hipLaunchKernelGGL(weight_sum_kernel, dim3((2 * a.d + 15) / 16), dim3(kThreads), 0, st,
-                         a.partial, (int)grid.x, a.d, a.dwq, a.dwk);
-    }
+    if (a.dwq || a.dwk)
+      hipLaunchKernelGGL(weight_sum_kernel, dim3((2 * a.d + 3) / 4), dim3(kThreads), 0, st,
+                         a.partial, (int)grid.x, a.d, a.dwq, a.dwk, a.Hq, a.Hk);
     return hipGetLastError();
   }
   if (a.tokens >= 4096) {
-    const dim3 grid((a.tokens + 3) / 4);
-    if (a.norm) hipLaunchKernelGGL((rotary_fwd_kernel<T, V, true, 4>), grid, dim3(kThreads), 0, st, a);
-    else hipLaunchKernelGGL((rotary_fwd_kernel<T, V, false, 4>), grid, dim3(kThreads), 0, st, a);
+    const dim3 grid((a.tokens + kRotaryTile - 1) / kRotaryTile, both);
+    if (a.norm)
+      hipLaunchKernelGGL((rotary_fwd_kernel<T, V, true, kRotaryTile>), grid, dim3(kThreads), 0, st, a);
+    else
+      hipLaunchKernelGGL((rotary_fwd_kernel<T, V, false, kRotaryTile>), grid, dim3(kThreads), 0, st, a);
   } else {
-    const dim3 grid(a.tokens);
+    const dim3 grid(a.tokens, both);
     if (a.norm) hipLaunchKernelGGL((rotary_fwd_kernel<T, V, true, 1>), grid, dim3(kThreads), 0, st, a);
     else hipLaunchKernelGGL((rotary_fwd_kernel<T, V, false, 1>), grid, dim3(kThreads), 0, st, a);
   }
@@ -429,12 +458,12 @@ template <typename T> hipError_t launch_t(const RotaryArgs &a, bool backward, hi
 
 }  // namespace
 
-// Workgroups of the backward: each keeps its weight-gradient sums over many
-// tiles of 4 tokens, so their number is bounded (one row of the workspace
-// each) and fixed by the number of tokens alone.
+// Workgroups of the backward for query and for key heads: each keeps its
+// weight-gradient sums over many tiles, so their number is bounded (a row of
+// the workspace each) and fixed by the number of tokens alone.
 int rotary_bwd_groups(int tokens) {
-  const int tiles = (tokens + 3) / 4;
-  return tiles < 1 ? 1 : (tiles < 1024 ? tiles : 1024);
+  const int tiles = (tokens + kRotaryTile - 1) / kRotaryTile;
+  return tiles < 1 ? 1 : (tiles < 512 ? tiles : 512);
 }
 
 hipError_t launch_rotary(const RotaryArgs &a, int in_dtype, bool backward, hipStream_t stream) {

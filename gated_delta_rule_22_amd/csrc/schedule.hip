@@ -19,6 +19,17 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kRankMax = 1024;   // rank-sort sequences only up to this many
 
+// Inclusive scan of s_part[1 .. kThreads] over the workgroup (s_part[0] stays).
+template <typename F> __device__ __forceinline__ void scan(int32_t *s_part, int t, F op) {
+  for (int o = 1; o < kThreads; o <<= 1) {
+    __syncthreads();
+    const int32_t x = s_part[t + 1], y = t >= o ? s_part[t + 1 - o] : x;
+    __syncthreads();
+    if (t >= o) s_part[t + 1] = op(x, y);
+  }
+  __syncthreads();
+}
+
 __global__ __launch_bounds__(kThreads) void seq_table_kernel(const int32_t *__restrict__ cu,
                                                              int B, int T, int N, SeqTable tab) {
   __shared__ int32_t s_part[kThreads + 1];
@@ -37,11 +48,8 @@ __global__ __launch_bounds__(kThreads) void seq_table_kernel(const int32_t *__re
     int32_t m = 0;                       // every P_i is >= 0
     for (int n = lo; n < hi; ++n) m = max(m, cu[n]);
     s_part[t + 1] = m;
-    if (t == 0) s_part[0] = 0;
-    __syncthreads();
-    if (t == 0)
-      for (int i = 1; i <= kThreads; ++i) s_part[i] = max(s_part[i], s_part[i - 1]);
-    __syncthreads();
+    if (t == 0) s_part[0] = 0;           // and every m is >= 0
+    scan(s_part, t, [](int32_t a, int32_t b) { return max(a, b); });
     int32_t run = s_part[t];             // max of cu[0 .. lo - 1] (and 0)
     for (int n = lo; n < hi; ++n) {
       run = max(run, cu[n]);
@@ -59,10 +67,7 @@ __global__ __launch_bounds__(kThreads) void seq_table_kernel(const int32_t *__re
   for (int n = lo; n < hi; ++n) sum += (tab.seq_len[n] + kChunk - 1) / kChunk;
   s_part[t + 1] = sum;
   if (t == 0) s_part[0] = 0;
-  __syncthreads();
-  if (t == 0)
-    for (int i = 1; i <= kThreads; ++i) s_part[i] += s_part[i - 1];
-  __syncthreads();
+  scan(s_part, t, [](int32_t a, int32_t b) { return a + b; });
   int32_t acc = s_part[t];
   for (int n = lo; n < hi; ++n) {
     tab.chunk_off[n] = acc;
