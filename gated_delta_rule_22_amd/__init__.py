@@ -18,5 +18,6 @@ __all__ = [*_BINDING, "workloads"]
 def __getattr__(name):
     if name in _BINDING:
         from . import _lib
-        return getattr(_lib, name)
+        value = globals()[name] = getattr(_lib, name)
+        return value
     raise AttributeError(name)

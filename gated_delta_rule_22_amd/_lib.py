@@ -288,6 +288,33 @@ def decode_step(q, k, v, g, beta, S, *, out=None):
 
 # ------------------------------------------------------------------ gated delta rule
 
+def _dense(t, name, dtype, shape, index):
+    """`_need` and the device in one quick test; the slow path says what is wrong."""
+    if (t.dtype is not dtype or t.shape != shape or t.get_device() != index
+            or not t.is_contiguous()):
+        _need(t, name, dtype, shape)
+        raise ValueError(f"all tensors must be on cuda:{index}, got {name} on {t.device}")
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+# The same numbers as torch.cuda.current_stream / current_device give, without
+# the objects around them (2 of the 12 us of a small call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _call(index, fn, *args):
+    """Calls a library function with the current stream of device `index` as its
+    last argument, that device being the current one."""
+    if _raw_stream is None or index != _raw_device():
+        with torch.cuda.device(index):
+            return fn(*args, torch.cuda.current_stream(index).cuda_stream)
+    return fn(*args, _raw_stream(index))
+
+
 def gdr_forward_workspace_bytes(B, T, Hk, Hv, dk, dv, N, dtype) -> int:
     code = dtype if isinstance(dtype, int) else (CKDA_BF16 if dtype == torch.bfloat16 else CKDA_F32)
     return int(library().gdr_forward_workspace_bytes(B, T, Hk, Hv, dk, dv, N, code))
@@ -297,24 +324,31 @@ def _gdr_sizes(q, k, v, g, beta, cu_seqlens):
     """Checks the inputs shared by the forward and the backward; their sizes."""
     if q.dim() != 4 or v.dim() != 4:
         raise ValueError("q, k and v must have 4 dimensions [B, T, heads, channels]")
+    if not q.is_cuda:
+        raise ValueError("q must be a device tensor")
     B, T, Hk, dk = q.shape
     Hv, dv = v.shape[-2:]
-    for t, n in ((q, "q"), (k, "k"), (v, "v")):
-        _need(t, n, q.dtype)
-    _need(k, "k", shape=(B, T, Hk, dk))
-    _need(v, "v", shape=(B, T, Hv, dv))
-    _need(g, "g", torch.float32, (B, T, Hv))
-    _need(beta, "beta", torch.float32, (B, T, Hv))
+    dt, index = q.dtype, q.get_device()
+    _dense(q, "q", dt, (B, T, Hk, dk), index)
+    _dense(k, "k", dt, (B, T, Hk, dk), index)
+    _dense(v, "v", dt, (B, T, Hv, dv), index)
+    _dense(g, "g", torch.float32, (B, T, Hv), index)
+    _dense(beta, "beta", torch.float32, (B, T, Hv), index)
     if cu_seqlens is None:
-        return B, T, Hk, Hv, dk, dv, B
-    _need(cu_seqlens, "cu_seqlens", torch.int32)
-    return B, T, Hk, Hv, dk, dv, cu_seqlens.numel() - 1
+        return B, T, Hk, Hv, dk, dv, B, index
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
+        raise ValueError("cu_seqlens must be [N + 1] offsets of at least one sequence")
+    _dense(cu_seqlens, "cu_seqlens", torch.int32, cu_seqlens.shape, index)
+    return B, T, Hk, Hv, dk, dv, cu_seqlens.shape[0] - 1, index
 
 
-def _same_device(dev, *tensors):
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"all tensors must be on {dev}, got one on {t.device}")
+def _scratch(workspace, need, index):
+    """The caller's workspace if it is large enough, else a new one."""
+    if workspace is None or workspace.numel() * workspace.element_size() < need:
+        return torch.empty(max(need, 1), dtype=torch.uint8, device=index)
+    if workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{index}")
+    return workspace
 
 
 def gdr_forward(q, k, v, g, beta, S0=None, cu_seqlens=None, *, out=None, final_state=None,
@@ -325,27 +359,29 @@ def gdr_forward(q, k, v, g, beta, S0=None, cu_seqlens=None, *, out=None, final_s
     ``output_final_state`` is False).  See ``gdr_forward`` in include/ckda.h for
     shapes; ``final_state`` may be ``S0`` itself."""
     code = _dtype_code(q)
-    B, T, Hk, Hv, dk, dv, N = _gdr_sizes(q, k, v, g, beta, cu_seqlens)
+    B, T, Hk, Hv, dk, dv, N, index = _gdr_sizes(q, k, v, g, beta, cu_seqlens)
+    f32, states = torch.float32, (N, Hv, dk, dv)
     if S0 is not None:
-        _need(S0, "S0", torch.float32, (N, Hv, dk, dv))
-    dev = q.device
-    o = out if out is not None else torch.empty((B, T, Hv, dv), dtype=q.dtype, device=dev)
-    _need(o, "out", q.dtype, (B, T, Hv, dv))
+        _dense(S0, "S0", f32, states, index)
+    if out is None:
+        out = torch.empty((B, T, Hv, dv), dtype=q.dtype, device=index)
+    else:
+        _dense(out, "out", q.dtype, (B, T, Hv, dv), index)
     S_T = None
     if output_final_state:
-        S_T = final_state if final_state is not None else torch.empty(
-            (N, Hv, dk, dv), dtype=torch.float32, device=dev)
-        _need(S_T, "final_state", torch.float32, (N, Hv, dk, dv))
-    ws_bytes = gdr_forward_workspace_bytes(B, T, Hk, Hv, dk, dv, N, code)
-    if workspace is None or workspace.numel() * workspace.element_size() < ws_bytes:
-        workspace = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=dev)
-    _same_device(dev, k, v, g, beta, S0, cu_seqlens, o, S_T, workspace)
-    with torch.cuda.device(dev):
-        st = library().gdr_forward(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S0),
-                                   _ptr(cu_seqlens), B, T, Hk, Hv, dk, dv, N, code, _ptr(o),
-                                   _ptr(S_T), _ptr(workspace), ws_bytes, _stream(dev))
+        S_T = final_state
+        if S_T is None:
+            S_T = torch.empty(states, dtype=f32, device=index)
+        else:
+            _dense(S_T, "final_state", f32, states, index)
+    lib = library()
+    need = lib.gdr_forward_workspace_bytes(B, T, Hk, Hv, dk, dv, N, code)
+    workspace = _scratch(workspace, need, index)
+    st = _call(index, lib.gdr_forward, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+               beta.data_ptr(), _addr(S0), _addr(cu_seqlens), B, T, Hk, Hv, dk, dv, N, code,
+               out.data_ptr(), _addr(S_T), workspace.data_ptr(), need)
     _check(st, "gdr_forward")
-    return o, S_T
+    return out, S_T
 
 
 def gdr_backward_workspace_bytes(B, T, Hk, Hv, dk, dv, N, dtype) -> int:
@@ -360,25 +396,22 @@ def gdr_backward(q, k, v, g, beta, do, S0=None, dS_T=None, cu_seqlens=None, *, w
     others fp32 (``dS0`` is None when ``need_dS0`` is False).  See
     ``gdr_backward`` in include/ckda.h."""
     code = _dtype_code(q)
-    B, T, Hk, Hv, dk, dv, N = _gdr_sizes(q, k, v, g, beta, cu_seqlens)
-    _need(do, "do", q.dtype, (B, T, Hv, dv))
+    B, T, Hk, Hv, dk, dv, N, index = _gdr_sizes(q, k, v, g, beta, cu_seqlens)
+    f32, states = torch.float32, (N, Hv, dk, dv)
+    _dense(do, "do", q.dtype, (B, T, Hv, dv), index)
     for t, n in ((S0, "S0"), (dS_T, "dS_T")):
         if t is not None:
-            _need(t, n, torch.float32, (N, Hv, dk, dv))
-    dev = q.device
-    f32 = dict(dtype=torch.float32, device=dev)
+            _dense(t, n, f32, states, index)
     dq, dk_, dv_ = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-    dg, db = torch.empty((B, T, Hv), **f32), torch.empty((B, T, Hv), **f32)
-    dS0 = torch.empty((N, Hv, dk, dv), **f32) if need_dS0 else None
-    ws_bytes = gdr_backward_workspace_bytes(B, T, Hk, Hv, dk, dv, N, code)
-    if workspace is None or workspace.numel() * workspace.element_size() < ws_bytes:
-        workspace = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=dev)
-    _same_device(dev, k, v, g, beta, do, S0, dS_T, cu_seqlens, workspace)
-    with torch.cuda.device(dev):
-        st = library().gdr_backward(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S0),
-                                    _ptr(cu_seqlens), B, T, Hk, Hv, dk, dv, N, code, _ptr(do),
-                                    _ptr(dS_T), _ptr(dq), _ptr(dk_), _ptr(dv_), _ptr(dg),
-                                    _ptr(db), _ptr(dS0), _ptr(workspace), ws_bytes, _stream(dev))
+    dg, db = torch.empty_like(g), torch.empty_like(beta)
+    dS0 = torch.empty(states, dtype=f32, device=index) if need_dS0 else None
+    lib = library()
+    need = lib.gdr_backward_workspace_bytes(B, T, Hk, Hv, dk, dv, N, code)
+    workspace = _scratch(workspace, need, index)
+    st = _call(index, lib.gdr_backward, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+               beta.data_ptr(), _addr(S0), _addr(cu_seqlens), B, T, Hk, Hv, dk, dv, N, code,
+               do.data_ptr(), _addr(dS_T), dq.data_ptr(), dk_.data_ptr(), dv_.data_ptr(),
+               dg.data_ptr(), db.data_ptr(), _addr(dS0), workspace.data_ptr(), need)
     _check(st, "gdr_backward")
     return dq, dk_, dv_, dg, db, dS0
 
@@ -390,29 +423,29 @@ def gdr_decode_step(q, k, v, g, beta, S, slots=None, *, out=None):
     ``o`` is zero.  Returns o ``[N, Hv, dv]`` in the type of ``q``."""
     if q.dim() != 3 or v.dim() != 3 or S.dim() != 4:
         raise ValueError("q, k and v must have 3 dimensions [N, heads, channels], S 4")
+    if not q.is_cuda:
+        raise ValueError("q must be a device tensor")
     N, Hk, dk = q.shape
     Hv, dv = v.shape[-2:]
-    code = _dtype_code(q)
-    for t, n in ((q, "q"), (k, "k"), (v, "v")):
-        _need(t, n, q.dtype)
-    _need(k, "k", shape=(N, Hk, dk))
-    _need(v, "v", shape=(N, Hv, dv))
-    _need(g, "g", torch.float32, (N, Hv))
-    _need(beta, "beta", torch.float32, (N, Hv))
+    code, dt, index, f32 = _dtype_code(q), q.dtype, q.get_device(), torch.float32
     pool = S.shape[0]
-    _need(S, "S", torch.float32, (pool, Hv, dk, dv))
+    _dense(q, "q", dt, (N, Hk, dk), index)
+    _dense(k, "k", dt, (N, Hk, dk), index)
+    _dense(v, "v", dt, (N, Hv, dv), index)
+    _dense(g, "g", f32, (N, Hv), index)
+    _dense(beta, "beta", f32, (N, Hv), index)
+    _dense(S, "S", f32, (pool, Hv, dk, dv), index)
     if slots is not None:
-        _need(slots, "slots", torch.int32, (N,))
-    dev = q.device
-    o = out if out is not None else torch.empty((N, Hv, dv), dtype=q.dtype, device=dev)
-    _need(o, "out", q.dtype, (N, Hv, dv))
-    _same_device(dev, k, v, g, beta, S, slots, o)
-    with torch.cuda.device(dev):
-        st = library().gdr_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S),
-                                       _ptr(slots), pool, _ptr(o), N, Hk, Hv, dk, dv, code,
-                                       _stream(dev))
+        _dense(slots, "slots", torch.int32, (N,), index)
+    if out is None:
+        out = torch.empty((N, Hv, dv), dtype=dt, device=index)
+    else:
+        _dense(out, "out", dt, (N, Hv, dv), index)
+    st = _call(index, library().gdr_decode_step, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+               g.data_ptr(), beta.data_ptr(), S.data_ptr(), _addr(slots), pool, out.data_ptr(),
+               N, Hk, Hv, dk, dv, code)
     _check(st, "gdr_decode_step")
-    return o
+    return out
 
 
 # ------------------------------------------------------------------ norm and rotation
@@ -462,28 +495,26 @@ def rotary_frequencies(rotary_dim, base=10000.0, *, scaling=None, factor=1.0,
     return freqs.to(device), scale
 
 
-def _rows(t, name, dtype=None, lead=None, d=None):
-    """Rows [..., heads, d] whose heads are dense and whose tokens are one
-    distance apart; (heads, tokens, distance in elements)."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
-    if t.dim() < 3:
-        raise ValueError(f"{name} must have at least 3 dimensions [..., heads, channels]")
-    if dtype is not None and t.dtype != dtype:
+def _rows(t, name, dtype, lead, heads, d, index):
+    """Checks rows [*lead, heads, d] whose heads are dense and whose tokens are
+    one distance apart; that distance in elements."""
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if lead is not None and tuple(t.shape[:-2]) != tuple(lead):
-        raise ValueError(f"{name} must have leading dimensions {tuple(lead)}, got {tuple(t.shape)}")
-    if d is not None and t.shape[-1] != d:
-        raise ValueError(f"{name} must have {d} channels, got {t.shape[-1]}")
-    heads, width = t.shape[-2:]
-    tokens = t.shape[:-2].numel()
-    if t.numel() == 0:
-        return heads, tokens, heads * width
-    if (width > 1 and t.stride(-1) != 1) or (heads > 1 and t.stride(-2) != width):
+    if t.get_device() != index:
+        where = "a device tensor" if index < 0 or not t.is_cuda else f"on cuda:{index}"
+        raise ValueError(f"{name} must be {where}")
+    shape = t.shape
+    if shape[:-2] != lead or shape[-1] != d or (heads is not None and shape[-2] != heads):
+        want = (*lead, "heads" if heads is None else heads, d)
+        raise ValueError(f"{name} must have shape {want}, got {tuple(shape)}")
+    row = shape[-2] * d
+    if t.is_contiguous():
+        return row
+    stride = t.stride()
+    if (d > 1 and stride[-1] != 1) or (shape[-2] > 1 and stride[-2] != d):
         raise ValueError(f"{name}: a token's heads must be contiguous")
-    ld = None
-    span = 1                            # tokens that the dimensions so far cover
-    for n, s in zip(reversed(t.shape[:-2]), reversed(t.stride()[:-2])):
+    ld, span = None, 1                  # tokens that the dimensions so far cover
+    for n, s in zip(reversed(lead), reversed(stride[:-2])):
         if n == 1:
             continue
         if ld is None:
@@ -491,22 +522,33 @@ def _rows(t, name, dtype=None, lead=None, d=None):
         elif s != ld * span:
             raise ValueError(f"{name}: tokens must be evenly spaced")
         span *= n
-    ld = heads * width if ld is None else ld
-    if ld < heads * width:
+    if ld is None:
+        return row
+    if ld < row:
         raise ValueError(f"{name}: tokens must not overlap")
-    return heads, tokens, ld
+    return ld
 
 
-def _angles(positions, freqs, lead, d):
+def _angles(positions, freqs, lead, d, index):
+    """Checks positions and freqs; the number of rotated channels."""
     if freqs is None:
-        return 0, None
+        return 0
     if positions is None:
         raise ValueError("positions are needed with freqs")
-    _need(positions, "positions", torch.int32, lead)
-    _need(freqs, "freqs", torch.float64)
-    if freqs.dim() != 1 or not 0 < 2 * freqs.numel() <= d:
+    _dense(positions, "positions", torch.int32, lead, index)
+    if freqs.dim() != 1 or not 0 < 2 * freqs.shape[0] <= d:
         raise ValueError(f"freqs must have 1 to {d // 2} entries, got {tuple(freqs.shape)}")
-    return 2 * freqs.numel(), positions
+    _dense(freqs, "freqs", torch.float64, freqs.shape, index)
+    return 2 * freqs.shape[0]
+
+
+def _lead(x, name):
+    if x.dim() < 3:
+        raise ValueError(f"{name} must have at least 3 dimensions [..., heads, channels]")
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    lead = x.shape[:-2]
+    return lead, lead[0] if len(lead) == 1 else lead.numel(), x.shape[-2], x.shape[-1], x.get_device()
 
 
 def _choice(table, value, name):
@@ -525,30 +567,30 @@ def qk_norm_rotary(q, k, positions=None, freqs=None, *, norm="rms", q_weight=Non
     projection; results are dense unless ``q_out`` / ``k_out`` (which may be
     ``q`` / ``k``) are given.  See ``qk_norm_rotary`` in include/ckda.h and
     :func:`rotary_frequencies`."""
-    code = _dtype_code(q)
-    Hq, tokens, ldq = _rows(q, "q")
-    lead, d = tuple(q.shape[:-2]), q.shape[-1]
-    Hk, _, ldk = _rows(k, "k", q.dtype, lead, d)
-    rd, positions = _angles(positions, freqs, lead, d)
+    code, dt = _dtype_code(q), q.dtype
+    lead, tokens, Hq, d, index = _lead(q, "q")
+    Hk = k.shape[-2] if k.dim() > 1 else 0
+    ldq = _rows(q, "q", dt, lead, Hq, d, index)
+    ldk = _rows(k, "k", dt, lead, None, d, index)
+    rd = _angles(positions, freqs, lead, d, index)
     for t, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
         if t is not None:
-            _need(t, n, torch.float32, (d,))
-    dev = q.device
-    qo = q_out if q_out is not None else torch.empty(q.shape, dtype=q.dtype, device=dev)
-    ko = k_out if k_out is not None else torch.empty(k.shape, dtype=q.dtype, device=dev)
-    hq, _, ldqo = _rows(qo, "q_out", q.dtype, lead, d)
-    hk, _, ldko = _rows(ko, "k_out", q.dtype, lead, d)
-    if (hq, hk) != (Hq, Hk):
-        raise ValueError("q_out and k_out must have the heads of q and k")
-    _same_device(dev, k, positions, freqs, q_weight, k_weight, qo, ko)
-    with torch.cuda.device(dev):
-        st = library().qk_norm_rotary(
-            _ptr(q), _ptr(k), _ptr(positions), _ptr(freqs), _ptr(q_weight), _ptr(k_weight),
-            tokens, Hq, Hk, d, rd, ldq, ldk, _choice(_NORMS, norm, "norm"),
-            _choice(_LAYOUTS, layout, "layout"), eps, q_scale, rotary_scale, code, _ptr(qo),
-            _ptr(ko), ldqo, ldko, _stream(dev))
+            _dense(t, n, torch.float32, (d,), index)
+    ldqo, ldko = Hq * d, Hk * d
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=dt, device=index)
+    else:
+        ldqo = _rows(q_out, "q_out", dt, lead, Hq, d, index)
+    if k_out is None:
+        k_out = torch.empty(k.shape, dtype=dt, device=index)
+    else:
+        ldko = _rows(k_out, "k_out", dt, lead, Hk, d, index)
+    st = _call(index, library().qk_norm_rotary, q.data_ptr(), k.data_ptr(), _addr(positions),
+               _addr(freqs), _addr(q_weight), _addr(k_weight), tokens, Hq, Hk, d, rd, ldq, ldk,
+               _choice(_NORMS, norm, "norm"), _choice(_LAYOUTS, layout, "layout"), eps, q_scale,
+               rotary_scale, code, q_out.data_ptr(), k_out.data_ptr(), ldqo, ldko)
     _check(st, "qk_norm_rotary")
-    return qo, ko
+    return q_out, k_out
 
 
 def qk_norm_rotary_backward(dq_out, dk_out, q, k, positions=None, freqs=None, *, norm="rms",
@@ -558,61 +600,59 @@ def qk_norm_rotary_backward(dq_out, dk_out, q, k, positions=None, freqs=None, *,
     ``dk_out`` of its results: ``(dq, dk, dq_weight, dk_weight)``, the weights'
     fp32 (None where there is no weight).  ``dq`` / ``dk`` may be slices of the
     projection's gradient."""
-    code = _dtype_code(q)
-    Hq, tokens, ldq = _rows(q, "q")
-    lead, d = tuple(q.shape[:-2]), q.shape[-1]
-    Hk, _, ldk = _rows(k, "k", q.dtype, lead, d)
-    uq, _, lddq = _rows(dq_out, "dq_out", q.dtype, lead, d)
-    uk, _, lddk = _rows(dk_out, "dk_out", q.dtype, lead, d)
-    rd, positions = _angles(positions, freqs, lead, d)
+    code, dt, f32 = _dtype_code(q), q.dtype, torch.float32
+    lead, tokens, Hq, d, index = _lead(q, "q")
+    Hk = k.shape[-2] if k.dim() > 1 else 0
+    ldq = _rows(q, "q", dt, lead, Hq, d, index)
+    ldk = _rows(k, "k", dt, lead, None, d, index)
+    lddq = _rows(dq_out, "dq_out", dt, lead, Hq, d, index)
+    lddk = _rows(dk_out, "dk_out", dt, lead, Hk, d, index)
+    rd = _angles(positions, freqs, lead, d, index)
     for t, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
         if t is not None:
-            _need(t, n, torch.float32, (d,))
-    dev = q.device
-    gq = dq if dq is not None else torch.empty(q.shape, dtype=q.dtype, device=dev)
-    gk = dk if dk is not None else torch.empty(k.shape, dtype=q.dtype, device=dev)
-    oq, _, ldgq = _rows(gq, "dq", q.dtype, lead, d)
-    ok, _, ldgk = _rows(gk, "dk", q.dtype, lead, d)
-    if (uq, uk) != (Hq, Hk) or (oq, ok) != (Hq, Hk):
-        raise ValueError("gradients must have the heads of q and k")
-    dwq = None if q_weight is None else torch.empty(d, dtype=torch.float32, device=dev)
-    dwk = None if k_weight is None else torch.empty(d, dtype=torch.float32, device=dev)
-    ws_bytes = 0
+            _dense(t, n, f32, (d,), index)
+    ldgq, ldgk = Hq * d, Hk * d
+    if dq is None:
+        dq = torch.empty(q.shape, dtype=dt, device=index)
+    else:
+        ldgq = _rows(dq, "dq", dt, lead, Hq, d, index)
+    if dk is None:
+        dk = torch.empty(k.shape, dtype=dt, device=index)
+    else:
+        ldgk = _rows(dk, "dk", dt, lead, Hk, d, index)
+    dwq = None if q_weight is None else torch.empty(d, dtype=f32, device=index)
+    dwk = None if k_weight is None else torch.empty(d, dtype=f32, device=index)
+    lib, need, scratch = library(), 0, None
     if q_weight is not None or k_weight is not None:
-        ws_bytes = int(library().qk_norm_rotary_backward_workspace_bytes(tokens, d))
-        if workspace is None or workspace.numel() * workspace.element_size() < ws_bytes:
-            workspace = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=dev)
-    _same_device(dev, k, dq_out, dk_out, positions, freqs, q_weight, k_weight, gq, gk, workspace)
-    with torch.cuda.device(dev):
-        st = library().qk_norm_rotary_backward(
-            _ptr(dq_out), _ptr(dk_out), _ptr(q), _ptr(k), _ptr(positions), _ptr(freqs),
-            _ptr(q_weight), _ptr(k_weight), tokens, Hq, Hk, d, rd, lddq, lddk, ldq, ldk,
-            _choice(_NORMS, norm, "norm"), _choice(_LAYOUTS, layout, "layout"), eps, q_scale,
-            rotary_scale, code, _ptr(gq), _ptr(gk), ldgq, ldgk, _ptr(dwq), _ptr(dwk),
-            _ptr(workspace), ws_bytes, _stream(dev))
+        need = lib.qk_norm_rotary_backward_workspace_bytes(tokens, d)
+        scratch = _scratch(workspace, need, index)
+    st = _call(index, lib.qk_norm_rotary_backward, dq_out.data_ptr(), dk_out.data_ptr(),
+               q.data_ptr(), k.data_ptr(), _addr(positions), _addr(freqs), _addr(q_weight),
+               _addr(k_weight), tokens, Hq, Hk, d, rd, lddq, lddk, ldq, ldk,
+               _choice(_NORMS, norm, "norm"), _choice(_LAYOUTS, layout, "layout"), eps, q_scale,
+               rotary_scale, code, dq.data_ptr(), dk.data_ptr(), ldgq, ldgk, _addr(dwq),
+               _addr(dwk), _addr(scratch), need)
     _check(st, "qk_norm_rotary_backward")
-    return gq, gk, dwq, dwk
+    return dq, dk, dwq, dwk
 
 
 def rotary(x, positions, freqs, *, layout="half", rotary_scale=1.0, inverse=False, out=None):
     """Rotates the first ``2 len(freqs)`` channels of every head of ``x``
     [..., H, d] by ``positions * freqs``; ``inverse`` by the opposite angle (the
     backward).  ``out`` may be ``x``.  See ``ckda_rotary`` in include/ckda.h."""
-    code = _dtype_code(x)
-    H, tokens, ldx = _rows(x, "x")
-    lead, d = tuple(x.shape[:-2]), x.shape[-1]
+    code, dt = _dtype_code(x), x.dtype
+    lead, tokens, H, d, index = _lead(x, "x")
     if freqs is None:
         raise ValueError("freqs are needed")
-    rd, positions = _angles(positions, freqs, lead, d)
-    dev = x.device
-    o = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=dev)
-    ho, _, ldo = _rows(o, "out", x.dtype, lead, d)
-    if ho != H:
-        raise ValueError("out must have the heads of x")
-    _same_device(dev, positions, freqs, o)
-    with torch.cuda.device(dev):
-        st = library().ckda_rotary(_ptr(x), _ptr(positions), _ptr(freqs), tokens, H, d, rd, ldx,
-                                   _choice(_LAYOUTS, layout, "layout"), rotary_scale,
-                                   int(inverse), code, _ptr(o), ldo, _stream(dev))
+    ldx = _rows(x, "x", dt, lead, H, d, index)
+    rd = _angles(positions, freqs, lead, d, index)
+    ldo = H * d
+    if out is None:
+        out = torch.empty(x.shape, dtype=dt, device=index)
+    else:
+        ldo = _rows(out, "out", dt, lead, H, d, index)
+    st = _call(index, library().ckda_rotary, x.data_ptr(), positions.data_ptr(), freqs.data_ptr(),
+               tokens, H, d, rd, ldx, _choice(_LAYOUTS, layout, "layout"), rotary_scale,
+               1 if inverse else 0, code, out.data_ptr(), ldo)
     _check(st, "ckda_rotary")
-    return o
+    return out
