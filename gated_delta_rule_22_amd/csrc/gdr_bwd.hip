@@ -3,7 +3,7 @@
 // With dS' the gradient of the state behind the chunk and the forward's
 // symbols (gdr_chunk.hip):
 //
-//   dU = P^T dO + (gam_n / gam) K dS'        F = T^T dU   ( = dV )
+//   X = beta (P^T dO + (gam_n / gam) K dS')  F = X + T^T X   ( = dV )
 //   dS = gam_n dS' + Q^T (gam dO) - K^T (gam F)
 //   dP_ij = r_ij dO_i.U_j                    dA_ij = -r_ij F_i.U_j
 //   dQ = gam dO S^T + dP K
@@ -198,7 +198,7 @@ __global__ __launch_bounds__(2 * kThreads, 2) void reverse_kernel(
 #pragma unroll
       for (int r = 0; r < 4; ++r) S[i][r] = dS_T[sbase + (size_t)(16 * i + 4 * h + r) * DV];
   // The gate factors of a lane's tokens, from memory a chunk ahead.
-  f4 gam[4], last[4];
+  f4 gam[4], last[4], bet[4];
   float gn = 0.f;
   auto fetch_gates = [&](int c) {
     const float *g = reinterpret_cast<const float *>(rec_base + ((c0 + c) * Hv + hv) * kRecBwd +
@@ -207,6 +207,7 @@ __global__ __launch_bounds__(2 * kThreads, 2) void reverse_kernel(
     for (int jt = 0; jt < 4; ++jt) {
       gam[jt] = *reinterpret_cast<const f4 *>(g + kGam * C + 16 * jt + 4 * h);
       last[jt] = *reinterpret_cast<const f4 *>(g + kLast * C + 16 * jt + 4 * h);
+      bet[jt] = *reinterpret_cast<const f4 *>(g + kBeta * C + 16 * jt + 4 * h);
     }
     gn = g[kGam * C + C - 1];
   };
@@ -226,7 +227,7 @@ __global__ __launch_bounds__(2 * kThreads, 2) void reverse_kernel(
       *reinterpret_cast<bf8 *>(p + (KS + ks) * (DV / 16) * kFrag) = sf[ks].lo;
     }
     bf8 kf[KS][4];
-    f4 X[4];                             // dU
+    f4 X[4];                             // beta dU
     auto read_k = [&](int ks) {
 #pragma unroll
       for (int jt = 0; jt < 4; ++jt) kf[ks][jt] = rows_frag<DK>(K, 16 * jt, 32 * ks, lane);
@@ -265,12 +266,12 @@ __global__ __launch_bounds__(2 * kThreads, 2) void reverse_kernel(
 #pragma unroll
     for (int i = 0; i < MT; ++i) qd[i] = *reinterpret_cast<const f4 *>(tiles + (4 + i) * 1024);
 #pragma unroll
-    for (int jt = 0; jt < 4; ++jt) X[jt] = X[jt] * last[jt] + pd[jt];
+    for (int jt = 0; jt < 4; ++jt) X[jt] = (X[jt] * last[jt] + pd[jt]) * bet[jt];
     const Split x0 = split8(X[0], X[1]), x1 = split8(X[2], X[3]);
     fence_schedule();
     f4 F[4];
 #pragma unroll
-    for (int jt = 0; jt < 4; ++jt) F[jt] = 0.f;
+    for (int jt = 0; jt < 4; ++jt) F[jt] = X[jt];
 #pragma unroll
     for (int term = 0; term < 3; ++term)
 #pragma unroll
@@ -601,6 +602,7 @@ __global__ __launch_bounds__(kThreads, 2) void grad_kernel(
     if (h == 0 && tok < valid) dbeta[(row0 + tok) * Hv + hv] = db / (bet * bet);
 
     // Decays and masks, then dQ and dK from the triangular products.
+    float diag = 0.f;
 #pragma unroll
     for (int s = 0; s < 5; ++s) {
       const bool rows = s <= w;
@@ -612,10 +614,14 @@ __global__ __launch_bounds__(kThreads, 2) void grad_kernel(
       for (int r = 0; r < 4; ++r) {
         const float z = pow2(sign * ((ghi - go[r]) + (glo - lo[r])));
         const int behind = rows ? tok - first - r : first + r - tok;   // i - j
-        pp[s][r] = behind >= 0 ? pp[s][r] * z : 0.f;
+        if (s == w) diag += behind == 0 ? pp[s][r] : 0.f;
+        pp[s][r] = behind > 0 ? pp[s][r] * z : 0.f;
         xx[s][r] = behind > 0 ? -xx[s][r] * z : 0.f;
       }
     }
+    // dP_ii stays out of the operands: its parts of q.dq and k.dk cancel in dG,
+    // which may be far smaller than they are.
+    diag = over_quarters(diag);
     {
       // As operands: row block over tiles 0-1; over tiles 2-3 for w >= 2 (zero
       // for w < 2) or column block over tiles 0-1 for w < 2 (zero for w >= 2);
@@ -648,8 +654,8 @@ __global__ __launch_bounds__(kThreads, 2) void grad_kernel(
         b += w >= 2 ? r2 : none;
         c += w >= 2 ? none : r1 + r2;
         dG += sum4(qv * a) + sum4(kv * (b - c));
-        dQ[i] += a;
-        dK[i] += b + c;
+        dQ[i] += a + diag * kv;
+        dK[i] += b + c + diag * qv;
         computed(dQ[i]);
         computed(dK[i]);
         computed(dG);

@@ -4,8 +4,8 @@
 // e^(G_i - G_j), gam_i = e^(G_i) and S the state that enters the chunk:
 //
 //   Ah_ij = r_ij k_i.k_j (i > j)          P_ij = r_ij q_i.k_j (i >= j)
-//   T = diag(beta) (I + Ah diag(beta))^-1
-//   U = T (V - gam K S)                   O = gam Q S + P U
+//   I + T = (I + Ah diag(beta))^-1        X = V - gam K S
+//   U = beta (X + T X)                    O = gam Q S + P U
 //   S <- gam_n S + K^T (gam_n / gam U)
 //
 // The gate is one number per token and head, so decays scale rows and columns
@@ -222,11 +222,16 @@ __global__ __launch_bounds__(kThreads) void prepare_kernel(
 #pragma unroll
     for (int ks = 0; ks <= it / 2; ++ks) {
       const float *p = M + (16 * it + m) * kMStride + 32 * ks + 4 * h;
-      const float bi = s_b[16 * it + m];
-      // the tile right of an even diagonal one lies above the diagonal
-      f4 right = 0.f;
-      if (2 * ks + 1 <= it) right = *reinterpret_cast<const f4 *>(p + 16) * bi;
-      const Split s = split8(*reinterpret_cast<const f4 *>(p) * bi, right);
+      // without the unit diagonal, which the chain adds in fp32; the tile right
+      // of an even diagonal one lies above the diagonal
+      f4 left = *reinterpret_cast<const f4 *>(p), right = 0.f;
+      if (2 * ks + 1 <= it) right = *reinterpret_cast<const f4 *>(p + 16);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        if (2 * ks == it && 4 * h + r == m) left[r] = 0.f;
+        if (2 * ks + 1 == it && 4 * h + r == m) right[r] = 0.f;
+      }
+      const Split s = split8(left, right);
       *reinterpret_cast<bf8 *>(rec + kRecTh + frag_at(it, ks) + lane * 16) = s.hi;
       *reinterpret_cast<bf8 *>(rec + kRecTl + frag_at(it, ks) + lane * 16) = s.lo;
     }
@@ -258,7 +263,7 @@ template <int DK, int BV, bool STORE> struct ChainLds {
   static constexpr int kQ = kRec + kRecFwd;                      // the rest: !STORE
   static constexpr int kS = kQ + gdr::kTile<DK>, kSWave = 2 * (DK / 32) * kFrag;
   static constexpr int kU = kS + BV / 16 * kSWave;
-  static constexpr int kBytes = STORE ? kQ : kU + BV / 16 * 2 * kFrag;
+  static constexpr int kBytes = STORE ? kQ : kU + BV / 16 * 4 * kFrag;
 };
 
 template <int DK, int DV, int BV, bool STORE>
@@ -282,7 +287,7 @@ __global__ __launch_bounds__(8 * BV, 2) void chain_kernel(
   const char *K = lds + L::kK, *V = lds + L::kV, *R = lds + L::kRec, *Q = lds + L::kQ;
   const float *gate = reinterpret_cast<const float *>(R + kRecGate);
   char *s_S = lds + L::kS + wave * L::kSWave + lane * 16;
-  char *s_U = lds + L::kU + wave * 2 * kFrag + lane * 16;
+  char *s_U = lds + L::kU + wave * 4 * kFrag + lane * 16;
 
   if (threadIdx.x >= kHelp) {            // helper waves
     const int t = threadIdx.x - kHelp;
@@ -346,15 +351,17 @@ __global__ __launch_bounds__(8 * BV, 2) void chain_kernel(
       lds_barrier();                     // B
       put(next);                         // before the stores, which loads' waits count too
       if (!STORE) {
-        // One term of P and of U: each is within 2^-9 of its value, and so is
-        // the bf16 output itself.
-        const bf8 u0 = *reinterpret_cast<const bf8 *>(s_U);
-        const bf8 u1 = *reinterpret_cast<const bf8 *>(s_U + kFrag);
+        // One term of P: it is within 2^-9 of its value, and so is the bf16
+        // output itself.
+        const Split u0 = {*reinterpret_cast<const bf8 *>(s_U),
+                          *reinterpret_cast<const bf8 *>(s_U + 2 * kFrag)};
+        const Split u1 = {*reinterpret_cast<const bf8 *>(s_U + kFrag),
+                          *reinterpret_cast<const bf8 *>(s_U + 3 * kFrag)};
 #pragma unroll
         for (int it = 0; it < 4; ++it) {
 #pragma unroll
           for (int ks = 0; ks <= it / 2; ++ks)
-            a[it] = mfma(ks ? u1 : u0, p[frag_at(it, ks) / kFrag], a[it]);
+            a[it] = dot2(ks ? u1 : u0, p[frag_at(it, ks) / kFrag], a[it]);
           const int tok = c * C + 16 * it + m;
           if (tok < len)
             *reinterpret_cast<bf4 *>(o + ((row0 + tok) * Hv + hv) * DV + col + 4 * h) =
@@ -377,7 +384,7 @@ __global__ __launch_bounds__(8 * BV, 2) void chain_kernel(
 
   // The gate factors of a lane's tokens come from memory a chunk ahead: read
   // from LDS they would be 9 cycles of its time each for 64 bytes.
-  f4 gam[4], last[4];
+  f4 gam[4], last[4], bet[4];
   float gn = 0.f;
   auto fetch_gates = [&](int c) {
     const float *g = reinterpret_cast<const float *>(rec_base + ((c0 + c) * Hv + hv) * kRec +
@@ -386,6 +393,7 @@ __global__ __launch_bounds__(8 * BV, 2) void chain_kernel(
     for (int it = 0; it < 4; ++it) {
       gam[it] = *reinterpret_cast<const f4 *>(g + kGam * C + 16 * it + 4 * h);
       last[it] = *reinterpret_cast<const f4 *>(g + kLast * C + 16 * it + 4 * h);
+      bet[it] = *reinterpret_cast<const f4 *>(g + kBeta * C + 16 * it + 4 * h);
     }
     gn = g[kGam * C + C - 1];
   };
@@ -453,7 +461,7 @@ __global__ __launch_bounds__(8 * BV, 2) void chain_kernel(
     fence_schedule();
     f4 U[4];
 #pragma unroll
-    for (int it = 0; it < 4; ++it) U[it] = 0.f;
+    for (int it = 0; it < 4; ++it) U[it] = X[it];
     // the four tiles' products turn by turn: each waits for its own last one
 #pragma unroll
     for (int term = 0; term < 3; ++term)
@@ -469,16 +477,18 @@ __global__ __launch_bounds__(8 * BV, 2) void chain_kernel(
     for (int i = 0; i < MT; ++i) S[i] *= gn;
 #pragma unroll
     for (int i = 0; i < MT; ++i) kt[1][i] = cols_frag<DK>(K, 32, 16 * i, lane);
-    if (STORE) {
-      char *p = U_keep + (((c0 + c) * Hv + hv) * (4 * (DV / 16)) + col / 16) * kFrag + lane * 16;
+#pragma unroll
+    for (int it = 0; it < 4; ++it) U[it] *= bet[it];
+    {
       const Split u0 = split8(U[0], U[1]), u1 = split8(U[2], U[3]);
+      char *p = STORE ? U_keep + (((c0 + c) * Hv + hv) * (4 * (DV / 16)) + col / 16) * kFrag +
+                            lane * 16
+                      : s_U;
+      constexpr int step = STORE ? (DV / 16) * kFrag : kFrag;
       *reinterpret_cast<bf8 *>(p) = u0.hi;
-      *reinterpret_cast<bf8 *>(p + (DV / 16) * kFrag) = u1.hi;
-      *reinterpret_cast<bf8 *>(p + 2 * (DV / 16) * kFrag) = u0.lo;
-      *reinterpret_cast<bf8 *>(p + 3 * (DV / 16) * kFrag) = u1.lo;
-    } else {
-      *reinterpret_cast<bf8 *>(s_U) = join(round4(U[0]), round4(U[1]));
-      *reinterpret_cast<bf8 *>(s_U + kFrag) = join(round4(U[2]), round4(U[3]));
+      *reinterpret_cast<bf8 *>(p + step) = u1.hi;
+      *reinterpret_cast<bf8 *>(p + 2 * step) = u0.lo;
+      *reinterpret_cast<bf8 *>(p + 3 * step) = u1.lo;
     }
     fence_schedule();
     lds_barrier();                       // B
