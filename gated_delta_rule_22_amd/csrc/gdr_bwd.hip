@@ -10,9 +10,11 @@
 //   dK = [-gam F S^T + dA K] + [dP^T Q + dA^T K + (gam_n / gam) U dS'^T]
 //   dbeta = F.U / beta^2
 //   dG_i = q_i.dQ_i + k_i.dK_i[first bracket] - k_i.dK_i[second bracket]
-//   dg_t = sum_{i >= t} dG_i + sum_j w_j + gam_n <S, dS'>
+//   dg_t = sum_{i >= t} dG_i + sum_{j < t} w_j + gam_n <S, dS'>
 //
-// where w_j is the last term's part of k_j.dK_j.  (F and U carry a factor beta
+// where w_j is the last term's part of k_j.dK_j, which dG_j leaves out (it
+// could be added for all j and taken off for j >= t, but a fast gate's gradient
+// is far smaller than the w_j that would cancel).  (F and U carry a factor beta
 // each, and beta is kept off zero by kBetaFloor, so F.U / beta^2 holds at
 // beta = 0 too.)
 //
@@ -44,7 +46,7 @@ template <int DK> struct ReverseLds {
   static constexpr int kWave = (4 + DK / 16) * 1024;   // a wave's tiles
   static constexpr int kK = 0, kT = kTile<DK>, kQ = kT + 2 * kTri, kD = kQ + kTile<DK>;
   static constexpr int kP = kD + kTile<64>, kGam = kP + 2 * kTri;
-  static constexpr int kTiles = kGam + C * 4, kBytes = kTiles + 4 * kWave;
+  static constexpr int kTiles = kGam + 2 * C * 4, kBytes = kTiles + 4 * kWave;
 };
 
 template <int DK, int DV>
@@ -98,14 +100,14 @@ __global__ __launch_bounds__(2 * kThreads, 2) void reverse_kernel(
         const int at = (t + i * kThreads) * 16;
         gp.r[i] = load16(rec + (at < kTri ? kRecPh + at : kRecPl + at - kTri), true);
       }
-      gam = reinterpret_cast<const float *>(rec + kRecGate)[kGam * C + t % C];
+      gam = reinterpret_cast<const float *>(rec + kRecGate)[(t & C ? kDiagP : kGam) * C + t % C];
     };
     auto put_own = [&](int c) {
       const int valid = min(C, len - c * C);
       gq.store(lds + L::kQ, valid, t);
       gd.store(lds + L::kD, valid, t);
       gp.store_mixed(lds + L::kP, t);
-      if (t < C) reinterpret_cast<float *>(lds + L::kGam)[t] = gam;
+      if (t < 2 * C) reinterpret_cast<float *>(lds + L::kGam)[t] = gam;
     };
     f4 pd[4], qd[MT];
     auto ahead = [&]() {
@@ -117,6 +119,7 @@ __global__ __launch_bounds__(2 * kThreads, 2) void reverse_kernel(
 #pragma unroll
       for (int jt = 0; jt < 4; ++jt) {
         d[jt] = *reinterpret_cast<const f4 *>(s_gam + 16 * jt + 4 * h);
+        pd[jt] = *reinterpret_cast<const f4 *>(s_gam + C + 16 * jt + 4 * h);   // P_ii
 #pragma unroll
         for (int ks = jt / 2; ks < 2; ++ks)
           pf[jt][ks] = {tri_frag_t(P, jt, ks, lane), tri_frag_t(P + kTri, jt, ks, lane)};
@@ -128,8 +131,9 @@ __global__ __launch_bounds__(2 * kThreads, 2) void reverse_kernel(
       const bf8 d0 = join(r[0], r[1]), d1 = join(r[2], r[3]);
 #pragma unroll
       for (int jt = 0; jt < 4; ++jt) {
-        pd[jt] = 0.f;
-        d[jt] *= widen4(r[jt]);
+        const f4 x = widen4(r[jt]);
+        pd[jt] *= x;
+        d[jt] *= x;
       }
 #pragma unroll
       for (int term = 0; term < 2; ++term)
@@ -331,7 +335,7 @@ __global__ __launch_bounds__(2 * kThreads, 2) void reverse_kernel(
 // registers.
 template <int DK, int DV> struct GradLds {
   static constexpr int kK = 0, kQ = kK + kTile<DK>, kGate = kQ + kTile<DK>;
-  static constexpr int kSum = kGate + kGateBytes, kX = kSum + 256 + 64;
+  static constexpr int kSum = kGate + kGateBytes, kX = kSum + 512 + 64;
   static constexpr int kD = kX, kU = kD + kTile<64>, kF = kU + 16 * kFrag;
   static constexpr int kBytes = kF + 16 * kFrag;
   static_assert(kX + 256 * DK <= kBytes, "a state's 64 columns fit the window");
@@ -388,7 +392,7 @@ __global__ __launch_bounds__(kThreads, 2) void grad_kernel(
   const int tok = 16 * w + m;            // this lane's token
   const char *K = lds + L::kK, *Q = lds + L::kQ, *D = lds + L::kD;
   float *gate = reinterpret_cast<float *>(lds + L::kGate);
-  float *s_dG = reinterpret_cast<float *>(lds + L::kSum), *s_n = s_dG + C;
+  float *s_dG = reinterpret_cast<float *>(lds + L::kSum), *s_w = s_dG + C, *s_n = s_w + C;
 
   {
     Stage<DK> gk, gq;
@@ -434,7 +438,7 @@ __global__ __launch_bounds__(kThreads, 2) void grad_kernel(
       const float *rg = reinterpret_cast<const float *>(rec_base + ch * kRecBwd + kRecGate);
       const float ga = rg[t], gb = rg[kThreads + t % C];
       gate[t] = ga;
-      if (t < C) gate[kThreads + t] = gb;
+      if (t < C) gate[kThreads + t] = gb;   // five of the six rows
     }
     put_rows();
     __syncthreads();
@@ -661,21 +665,25 @@ __global__ __launch_bounds__(kThreads, 2) void grad_kernel(
         computed(dG);
       }
     }
-    dG = over_quarters(dG - ws);
-    if (h == 0) s_dG[tok] = dG;
-    // sum_j w_j + gam_n <S, dS'> over the workgroup
-    float n = ws + gn * dot;
-    for (int o = 32; o > 0; o >>= 1) n += __shfl_xor(n, o);
-    if (lane == 0) s_n[w] = n;
+    dG = over_quarters(dG);
+    ws = over_quarters(ws);
+    if (h == 0) {
+      s_dG[tok] = dG;
+      s_w[tok] = ws;
+    }
+    for (int o = 32; o > 0; o >>= 1) dot += __shfl_xor(dot, o);
+    if (lane == 0) s_n[w] = dot;
     __syncthreads();
     if (w == 0) {
-      float z = s_dG[lane];
+      float z = s_dG[lane], y = s_w[lane];
 #pragma unroll
       for (int o = 1; o < 64; o <<= 1) {
-        const float v = __shfl_down(z, o);
-        if (lane + o < 64) z += v;
+        const float a = __shfl_down(z, o), b = __shfl_up(y, o);
+        if (lane + o < 64) z += a;
+        if (lane >= o) y += b;
       }
-      z += (s_n[0] + s_n[1]) + (s_n[2] + s_n[3]);
+      y = __shfl_up(y, 1);               // over the tokens before this one
+      z += (lane ? y : 0.f) + gn * ((s_n[0] + s_n[1]) + (s_n[2] + s_n[3]));
       if (lane < valid) {
         const size_t gi = (row0 + lane) * Hv + hv;
         dg[gi] = g[gi] < (float)kGateFloor ? 0.f : z;   // a floored gate is constant

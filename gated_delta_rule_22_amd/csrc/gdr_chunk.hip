@@ -137,7 +137,9 @@ __global__ __launch_bounds__(kThreads) void prepare_kernel(
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const float x = (hi_i - hj[r]) + (lo_i - lj[r]);
-          p[r] = i >= 16 * jt + 4 * h + r ? p[r] * pow2(x) : 0.f;
+          const int j = 16 * jt + 4 * h + r;
+          if (BWD && i == j) gate[kDiagP * C + i] = p[r];
+          p[r] = (BWD ? i > j : i >= j) ? p[r] * pow2(x) : 0.f;
         }
         return p;
       };
