@@ -143,23 +143,31 @@ extern "C" int gdr_decode_step(const void *q, const void *k, const void *v, cons
 
 namespace {
 
-// Workspace of the backward.  bf16 inputs: the sequence table, then per
-// (chunk, value head) the records, S, U, dS and F.  fp32 inputs: the table,
-// the expanded q, k, gates and their gradients, then the fp64 backward's own
-// workspace (its table included).
+// fp32 inputs take the per-channel fp64 backward, and so do bf16 inputs of no
+// more than this many (token, value head) pairs: an fp32 gradient of so few can
+// be the small difference of a handful of terms, each within 2^-18 in the
+// chunkwise path, where more of them average out.  (130 us against 45 us.)
+constexpr size_t kFewRows = 128;
+bool gdr_bwd_f64(int B, int T, int Hv, int in_dtype) {
+  return in_dtype == CKDA_F32 || (size_t)B * T * Hv <= kFewRows;
+}
+
+// Workspace of the backward: the sequence table, then for the chunkwise path
+// per (chunk, value head) the records, S, U, dS and F; for the fp64 path the
+// expanded operands and their gradients and its own workspace.
 struct GdrBwdLayout {
   size_t n_chunks, total;
-  size_t rec, S, U, dS, F;               // bf16
-  size_t x[6], inner;                    // fp32
+  size_t rec, S, U, dS, F;
+  size_t wide[6], values[3], inner;      // [rows, Hv, dk], [rows, Hv, dv]
 };
 
 GdrBwdLayout gdr_bwd_layout(int B, int T, int Hv, int dk, int dv, int N, int in_dtype) {
   GdrBwdLayout L{};
   L.n_chunks = chunks_ub(B, T, N);
-  const size_t ch = L.n_chunks * Hv;
+  const size_t ch = L.n_chunks * Hv, rows = (size_t)B * T * Hv;
   size_t at = align256(sizeof(int32_t) * (4 * (size_t)N + 1));
   auto take = [&](size_t n) { const size_t p = at; at += align256(n); return p; };
-  if (in_dtype == CKDA_BF16) {
+  if (!gdr_bwd_f64(B, T, Hv, in_dtype)) {
     const GdrBwdBytes b = gdr_backward_bytes(dk, dv);
     L.rec = take(ch * b.rec);
     L.S = take(ch * b.state);
@@ -167,7 +175,9 @@ GdrBwdLayout gdr_bwd_layout(int B, int T, int Hv, int dk, int dv, int N, int in_
     L.dS = take(ch * b.state);
     L.F = take(ch * b.rows);
   } else {
-    for (size_t &x : L.x) x = take((size_t)B * T * Hv * dk * 4);
+    for (size_t &x : L.wide) x = take(rows * dk * 4);
+    if (in_dtype == CKDA_BF16)
+      for (size_t &x : L.values) x = take(rows * dv * 4);
     L.inner = take(ckda_backward_workspace_bytes(B, T, Hv, dk, dv, N, CKDA_F32));
   }
   L.total = at;
@@ -223,7 +233,7 @@ extern "C" int gdr_backward(const void *q, const void *k, const void *v, const f
   const Seqs seqs{seq_table(workspace, N), packed ? -1 : T};
   if (packed && launch_seq_table(cu_seqlens, B, T, N, seqs.tab, st) != hipSuccess)
     return CKDA_ERR_LAUNCH;
-  if (in_dtype == CKDA_BF16) {
+  if (!gdr_bwd_f64(B, T, Hv, in_dtype)) {
     GdrBwdArgs a{};
     a.fwd.q = q; a.fwd.k = k; a.fwd.v = v; a.fwd.g = g; a.fwd.beta = beta; a.fwd.S0 = S0;
     a.fwd.seqs = seqs; a.fwd.n_chunks_ub = L.n_chunks;
@@ -233,22 +243,27 @@ extern "C" int gdr_backward(const void *q, const void *k, const void *v, const f
     a.dq = dq; a.dk = d_k; a.dv = d_v; a.dg = dg; a.dbeta = dbeta; a.dS0 = dS0;
     return launch_gdr_backward(a, st) == hipSuccess ? CKDA_OK : CKDA_ERR_LAUNCH;
   }
-  float *x[6];
-  for (int i = 0; i < 6; ++i) x[i] = reinterpret_cast<float *>(w + L.x[i]);
-  if (rows > 0 &&
-      launch_gdr_expand(static_cast<const float *>(q), static_cast<const float *>(k), g, rows, Hk,
-                        Hv, dk, x[0], x[1], x[2], st) != hipSuccess)
-    return CKDA_ERR_LAUNCH;
+  GdrF64Args a{};
+  a.q = q; a.k = k; a.v = v; a.d_o = d_o; a.g = g;
+  a.seqs = seqs; a.rows = rows;
+  a.N = N; a.Hk = Hk; a.Hv = Hv; a.dk = dk; a.dv = dv;
+  float **wide[] = {&a.qx, &a.kx, &a.gx, &a.dqx, &a.dkx, &a.dgx};
+  for (int i = 0; i < 6; ++i) *wide[i] = reinterpret_cast<float *>(w + L.wide[i]);
+  if (in_dtype == CKDA_BF16) {
+    float **values[] = {&a.vx, &a.dox, &a.dvx};
+    for (int i = 0; i < 3; ++i) *values[i] = reinterpret_cast<float *>(w + L.values[i]);
+  }
+  a.dq = dq; a.dk_out = d_k; a.dv_out = d_v; a.dg = dg;
+  if (rows > 0 && launch_gdr_expand(a, in_dtype, st) != hipSuccess) return CKDA_ERR_LAUNCH;
   // The per-channel backward, signs ignored (the gates are positive).
-  if (int s = kda_backward(x[0], x[1], v, x[2], beta, S0, cu_seqlens, B, T, Hv, dk, dv, N, CKDA_F32,
-                           static_cast<const float *>(d_o), dS_T, x[3], x[4],
-                           static_cast<float *>(d_v), x[5], dbeta, dS0, w + L.inner,
-                           L.total - L.inner, stream))
+  const bool wide_in = in_dtype == CKDA_BF16;
+  if (int s = kda_backward(a.qx, a.kx, wide_in ? a.vx : v, a.gx, beta, S0, cu_seqlens, B, T, Hv, dk,
+                           dv, N, CKDA_F32,
+                           wide_in ? a.dox : static_cast<const float *>(d_o), dS_T, a.dqx, a.dkx,
+                           wide_in ? a.dvx : static_cast<float *>(d_v), a.dgx, dbeta, dS0,
+                           w + L.inner, L.total - L.inner, stream))
     return s;
-  if (rows > 0 &&
-      launch_gdr_collect(x[3], x[4], x[5], g, seqs, N, rows, Hk, Hv, dk, static_cast<float *>(dq),
-                         static_cast<float *>(d_k), dg, st) != hipSuccess)
-    return CKDA_ERR_LAUNCH;
+  if (rows > 0 && launch_gdr_collect(a, in_dtype, st) != hipSuccess) return CKDA_ERR_LAUNCH;
   return CKDA_OK;
 }
 

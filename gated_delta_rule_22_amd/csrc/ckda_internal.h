@@ -160,12 +160,21 @@ struct GdrBwdArgs {
 struct GdrBwdBytes { size_t rec, state, rows; };   // rec; S and dS; U and F
 GdrBwdBytes gdr_backward_bytes(int dk, int dv);
 hipError_t launch_gdr_backward(const GdrBwdArgs &a, hipStream_t stream);
-// fp32 inputs' backward: layouts to and from the per-channel fp64 backward.
-hipError_t launch_gdr_expand(const float *q, const float *k, const float *g, size_t rows, int Hk,
-                             int Hv, int dk, float *qx, float *kx, float *gx, hipStream_t stream);
-hipError_t launch_gdr_collect(const float *dqx, const float *dkx, const float *dgx,
-                              const float *g, Seqs seqs, int N, size_t rows, int Hk, int Hv,
-                              int dk, float *dq, float *dk_out, float *dg, hipStream_t stream);
+// Layouts to and from the per-channel fp64 backward: everything in fp32 and per
+// value head and channel.  vx, dox and dvx are NULL where v, d_o and dv are
+// fp32 themselves.
+struct GdrF64Args {
+    const void *q, *k, *v, *d_o;
+    const float *g;
+    Seqs seqs;
+    size_t rows;
+    int N, Hk, Hv, dk, dv;
+    float *qx, *kx, *gx, *vx, *dox, *dqx, *dkx, *dgx, *dvx;
+    void *dq, *dk_out, *dv_out;
+    float *dg;
+};
+hipError_t launch_gdr_expand(const GdrF64Args &a, int in_dtype, hipStream_t stream);
+hipError_t launch_gdr_collect(const GdrF64Args &a, int in_dtype, hipStream_t stream);
 
 // ---------------------------------------------------------------- norm and rotation
 struct RotaryArgs {

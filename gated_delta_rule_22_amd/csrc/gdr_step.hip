@@ -6,6 +6,8 @@
 // (the recurrence of ckda_decode_step with one positive gate per head instead
 // of one signed gate per key channel.)  Head h reads query/key head
 // h / (Hv / Hk).
+#include <type_traits>
+
 #include "ckda_internal.h"
 
 namespace ckda {
@@ -191,35 +193,43 @@ __global__ __launch_bounds__(kThreads) void gdr_token_kernel(
       S_T[sbase + (size_t)(16 * (i >> 2) + 4 * rr + (i & 3)) * DV] = S[i];
 }
 
-// ------------------------------------------------- fp32 inputs' backward
-// The fp64 backward of the per-channel recurrence takes q, k and gates per
-// value head and channel.  These kernels lay them out and sum its gradients
-// back: over a group's heads for q and k, over the channels for the gate
-// (dg = a sum_c dalpha_c, a = exp g).  Gates below e^-87 count as e^-87, the
-// smallest that fp32 holds to full precision.
+// ------------------------------------------------- the backward in fp64
+// The fp64 backward of the per-channel recurrence takes fp32 operands, q, k and
+// gates per value head and channel.  These kernels lay them out and sum its
+// gradients back: over a group's heads for q and k, over the channels for the
+// gate (dg = a sum_c dalpha_c, a = exp g).  Gates below e^-87 count as e^-87,
+// the smallest that fp32 holds to full precision.
 __device__ __forceinline__ float linear_gate(float g) { return expf(g < -87.f ? -87.f : g); }
 
+template <typename TIn>
 __global__ __launch_bounds__(kThreads) void gdr_expand_kernel(
-    const float *__restrict__ q, const float *__restrict__ k, const float *__restrict__ g,
-    size_t rows, int Hk, int Hv, int dk, float *__restrict__ qx, float *__restrict__ kx,
-    float *__restrict__ gx) {
-  const size_t total = rows * Hv * dk;
-  for (size_t i = (size_t)blockIdx.x * kThreads + threadIdx.x; i < total;
-       i += (size_t)gridDim.x * kThreads) {
+    const TIn *__restrict__ q, const TIn *__restrict__ k, const TIn *__restrict__ v,
+    const TIn *__restrict__ d_o, const float *__restrict__ g, size_t rows, int Hk, int Hv, int dk,
+    int dv, float *__restrict__ qx, float *__restrict__ kx, float *__restrict__ gx,
+    float *__restrict__ vx, float *__restrict__ dox) {
+  const size_t total = rows * Hv * dk, step = (size_t)gridDim.x * kThreads;
+  const size_t first = (size_t)blockIdx.x * kThreads + threadIdx.x;
+  for (size_t i = first; i < total; i += step) {
     const size_t rh = i / dk;
     const int c = (int)(i - rh * dk), h = (int)(rh % Hv);
     const size_t src = ((rh / Hv) * Hk + h / (Hv / Hk)) * dk + c;
-    qx[i] = q[src];
-    kx[i] = k[src];
+    qx[i] = to_f32(q[src]);
+    kx[i] = to_f32(k[src]);
     gx[i] = linear_gate(g[rh]);
   }
+  if (vx)                                // NULL: v and d_o are fp32 already
+    for (size_t i = first; i < rows * Hv * dv; i += step) {
+      vx[i] = to_f32(v[i]);
+      dox[i] = to_f32(d_o[i]);
+    }
 }
 
+template <typename TIn>
 __global__ __launch_bounds__(kThreads) void gdr_collect_kernel(
     const float *__restrict__ dqx, const float *__restrict__ dkx, const float *__restrict__ dgx,
-    const float *__restrict__ g, int N, size_t rows, int Hk,
-    int Hv, int dk, float *__restrict__ dq, float *__restrict__ dk_out, float *__restrict__ dg,
-    Seqs seqs) {
+    const float *__restrict__ dvx, const float *__restrict__ g, int N, size_t rows, int Hk, int Hv,
+    int dk, int dv, TIn *__restrict__ dq, TIn *__restrict__ dk_out, TIn *__restrict__ dv_out,
+    float *__restrict__ dg, Seqs seqs) {
   // One wave per (token, query/key head).  Rows outside every sequence are
   // left alone, as everywhere: a row belongs to the last sequence that starts
   // at or before it, if that sequence reaches it.
@@ -243,8 +253,8 @@ __global__ __launch_bounds__(kThreads) void gdr_collect_kernel(
         a += dqx[at];
         b += dkx[at];
       }
-      dq[w * dk + c] = a;
-      dk_out[w * dk + c] = b;
+      put(dq + w * dk + c, a);
+      put(dk_out + w * dk + c, b);
     }
     for (int r = 0; r < rep; ++r) {
       const size_t rh = row * Hv + hk * rep + r;
@@ -252,7 +262,9 @@ __global__ __launch_bounds__(kThreads) void gdr_collect_kernel(
       double s = 0.;
       for (int c = lane; c < dk; c += 64) s += (double)dgx[rh * dk + c] * al;
       for (int off = 32; off > 0; off >>= 1) s += __shfl_xor(s, off);
-      if (lane == 0) dg[rh] = (float)s;
+      if (lane == 0) dg[rh] = g[rh] < -87.f ? 0.f : (float)s;
+      if (dvx)
+        for (int c = lane; c < dv; c += 64) put(dv_out + rh * dv + c, dvx[rh * dv + c]);
     }
   }
 }
@@ -319,20 +331,30 @@ hipError_t launch_gdr_token(const GdrArgs &a, int in_dtype, hipStream_t stream) 
                                : token_typed<float>(a, stream);
 }
 
-hipError_t launch_gdr_expand(const float *q, const float *k, const float *g, size_t rows, int Hk,
-                             int Hv, int dk, float *qx, float *kx, float *gx,
-                             hipStream_t stream) {
-  hipLaunchKernelGGL(gdr_expand_kernel, dim3(blocks_for(rows * Hv * dk)), dim3(kThreads), 0,
-                     stream, q, k, g, rows, Hk, Hv, dk, qx, kx, gx);
+hipError_t launch_gdr_expand(const GdrF64Args &a, int in_dtype, hipStream_t stream) {
+  const dim3 grid(blocks_for(a.rows * a.Hv * (a.dk > a.dv ? a.dk : a.dv)));
+  auto run = [&](auto *q) {
+    using T = std::remove_pointer_t<decltype(q)>;
+    hipLaunchKernelGGL(gdr_expand_kernel<T>, grid, dim3(kThreads), 0, stream, q,
+                       static_cast<const T *>(a.k), static_cast<const T *>(a.v),
+                       static_cast<const T *>(a.d_o), a.g, a.rows, a.Hk, a.Hv, a.dk, a.dv, a.qx,
+                       a.kx, a.gx, a.vx, a.dox);
+  };
+  if (in_dtype == CKDA_BF16) run(static_cast<__hip_bfloat16 *>(const_cast<void *>(a.q)));
+  else run(static_cast<float *>(const_cast<void *>(a.q)));
   return hipGetLastError();
 }
 
-hipError_t launch_gdr_collect(const float *dqx, const float *dkx, const float *dgx,
-                              const float *g, Seqs seqs, int N, size_t rows, int Hk, int Hv,
-                              int dk, float *dq, float *dk_out, float *dg, hipStream_t stream) {
-  hipLaunchKernelGGL(gdr_collect_kernel, dim3(blocks_for(rows * Hk * 64)), dim3(kThreads), 0,
-                     stream, dqx, dkx, dgx, g, N, rows, Hk, Hv, dk, dq,
-                     dk_out, dg, seqs);
+hipError_t launch_gdr_collect(const GdrF64Args &a, int in_dtype, hipStream_t stream) {
+  const dim3 grid(blocks_for(a.rows * a.Hk * 64));
+  auto run = [&](auto *dq) {
+    using T = std::remove_pointer_t<decltype(dq)>;
+    hipLaunchKernelGGL(gdr_collect_kernel<T>, grid, dim3(kThreads), 0, stream, a.dqx, a.dkx, a.dgx,
+                       a.dvx, a.g, a.N, a.rows, a.Hk, a.Hv, a.dk, a.dv, dq,
+                       static_cast<T *>(a.dk_out), static_cast<T *>(a.dv_out), a.dg, a.seqs);
+  };
+  if (in_dtype == CKDA_BF16) run(static_cast<__hip_bfloat16 *>(a.dq));
+  else run(static_cast<float *>(a.dq));
   return hipGetLastError();
 }
 

@@ -351,8 +351,9 @@ int ckda_decode_step(const void *q, const void *k, const void *v, const float *g
  * applied: q arrives pre-scaled (qk_norm_rotary does that).
  *
  * Gates: any g, nominally <= 0.  Log-gates below -1e4 (so also -infinity, a
- * full reset of the state) count as -1e4; backward with fp32 inputs: below
- * -87 as -87.  A NaN in any input reaches only the outputs of the heads that
+ * full reset of the state) count as -1e4; a backward that runs in fp64 (see
+ * gdr_backward) counts those below -87 as -87.  A gate that is raised so has
+ * gradient 0.  A NaN in any input reaches only the outputs of the heads that
  * read it, in its own sequence.
  */
 
@@ -403,14 +404,14 @@ size_t gdr_backward_workspace_bytes(int B, int T, int Hk, int Hv, int dk, int dv
  *  dq, d_k     [B, T, Hk, dk]  in_dtype, summed over the value heads that share
  *              the head
  *  d_v         [B, T, Hv, dv]  in_dtype
- *  dg, dbeta   [B, T, Hv]      fp32 (dg: of the log-gate; 0 where it is below
- *              the floor, for bf16 inputs)
+ *  dg, dbeta   [B, T, Hv]      fp32 (dg: of the log-gate)
  *  dS0         [N, Hv, dk, dv] fp32, or NULL to skip
  *
  * No output overlaps an input, another output or the workspace.  Numerics:
  * bf16 inputs as the forward's states (fp32 accumulation, fp32 operands in two
- * bf16 terms), also where only bf16 gradients depend on it; fp32 inputs run
- * ckda_backward's fp64 path on expanded operands.
+ * bf16 terms), also where only bf16 gradients depend on it; fp32 inputs, and
+ * bf16 inputs of at most 128 (token, value head) pairs, run ckda_backward's
+ * fp64 path on expanded operands.
  */
 int gdr_backward(const void *q, const void *k, const void *v, const float *g, const float *beta,
                  const float *S0, const int32_t *cu_seqlens, int B, int T, int Hk, int Hv, int dk,

@@ -4,8 +4,9 @@ token recurrence, and against differences of its forward.
 Tolerances (2-norm, relative), as for the forward: an fp32 gradient of bf16
 inputs passes the forward's chain, the reverse chain and the gradient's own
 products, three times the roundings of a state, rounded up to a power of two:
-2^-13; bf16 gradients add one rounding of 2^-8.  fp32 inputs run in fp64 and
-round their gates (2^-24, over up to 2^8 tokens), intermediates to fp32 and the
+2^-13; bf16 gradients add one rounding of 2^-8.  fp32 inputs (and bf16 calls of
+at most 128 token-head pairs, held to the same bounds as longer ones) run in
+fp64 and round their gates (2^-24, over up to 2^8 tokens), intermediates to fp32 and the
 result once: 2^-18."""
 import pytest
 import torch
@@ -96,9 +97,10 @@ def test_no_states(dtype):
     check(inputs(7, [70, 129], 2, 2, 64, 128, dtype, s0=False), [70, 129], dtype, 3, False)
 
 
-def test_resets():
-    """Log-gates of -infinity forget everything and have no gradient."""
-    lens = [140]
+@pytest.mark.parametrize("lens", [[140], [20]])
+def test_resets(lens):
+    """Log-gates of -infinity forget everything and have no gradient (the
+    chunkwise path, and the fp64 one that short calls take)."""
     x = inputs(9, lens, 1, 2, 128, 128, BF, "resets")
     do, dS = upstream(4, x, lens, BF)
     got = run(x, do, dS, lens)
