@@ -15,7 +15,6 @@
 // prepare_kernel makes T, P and the gate factors of every chunk in parallel;
 // chain_kernel runs the chunks of a (sequence, head) in order.
 #include "gdr_chunk.h"
-#include <stdlib.h>
 
 namespace ckda {
 using namespace gdr;
@@ -537,9 +536,13 @@ hipError_t launch_chain(const GdrArgs &a, char *rec, char *S, char *U, hipStream
   return hipGetLastError();
 }
 
-// Columns of a workgroup.  64 load a chunk's operands once for twice the
-// columns; 32 halve the LDS traffic of a compute unit, which bounds the chunk,
-// and pay where half the chip would stand idle.
+// Columns of a workgroup of STORE; without it, 64.  64 load a chunk's operands once for twice the
+// columns, and leave the helpers twice the threads: with an output they have so
+// much to do that 32 columns lose at any size (a layer of 128 heads 368 against
+// 203 us, one sequence of 16 heads 223 against 175).  Without one, 32 halve the
+// LDS traffic of a compute unit and win where half the chip would stand idle
+// (56 heads of 64 columns 74 against 86 us), and lose where it would not (a
+// layer 300 against 240).
 int chain_columns(int pairs, int dv) {
   return (size_t)pairs * (dv / 64) <= 128 ? 32 : 64;
 }
@@ -555,9 +558,10 @@ hipError_t forward_typed(const GdrArgs &a, char *rec, char *S, char *U, hipStrea
                        q, k, a.g, a.beta, a.seqs, a.N, a.Hk, a.Hv, rec);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }
-  return chain_columns(a.N * a.Hv, DV) == 64
-             ? launch_chain<DK, DV, 64, STORE>(a, rec, S, U, st)
-             : launch_chain<DK, DV, 32, STORE>(a, rec, S, U, st);
+  if constexpr (STORE)
+    if (chain_columns(a.N * a.Hv, DV) == 32)
+      return launch_chain<DK, DV, 32, STORE>(a, rec, S, U, st);
+  return launch_chain<DK, DV, 64, STORE>(a, rec, S, U, st);
 }
 
 template <bool STORE>
