@@ -21,7 +21,7 @@ int gdr_shape_status(int B, int T, int Hk, int Hv, int dk, int dv, int N, int in
     return CKDA_ERR_SHAPE;
   if (Hv % Hk != 0) return CKDA_ERR_SHAPE;
   if ((long long)B * T * Hv >= (1LL << 31)) return CKDA_ERR_SHAPE;
-  if ((long long)N * Hv >= (1LL << 28)) return CKDA_ERR_SHAPE;
+  if ((long long)N * Hv >= (1LL << 21)) return CKDA_ERR_SHAPE;   // 2^32 threads of a launch
   if ((long long)Hv * (dk > dv ? dk : dv) * 4 * kChunk >= (1LL << 31)) return CKDA_ERR_SHAPE;
   if (packed ? B != 1 : N != B) return CKDA_ERR_SHAPE;
   return CKDA_OK;
@@ -110,7 +110,7 @@ extern "C" int gdr_forward(const void *q, const void *k, const void *v, const fl
     return CKDA_ERR_LAUNCH;
   const hipError_t r = in_dtype == CKDA_BF16
                            ? launch_gdr_forward(a, static_cast<char *>(workspace) + L.rec, st)
-                           : launch_gdr_token(a, in_dtype, st);
+                           : launch_gdr_token(a, st);
   return r == hipSuccess ? CKDA_OK : CKDA_ERR_LAUNCH;
 }
 
@@ -122,7 +122,7 @@ extern "C" int gdr_decode_step(const void *q, const void *k, const void *v, cons
   if (N < 1 || pool < 1 || Hk < 1 || Hv < 1 || Hv % Hk != 0 || !dims_ok(dk) || !dims_ok(dv))
     return CKDA_ERR_SHAPE;
   if (!slots && pool != N) return CKDA_ERR_SHAPE;
-  if ((long long)N * Hv >= (1LL << 31) || (long long)pool * Hv >= (1LL << 31))
+  if ((long long)N * Hv >= (1LL << 24) || (long long)pool * Hv >= (1LL << 31))
     return CKDA_ERR_SHAPE;
   if (!q || !k || !v || !g || !beta || !S || !o) return CKDA_ERR_NULL;
   const void *ptrs[] = {q, k, v, S, o};
@@ -272,7 +272,8 @@ namespace {
 
 int rows_status(int tokens, int Hq, int Hk, int d, int rd, int norm, int layout, int in_dtype) {
   if (in_dtype != CKDA_BF16 && in_dtype != CKDA_F32) return CKDA_ERR_DTYPE;
-  if (tokens < 0 || Hq < 0 || Hk < 0 || Hq + (long long)Hk < 1 || Hq > 65535 || Hk > 65535)
+  if (tokens < 0 || tokens >= 1 << 27 || Hq < 0 || Hk < 0 || Hq + (long long)Hk < 1 ||
+      Hq > 65535 || Hk > 65535)
     return CKDA_ERR_SHAPE;
   if (d < 2 || d > 256 || d % 2 || rd < 0 || rd > d || rd % 2) return CKDA_ERR_SHAPE;
   if (norm < CKDA_NORM_NONE || norm > CKDA_NORM_RMS) return CKDA_ERR_SHAPE;

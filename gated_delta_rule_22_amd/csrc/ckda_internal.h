@@ -141,7 +141,7 @@ hipError_t launch_gdr_step(const void *q, const void *k, const void *v, const fl
                            int N, int Hk, int Hv, int dk, int dv, int in_dtype,
                            hipStream_t stream);
 // Token by token, fp32 arithmetic, any input type.
-hipError_t launch_gdr_token(const GdrArgs &a, int in_dtype, hipStream_t stream);
+hipError_t launch_gdr_token(const GdrArgs &a, hipStream_t stream);
 // Chunkwise on bf16 matrix cores (bf16 inputs): `rec` holds
 // gdr_forward_rec_bytes() for every chunk and value head.
 size_t gdr_forward_rec_bytes();

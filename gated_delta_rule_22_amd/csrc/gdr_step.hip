@@ -106,91 +106,163 @@ __global__ __launch_bounds__(kThreads) void gdr_step_kernel(
         st[r] + s_k[rg * kRows + r] * e;
 }
 
-// A sequence token by token.  A wave owns 16 columns of one head's state for
-// the whole sequence: lane (r, c) keeps column c of the rows
-// {16 i + 4 r + j}, DK / 4 of them, in registers, so a token costs 3 DK / 4
-// products and two sums over 4 lanes, and nothing but the staged tokens goes
-// through LDS.  The chain of one token (sum of S^T k, the write, the next
-// token's sum) is the bound, not bandwidth: fp32 inputs take this path, where
-// a product in fp32 terms on the matrix cores would cost six bf16 products.
+// A sequence token by token, for fp32 inputs: on the matrix cores a product of
+// fp32 terms would cost six bf16 ones.  16 lanes share a column of the state
+// and keep DK / 16 of its rows each in registers for the whole sequence, so
+// a token costs a lane 4 DK / 16 products and two sums over 16 lanes, which are
+// DPP adds between neighbours, and nothing but the staged tokens goes through
+// LDS.  The bound is the chain of one token, sum of S^T k, e, the write, the
+// next token's sum; around it
+//  - the next tokens are loaded from memory a stage ahead and from LDS a token
+//    ahead,
+//  - a S, beta v and -beta a are made before the sum is there, and
+//  - o's sum waits for the next token's, so that the two run side by side.
+// 2 x 333 tokens, 4 heads of 64 x 64: 43 us, 0.13 us a token; 8 x 1024, 16 heads
+// of 128 x 128, where all compute units are full: 444 us.  Fewer lanes a column
+// sum less and hide less: 4 of them took 591 us where 16 took 510 (before the
+// stage's tokens were unrolled), 552 against 220 on 1024 tokens of 2 such heads,
+// and won only on thousands of 64 x 64 heads, 400 against 483.
+constexpr int kLanes = 16, kTokenCols = kThreads / kLanes;
 constexpr int kStage = 16;               // tokens staged into LDS at a time
 
-template <typename TIn, int DK, int DV>
+template <int CTRL> __device__ __forceinline__ float dpp_add(float x) {
+  return x + __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), CTRL,
+                                                                0xf, 0xf, true));
+}
+// Sums of both over each 16 neighbouring lanes, in all of them.
+__device__ __forceinline__ void sum_lanes(float &x, float &y) {
+  x = dpp_add<0xB1>(x), y = dpp_add<0xB1>(y);              // quad_perm, lane ^ 1
+  x = dpp_add<0x4E>(x), y = dpp_add<0x4E>(y);              // quad_perm, lane ^ 2
+  x = dpp_add<0x141>(x), y = dpp_add<0x141>(y);            // mirror of 8 lanes
+  x = dpp_add<0x140>(x), y = dpp_add<0x140>(y);            // mirror of 16 lanes
+}
+
+template <int DK, int DV>
 __global__ __launch_bounds__(kThreads) void gdr_token_kernel(
-    const TIn *__restrict__ q, const TIn *__restrict__ k, const TIn *__restrict__ v,
+    const float *__restrict__ q, const float *__restrict__ k, const float *__restrict__ v,
     const float *__restrict__ g, const float *__restrict__ beta, const float *__restrict__ S0,
-    Seqs seqs, int Hk, int Hv, TIn *__restrict__ o, float *__restrict__ S_T) {
-  constexpr int kCols = 64;              // columns of a workgroup: 4 waves of 16
-  constexpr int kBlocks = DV / kCols;
-  constexpr int kRows = DK / 4;
-  __shared__ float s_k[kStage][DK], s_q[kStage][DK], s_v[kStage][kCols];
-  __shared__ float s_a[kStage], s_b[kStage];
+    Seqs seqs, int Hk, int Hv, float *__restrict__ o, float *__restrict__ S_T) {
+  constexpr int kCols = kTokenCols, kBlocks = DV / kCols;
+  constexpr int kVec = DK / kLanes / 4;  // a lane's rows: 4 of each 4 kLanes
+  constexpr int kPer = kStage * DK / 4 / kThreads, kPerV = kStage * kCols / kThreads;
+  static_assert(kStage == kLanes, "a lane keeps one token's output of a stage");
+  static_assert(kPer * kThreads * 4 == kStage * DK && kPerV >= 1, "whole passes");
+  __shared__ nf4 s_k[2][kStage][DK / 4], s_q[2][kStage][DK / 4];
+  __shared__ float s_v[2][kStage][kCols], s_a[2][kStage], s_b[2][kStage];
   const int blk = blockIdx.x % kBlocks, nh = blockIdx.x / kBlocks;
   const int n = seqs.order(nh / Hv), h = nh % Hv, hk = h / (Hv / Hk);
-  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-  const int rr = lane >> 4, c = lane & 15;
-  const int col = wave * 16 + c;
+  const int t = threadIdx.x, rr = t % kLanes, col = t / kLanes;
   const size_t first = seqs.start(n);
   const int len = seqs.len(n);
   const size_t sbase = ((size_t)n * Hv + h) * DK * DV + (size_t)blk * kCols + col;
 
-  float S[kRows];
+  nf4 S[kVec];
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    const int row = 16 * (i >> 2) + 4 * rr + (i & 3);
-    S[i] = S0 ? S0[sbase + (size_t)row * DV] : 0.f;
+  for (int i = 0; i < kVec; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      S[i][j] = S0 ? S0[sbase + (size_t)(4 * (kLanes * i + rr) + j) * DV] : 0.f;
+
+  nf4 rk[kPer], rq[kPer];
+  float rv[kPerV], ra = 0.f, rb = 0.f;
+  auto fetch = [&](int t0) {             // rows behind the sequence read its last one
+    const int end = len - 1 - t0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int at = t + i * kThreads;
+      const size_t row = ((first + t0 + min(at / (DK / 4), end)) * Hk + hk) * DK + 4 * (at % (DK / 4));
+      rk[i] = *reinterpret_cast<const nf4 *>(k + row);
+      rq[i] = *reinterpret_cast<const nf4 *>(q + row);
+    }
+#pragma unroll
+    for (int i = 0; i < kPerV; ++i) {
+      const int at = t + i * kThreads;
+      rv[i] = v[((first + t0 + min(at / kCols, end)) * Hv + h) * DV + blk * kCols + at % kCols];
+    }
+    if (t < kStage) {
+      ra = g[(first + t0 + min(t, end)) * Hv + h];
+      rb = beta[(first + t0 + min(t, end)) * Hv + h];
+    }
+  };
+  auto stage = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int at = t + i * kThreads;
+      s_k[buf][at / (DK / 4)][at % (DK / 4)] = rk[i];
+      s_q[buf][at / (DK / 4)][at % (DK / 4)] = rq[i];
+    }
+#pragma unroll
+    for (int i = 0; i < kPerV; ++i) {
+      const int at = t + i * kThreads;
+      s_v[buf][at / kCols][at % kCols] = rv[i];
+    }
+    if (t < kStage) {
+      s_a[buf][t] = expf(ra);
+      s_b[buf][t] = rb;
+    }
+  };
+  if (len > 0) {
+    fetch(0);
+    stage(0);
   }
-  for (int t0 = 0; t0 < len; t0 += kStage) {
+  for (int t0 = 0, buf = 0; t0 < len; t0 += kStage, buf ^= 1) {
+    __syncthreads();                     // this stage is written, the other one read
+    if (t0 + kStage < len) fetch(t0 + kStage);
     const int m = min(kStage, len - t0);
-    __syncthreads();
-    for (int i = t; i < m * DK; i += kThreads) {
-      const size_t at = ((first + t0 + i / DK) * Hk + hk) * DK + i % DK;
-      s_k[i / DK][i % DK] = to_f32(k[at]);
-      s_q[i / DK][i % DK] = to_f32(q[at]);
-    }
-    for (int i = t; i < m * kCols; i += kThreads)
-      s_v[i / kCols][i % kCols] =
-          to_f32(v[((first + t0 + i / kCols) * Hv + h) * DV + blk * kCols + i % kCols]);
-    if (t < m) {
-      s_a[t] = expf(g[(first + t0 + t) * Hv + h]);
-      s_b[t] = beta[(first + t0 + t) * Hv + h];
-    }
-    __syncthreads();
-    for (int s = 0; s < m; ++s) {
-      const float a = s_a[s];
-      float4 kk[kRows / 4];
-      float u0 = 0.f, u1 = 0.f;
+    nf4 kk[kVec], qq[kVec];
+    float a, b, vv;
+    auto take = [&](int s) {
 #pragma unroll
-      for (int i = 0; i < kRows / 4; ++i) {
-        kk[i] = *reinterpret_cast<const float4 *>(&s_k[s][16 * i + 4 * rr]);
-        u0 += kk[i].x * S[4 * i] + kk[i].y * S[4 * i + 1];
-        u1 += kk[i].z * S[4 * i + 2] + kk[i].w * S[4 * i + 3];
+      for (int i = 0; i < kVec; ++i) {
+        kk[i] = s_k[buf][s][kLanes * i + rr];
+        qq[i] = s_q[buf][s][kLanes * i + rr];
       }
-      float u = u0 + u1;
-      u += __shfl_xor(u, 16);
-      u += __shfl_xor(u, 32);
-      const float e = s_b[s] * (s_v[s][col] - a * u);
-      float w0 = 0.f, w1 = 0.f;
+      a = s_a[buf][s], b = s_b[buf][s], vv = s_v[buf][s][col];
+    };
+    take(0);
+    float w = 0.f, keep = 0.f;
+    auto finish = [&](int s) {           // w is o of token s now: one lane of the column keeps it
+      if (rr == s) keep = w;
+    };
+    auto token = [&](int s) {
+      nf4 x = kk[0] * S[0];
 #pragma unroll
-      for (int i = 0; i < kRows / 4; ++i) {
-        const float4 qq = *reinterpret_cast<const float4 *>(&s_q[s][16 * i + 4 * rr]);
-        S[4 * i] = a * S[4 * i] + kk[i].x * e;
-        S[4 * i + 1] = a * S[4 * i + 1] + kk[i].y * e;
-        S[4 * i + 2] = a * S[4 * i + 2] + kk[i].z * e;
-        S[4 * i + 3] = a * S[4 * i + 3] + kk[i].w * e;
-        w0 += qq.x * S[4 * i] + qq.y * S[4 * i + 1];
-        w1 += qq.z * S[4 * i + 2] + qq.w * S[4 * i + 3];
+      for (int i = 1; i < kVec; ++i) x += kk[i] * S[i];
+      float u = (x[0] + x[1]) + (x[2] + x[3]);
+      nf4 nk[kVec], nq[kVec];
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) nk[i] = kk[i], nq[i] = qq[i];
+      const float na = a, bv = b * vv, ab = b * a;
+      take(min(s + 1, kStage - 1));
+      sum_lanes(u, w);
+      if (s > 0) finish(s - 1);
+      const float e = bv - ab * u;
+      nf4 y = 0.f;
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) {
+        S[i] = na * S[i] + nk[i] * e;
+        y += nq[i] * S[i];
       }
-      float w = w0 + w1;
-      w += __shfl_xor(w, 16);
-      w += __shfl_xor(w, 32);
-      if (rr == 0) put(o + ((first + t0 + s) * Hv + h) * DV + blk * kCols + col, w);
+      w = (y[0] + y[1]) + (y[2] + y[3]);
+    };
+    if (m == kStage) {
+#pragma unroll
+      for (int s = 0; s < kStage; ++s) token(s);
+    } else {
+      for (int s = 0; s < m; ++s) token(s);
     }
+    float none = 0.f;
+    sum_lanes(w, none);
+    finish(m - 1);
+    if (rr < m) o[((first + t0 + rr) * Hv + h) * DV + blk * kCols + col] = keep;
+    if (t0 + kStage < len) stage(buf ^ 1);
   }
   if (S_T)
 #pragma unroll
-    for (int i = 0; i < kRows; ++i)
-      S_T[sbase + (size_t)(16 * (i >> 2) + 4 * rr + (i & 3)) * DV] = S[i];
+    for (int i = 0; i < kVec; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        S_T[sbase + (size_t)(4 * (kLanes * i + rr) + j) * DV] = S[i][j];
 }
 
 // ------------------------------------------------- the backward in fp64
@@ -290,25 +362,6 @@ hipError_t step_typed(const void *q, const void *k, const void *v, const float *
   return hipErrorInvalidValue;
 }
 
-template <typename TIn>
-hipError_t token_typed(const GdrArgs &a, hipStream_t stream) {
-  const dim3 grid((unsigned)((size_t)a.N * a.Hv * (a.dv / 64))), block(kThreads);
-#define GDR_CASE(DK_, DV_)                                                                   \
-  if (a.dk == DK_ && a.dv == DV_) {                                                          \
-    hipLaunchKernelGGL((gdr_token_kernel<TIn, DK_, DV_>), grid, block, 0, stream,            \
-                       static_cast<const TIn *>(a.q), static_cast<const TIn *>(a.k),         \
-                       static_cast<const TIn *>(a.v), a.g, a.beta, a.S0, a.seqs, a.Hk, a.Hv,  \
-                       static_cast<TIn *>(a.o), a.S_T);                                      \
-    return hipGetLastError();                                                                \
-  }
-  GDR_CASE(64, 64)
-  GDR_CASE(64, 128)
-  GDR_CASE(128, 64)
-  GDR_CASE(128, 128)
-#undef GDR_CASE
-  return hipErrorInvalidValue;
-}
-
 unsigned blocks_for(size_t items) {
   const size_t b = (items + kThreads - 1) / kThreads;
   return (unsigned)(b < 1 ? 1 : (b < 8192 ? b : 8192));
@@ -326,9 +379,22 @@ hipError_t launch_gdr_step(const void *q, const void *k, const void *v, const fl
              : step_typed<float>(q, k, v, g, beta, S, slots, pool, o, N, Hk, Hv, dk, dv, stream);
 }
 
-hipError_t launch_gdr_token(const GdrArgs &a, int in_dtype, hipStream_t stream) {
-  return in_dtype == CKDA_BF16 ? token_typed<__hip_bfloat16>(a, stream)
-                               : token_typed<float>(a, stream);
+hipError_t launch_gdr_token(const GdrArgs &a, hipStream_t stream) {
+  const dim3 grid((unsigned)((size_t)a.N * a.Hv * (a.dv / kTokenCols))), block(kThreads);
+#define GDR_CASE(DK_, DV_)                                                                   \
+  if (a.dk == DK_ && a.dv == DV_) {                                                          \
+    hipLaunchKernelGGL((gdr_token_kernel<DK_, DV_>), grid, block, 0, stream,                 \
+                       static_cast<const float *>(a.q), static_cast<const float *>(a.k),     \
+                       static_cast<const float *>(a.v), a.g, a.beta, a.S0, a.seqs, a.Hk,     \
+                       a.Hv, static_cast<float *>(a.o), a.S_T);                              \
+    return hipGetLastError();                                                                \
+  }
+  GDR_CASE(64, 64)
+  GDR_CASE(64, 128)
+  GDR_CASE(128, 64)
+  GDR_CASE(128, 128)
+#undef GDR_CASE
+  return hipErrorInvalidValue;
 }
 
 hipError_t launch_gdr_expand(const GdrF64Args &a, int in_dtype, hipStream_t stream) {

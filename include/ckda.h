@@ -374,7 +374,7 @@ size_t gdr_forward_workspace_bytes(int B, int T, int Hk, int Hv, int dk, int dv,
  *              sequences are allowed, rows outside every sequence are not
  *              written
  *  Hk, Hv      Hv a multiple of Hk; dk, dv each 64 or 128; B*T*Hv < 2^31,
- *              N*Hv < 2^28
+ *              N*Hv < 2^21
  *  o           [B, T, Hv, dv]  in_dtype
  *  S_T         [N, Hv, dk, dv] fp32 or NULL; may be S0 itself
  *  workspace   gdr_forward_workspace_bytes(...) bytes, 16-byte aligned
@@ -429,7 +429,8 @@ int gdr_backward(const void *q, const void *k, const void *v, const float *g, co
  *  slots       int32 [N]: the state of each row; or NULL: row n has state n
  *              and pool must be N.  A slot outside [0, pool) marks a padded
  *              row; a slot that an earlier row has named already does too.
- *              Padded rows get o = 0 and touch no state.
+ *              Padded rows get o = 0 and touch no state.  N*Hv < 2^24,
+ *              pool*Hv < 2^31
  *  o           [N, Hv, dv]     in_dtype, must not overlap S or an input
  *
  * Numerics: fp32 throughout, o rounded once.
@@ -461,8 +462,8 @@ enum {
  * over the pairs of the first rd channels, with the angle positions[token] *
  * freqs[pair]; y = n behind them.  Rows of q are then multiplied by q_scale.
  *
- *  q, k        tokens rows of Hq and Hk heads of d channels, ldq and ldk
- *              elements apart (>= Hq d, Hk d): slices of a packed projection
+ *  q, k        tokens (< 2^27) rows of Hq and Hk heads of d channels, ldq and
+ *              ldk elements apart (>= Hq d, Hk d): slices of a packed projection
  *              are read where they are.  Hq or Hk may be 0.
  *  positions   int32 [tokens], freqs  fp64 [rd/2] in radians per position;
  *              both may be NULL if rd is 0.  The angle is reduced in fp64, so

@@ -252,3 +252,11 @@ def test_frequencies():
                dict(rotary_dim=2, scaling="base"), dict(rotary_dim=8, base=1.0)):
         with pytest.raises(ValueError):
             ck.rotary_frequencies(**kw)
+
+
+def test_more_threads_than_a_launch_has(lib):
+    """2^32 threads of a launch: refused with the shape, not by a failing launch."""
+    assert lib.gdr_forward_workspace_bytes(1 << 20, 1, 2, 2, 64, 64, 1 << 20, 0) == 0
+    assert _fwd(lib, T=0, B=1 << 20, Hk=2, Hv=2) == SHAPE
+    assert _step(lib, N=1 << 22, pool=8) == SHAPE
+    assert _norm(lib, tokens=1 << 27) == _rot(lib, tokens=1 << 27) == SHAPE
