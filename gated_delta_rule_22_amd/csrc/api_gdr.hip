@@ -253,7 +253,7 @@ extern "C" int gdr_backward(const void *q, const void *k, const void *v, const f
     float **values[] = {&a.vx, &a.dox, &a.dvx};
     for (int i = 0; i < 3; ++i) *values[i] = reinterpret_cast<float *>(w + L.values[i]);
   }
-  a.dq = dq; a.dk_out = d_k; a.dv_out = d_v; a.dg = dg;
+  a.dq = dq; a.dk_out = d_k; a.dv_out = d_v; a.dg = dg; a.zero_start = !S0;
   if (rows > 0 && launch_gdr_expand(a, in_dtype, st) != hipSuccess) return CKDA_ERR_LAUNCH;
   // The per-channel backward, signs ignored (the gates are positive).
   const bool wide_in = in_dtype == CKDA_BF16;

@@ -172,6 +172,7 @@ struct GdrF64Args {
     float *qx, *kx, *gx, *vx, *dox, *dqx, *dkx, *dgx, *dvx;
     void *dq, *dk_out, *dv_out;
     float *dg;
+    bool zero_start;                     // sequences start from zero states
 };
 hipError_t launch_gdr_expand(const GdrF64Args &a, int in_dtype, hipStream_t stream);
 hipError_t launch_gdr_collect(const GdrF64Args &a, int in_dtype, hipStream_t stream);

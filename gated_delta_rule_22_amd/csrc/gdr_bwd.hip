@@ -376,7 +376,7 @@ __global__ __launch_bounds__(kThreads, 2) void grad_kernel(
     const char *__restrict__ U_keep, const char *__restrict__ dS_keep,
     const char *__restrict__ F_keep, __hip_bfloat16 *__restrict__ dq,
     __hip_bfloat16 *__restrict__ dk_out, __hip_bfloat16 *__restrict__ dv_out,
-    float *__restrict__ dg, float *__restrict__ dbeta) {
+    float *__restrict__ dg, float *__restrict__ dbeta, bool zero_start) {
   using L = GradLds<DK, DV>;
   constexpr int MT = DK / 16, NT = DV / 16, kParts = DV / 64;
   extern __shared__ __attribute__((aligned(16))) char lds[];
@@ -686,7 +686,9 @@ __global__ __launch_bounds__(kThreads, 2) void grad_kernel(
       z += (lane ? y : 0.f) + gn * ((s_n[0] + s_n[1]) + (s_n[2] + s_n[3]));
       if (lane < valid) {
         const size_t gi = (row0 + lane) * Hv + hv;
-        dg[gi] = g[gi] < (float)kGateFloor ? 0.f : z;   // a floored gate is constant
+        // a floored gate is constant, and one that scales a zero state does nothing
+        const bool idle = g[gi] < (float)kGateFloor || (zero_start && at + lane == 0);
+        dg[gi] = idle ? 0.f : z;
       }
     }
     if (u + 1 < rep) __syncthreads();
@@ -728,7 +730,7 @@ template <int DK, int DV> hipError_t backward_typed(const GdrBwdArgs &a, hipStre
   hipLaunchKernelGGL(gr, dim3((unsigned)(f.n_chunks_ub * f.Hk)), dim3(kThreads), gl, st, q, k, f.g,
                      f.beta, d_o, f.seqs, f.N, f.Hk, f.Hv, rec, S, U, dS, F,
                      static_cast<__hip_bfloat16 *>(a.dq), static_cast<__hip_bfloat16 *>(a.dk),
-                     static_cast<__hip_bfloat16 *>(a.dv), a.dg, a.dbeta);
+                     static_cast<__hip_bfloat16 *>(a.dv), a.dg, a.dbeta, !f.S0);
   return hipGetLastError();
 }
 

@@ -301,7 +301,7 @@ __global__ __launch_bounds__(kThreads) void gdr_collect_kernel(
     const float *__restrict__ dqx, const float *__restrict__ dkx, const float *__restrict__ dgx,
     const float *__restrict__ dvx, const float *__restrict__ g, int N, size_t rows, int Hk, int Hv,
     int dk, int dv, TIn *__restrict__ dq, TIn *__restrict__ dk_out, TIn *__restrict__ dv_out,
-    float *__restrict__ dg, Seqs seqs) {
+    float *__restrict__ dg, Seqs seqs, bool zero_start) {
   // One wave per (token, query/key head).  Rows outside every sequence are
   // left alone, as everywhere: a row belongs to the last sequence that starts
   // at or before it, if that sequence reaches it.
@@ -334,7 +334,8 @@ __global__ __launch_bounds__(kThreads) void gdr_collect_kernel(
       double s = 0.;
       for (int c = lane; c < dk; c += 64) s += (double)dgx[rh * dk + c] * al;
       for (int off = 32; off > 0; off >>= 1) s += __shfl_xor(s, off);
-      if (lane == 0) dg[rh] = g[rh] < -87.f ? 0.f : (float)s;
+      const bool idle = g[rh] < -87.f || (zero_start && row == (size_t)seqs.start(lo - 1));
+      if (lane == 0) dg[rh] = idle ? 0.f : (float)s;   // the gate of a zero state does nothing
       if (dvx)
         for (int c = lane; c < dv; c += 64) put(dv_out + rh * dv + c, dvx[rh * dv + c]);
     }
@@ -417,7 +418,8 @@ hipError_t launch_gdr_collect(const GdrF64Args &a, int in_dtype, hipStream_t str
     using T = std::remove_pointer_t<decltype(dq)>;
     hipLaunchKernelGGL(gdr_collect_kernel<T>, grid, dim3(kThreads), 0, stream, a.dqx, a.dkx, a.dgx,
                        a.dvx, a.g, a.N, a.rows, a.Hk, a.Hv, a.dk, a.dv, dq,
-                       static_cast<T *>(a.dk_out), static_cast<T *>(a.dv_out), a.dg, a.seqs);
+                       static_cast<T *>(a.dk_out), static_cast<T *>(a.dv_out), a.dg, a.seqs,
+                       a.zero_start);
   };
   if (in_dtype == CKDA_BF16) run(static_cast<__hip_bfloat16 *>(a.dq));
   else run(static_cast<float *>(a.dq));

@@ -97,6 +97,19 @@ def test_no_states(dtype):
     check(inputs(7, [70, 129], 2, 2, 64, 128, dtype, s0=False), [70, 129], dtype, 3, False)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("lens", [[1, 0, 1], [1] * 70, [70, 0, 129]])
+def test_first_gate_of_a_zero_state(lens, dtype):
+    """It scales nothing: its gradient is zero itself, not a rounding off."""
+    x = inputs(11, lens, 1, 2, 64, 64, dtype, s0=False)
+    do, dS = upstream(5, x, lens, dtype)
+    dg = run(x, do, dS, lens)[3]
+    first = [sum(lens[:i]) for i, n in enumerate(lens) if n]
+    assert not dg[first].any()
+    want = wanted(x, do, dS, lens)[3]
+    assert rel(dg, want) < tol("dg", dtype)
+
+
 @pytest.mark.parametrize("lens", [[140], [20]])
 def test_resets(lens):
     """Log-gates of -infinity forget everything and have no gradient (the
