@@ -144,10 +144,12 @@ extern "C" int gdr_decode_step(const void *q, const void *k, const void *v, cons
 namespace {
 
 // fp32 inputs take the per-channel fp64 backward, and so do bf16 inputs of no
-// more than this many (token, value head) pairs: an fp32 gradient of so few can
-// be the small difference of a handful of terms, each within 2^-18 in the
-// chunkwise path, where more of them average out.  (130 us against 45 us.)
-constexpr size_t kFewRows = 128;
+// more than this many (token, value head) pairs: the gate's gradient of a few
+// tokens of one or two heads can be the small difference of terms that are each
+// within 2^-18 in the chunkwise path (up to 1.8e-5 off), where more of them
+// average out.  It costs 125 us against 45 us at 128 pairs, 255 against 87 at
+// 512 tokens of a head of 128 x 128, 378 against 130 at 1024.
+constexpr size_t kFewRows = 1024;
 bool gdr_bwd_f64(int B, int T, int Hv, int in_dtype) {
   return in_dtype == CKDA_F32 || (size_t)B * T * Hv <= kFewRows;
 }

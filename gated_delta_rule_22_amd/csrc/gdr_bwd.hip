@@ -546,6 +546,7 @@ __global__ __launch_bounds__(kThreads, 2) void grad_kernel(
           a2 = mfma(s.lo, d[c], a2);
           b2 = mfma(s.lo, f[c].hi, b2);
           b = mfma(s.hi, f[c].lo, b);
+          b2 = mfma(s.lo, f[c].lo, b2);
         }
         const int off = place_of<DK>(16 * w + (lane & 15), 16 * i + 4 * (lane >> 4));
         const f4 qv = widen4(*reinterpret_cast<const bf4 *>(Q + off));
@@ -593,6 +594,7 @@ __global__ __launch_bounds__(kThreads, 2) void grad_kernel(
           c0 = mfma(s.hi, uo[c].hi, c0);
           c1 = mfma(s.lo, uo[c].hi, c1);
           c0 = mfma(s.hi, uo[c].lo, c0);
+          c1 = mfma(s.lo, uo[c].lo, c1);
         }
         c0 = (c0 + c1) * last;
         const int off = place_of<DK>(16 * w + (lane & 15), 16 * i + 4 * (lane >> 4));

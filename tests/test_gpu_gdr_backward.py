@@ -92,6 +92,48 @@ def test_gates(gate, beta, dtype):
     check(inputs(5, [150], 2, 4, 128, 64, dtype, gate, beta), [150], dtype, 2)
 
 
+# Calls of more than 1024 tokens times value heads: bf16 takes the chunkwise path.
+@pytest.mark.parametrize("lens", [[1025], [64] * 17, [63, 0, 65, 1, 700, 2, 200], [1] * 1030])
+def test_lengths_in_chunks(lens):
+    check(inputs(23 + len(lens), lens, 1, 1, 128, 128, BF), lens, BF)
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 64), (64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("hk,hv", [(1, 4), (3, 9), (5, 5)])
+def test_heads_and_dims_in_chunks(hk, hv, dk, dv):
+    check(inputs(25, [197, 133], hk, hv, dk, dv, BF), [197, 133], BF)
+
+
+@pytest.mark.parametrize("gate", ["one", "fast", "resets"])
+@pytest.mark.parametrize("beta", [1.0, 2.0])
+def test_gates_in_chunks(gate, beta):
+    lens = [350]
+    x = inputs(27, lens, 2, 4, 128, 64, BF, gate, beta)
+    x["g"] = x["g"].clamp(min=-1e4)      # the reference has no derivative at -infinity
+    check(x, lens, BF)
+
+
+def test_chunks_repeat_and_keep_to_their_rows():
+    """Rows outside the sequences stay, a head's NaN stays in it, reruns give the same bits."""
+    lens = [300, 170]
+    x = inputs(29, [600], 2, 4, 64, 128, BF)
+    x["S0"] = x["S0"].repeat(2, 1, 1, 1)
+    do, dS = upstream(11, x, lens, BF)
+    cu = torch.tensor([0, 300, 470], dtype=torch.int32, device="cuda")
+    one = run(x, do, dS, lens, cu=cu)
+    two = run(x, do, dS, lens, cu=cu)
+    for a, b in zip(one[:5], two[:5]):
+        assert torch.equal(a[:470], b[:470])
+    assert torch.equal(one[5], two[5])
+    x["v"][20, 1] = float("nan")
+    got = run(x, do, dS, lens, cu=cu)
+    for a, b, n in zip(got[:5], one[:5], NAMES):
+        assert torch.equal(a[300:470], b[300:470]), n
+    for i in (2, 3, 4):                  # dv, dg, dbeta of the other heads
+        assert torch.equal(got[i][:300, [0, 2, 3]], one[i][:300, [0, 2, 3]])
+    assert torch.isnan(got[3][:300, 1]).any()
+
+
 @pytest.mark.parametrize("dtype", [F32, BF])
 def test_no_states(dtype):
     check(inputs(7, [70, 129], 2, 2, 64, 128, dtype, s0=False), [70, 129], dtype, 3, False)
