@@ -277,13 +277,13 @@ __global__ __launch_bounds__(2 * kThreads, 2) void reverse_kernel(
 #pragma unroll
     for (int jt = 0; jt < 4; ++jt) F[jt] = X[jt];
 #pragma unroll
-    for (int term = 0; term < 3; ++term)
+    for (int term = 0; term < 4; ++term)
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
         for (int jt = 0; jt < 2 * ks + 2; ++jt) {
           const Split &x = ks ? x1 : x0;
-          F[jt] = mfma(term == 2 ? t[jt][ks].lo : t[jt][ks].hi, term == 1 ? x.lo : x.hi, F[jt]);
+          F[jt] = mfma(term & 2 ? t[jt][ks].lo : t[jt][ks].hi, term & 1 ? x.lo : x.hi, F[jt]);
         }
 #pragma unroll
     for (int i = 0; i < MT; ++i) S[i] = S[i] * gn + qd[i];
@@ -482,6 +482,7 @@ __global__ __launch_bounds__(kThreads, 2) void grad_kernel(
           xx[s] = mfma(z.hi, v.hi, xx[s]);
           a = mfma(z.lo, v.hi, a);
           xx[s] = mfma(z.hi, v.lo, xx[s]);
+          a = mfma(z.lo, v.lo, a);
           if (rows) {
             pp[s] = mfma(z.hi, y, pp[s]);
             b = mfma(z.lo, y, b);

@@ -465,14 +465,14 @@ __global__ __launch_bounds__(8 * BV, 2) void chain_kernel(
     for (int it = 0; it < 4; ++it) U[it] = X[it];
     // the four tiles' products turn by turn: each waits for its own last one
 #pragma unroll
-    for (int term = 0; term < 3; ++term)
+    for (int term = 0; term < 4; ++term)
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
         for (int it = 2 * ks; it < 4; ++it) {
           const Split &t = T[frag_at(it, ks) / kFrag];
           const Split &x = ks ? x1 : x0;
-          U[it] = mfma(term == 2 ? t.lo : t.hi, term == 1 ? x.lo : x.hi, U[it]);
+          U[it] = mfma(term & 2 ? t.lo : t.hi, term & 1 ? x.lo : x.hi, U[it]);
         }
 #pragma unroll
     for (int i = 0; i < MT; ++i) S[i] *= gn;
