@@ -341,10 +341,18 @@ template <int DK, int DV> struct GradLds {
   static_assert(kX + 256 * DK <= kBytes, "a state's 64 columns fit the window");
 };
 
-__device__ __forceinline__ float sum4(f4 a) { return (a[0] + a[1]) + (a[2] + a[3]); }
+__device__ __forceinline__ float dot4(f4 a, f4 b, float c) {
+  return fmaf(a[3], b[3], fmaf(a[2], b[2], fmaf(a[1], b[1], fmaf(a[0], b[0], c))));
+}
 __device__ __forceinline__ float over_quarters(float x) {
   x += __shfl_xor(x, 16);
   return x + __shfl_xor(x, 32);
+}
+
+// a.b + c of two packed bf16 pairs.
+__device__ __forceinline__ float dot_pair(uint32_t a, uint32_t b, float c) {
+  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf2, a), __builtin_bit_cast(bf2, b), c,
+                                         false);
 }
 
 // SEGMENTS runs of BYTES from `step` bytes to `step` bytes, to LDS one behind
@@ -458,7 +466,7 @@ __global__ __launch_bounds__(kThreads, 2) void grad_kernel(
     f4 pp[5], xx[5];                     // of dP and dA
 #pragma unroll
     for (int s = 0; s < 5; ++s) pp[s] = xx[s] = 0.f;
-    float dG = 0.f, ws = 0.f, dot = 0.f, db = 0.f;
+    float dG = 0.f, dGk = 0.f, ws = 0.f, dot = 0.f, db = 0.f;   // dGk: K's part of dG
 #pragma unroll
     for (int part = 0; part < kParts; ++part) {
       if (part) {
@@ -522,7 +530,7 @@ __global__ __launch_bounds__(kThreads, 2) void grad_kernel(
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             const f4 z = whole(f[c], half);
-            db += sum4(z * whole(uo[c], half));
+            db = dot4(z, whole(uo[c], half), db);
             computed(db);
             if (tok < valid)
               *reinterpret_cast<bf4 *>(o + 32 * c + 16 * half + 4 * h) = round4(z * back);
@@ -554,32 +562,38 @@ __global__ __launch_bounds__(kThreads, 2) void grad_kernel(
         const f4 kv = widen4(*reinterpret_cast<const bf4 *>(K + off));
         a = (a + a2) * gam;
         b = (b + b2) * -gam;
-        dG += sum4(qv * a) + sum4(kv * b);
+        dG = dot4(qv, a, dG);
+        dGk = dot4(kv, b, dGk);
         dQ[i] += a;
         dK[i] += b;
         computed(dQ[i]);
         computed(dK[i]);
         computed(dG);
+        computed(dGk);
       }
       // <S, dS'>, then dS' in place of S.
       t = renewed(t);
       lane = t & 63;
       using St = Segments<MT, 4 * kFrag>;
       constexpr int kLo = St::kPasses / 2;
+      float dot2nd = 0.f;
 #pragma unroll
       for (int i = 0; i < kLo; ++i) {
         const char *p = lds + L::kX + (St::Lin::mixed(t) + i * kThreads) * 16;
         const u4 z = St::Lin::halves(state.r[i], t), v = St::Lin::halves(state.r[i + kLo], t);
         const u4 a = *reinterpret_cast<const u4 *>(p);
         const u4 b = *reinterpret_cast<const u4 *>(p + kLo * kThreads * 16);
-        auto low = [](uint32_t q) { return __uint_as_float(q << 16); };
-        auto high = [](uint32_t q) { return __uint_as_float(q & 0xFFFF0000u); };
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          dot += (low(a[j]) + low(b[j])) * (low(z[j]) + low(v[j])) +
-                 (high(a[j]) + high(b[j])) * (high(z[j]) + high(v[j]));
+        for (int j = 0; j < 4; ++j) {
+          dot = dot_pair(a[j], z[j], dot);
+          dot2nd = dot_pair(b[j], z[j], dot2nd);
+          dot = dot_pair(a[j], v[j], dot);
+          dot2nd = dot_pair(b[j], v[j], dot2nd);
+        }
         computed(dot);
+        computed(dot2nd);
       }
+      dot += dot2nd;
       __syncthreads();
       state.store(lds + L::kX, t);
       __syncthreads();
@@ -599,7 +613,7 @@ __global__ __launch_bounds__(kThreads, 2) void grad_kernel(
         }
         c0 = (c0 + c1) * last;
         const int off = place_of<DK>(16 * w + (lane & 15), 16 * i + 4 * (lane >> 4));
-        ws += sum4(c0 * widen4(*reinterpret_cast<const bf4 *>(K + off)));
+        ws = dot4(c0, widen4(*reinterpret_cast<const bf4 *>(K + off)), ws);
         dK[i] += c0;
         computed(dK[i]);
         computed(ws);
@@ -660,7 +674,8 @@ __global__ __launch_bounds__(kThreads, 2) void grad_kernel(
         a += w >= 2 ? r1 : none;
         b += w >= 2 ? r2 : none;
         c += w >= 2 ? none : r1 + r2;
-        dG += sum4(qv * a) + sum4(kv * (b - c));
+        dG = dot4(qv, a, dG);
+        dGk = dot4(kv, b - c, dGk);
         dQ[i] += a + diag * kv;
         dK[i] += b + c + diag * qv;
         computed(dQ[i]);
@@ -668,7 +683,7 @@ __global__ __launch_bounds__(kThreads, 2) void grad_kernel(
         computed(dG);
       }
     }
-    dG = over_quarters(dG);
+    dG = over_quarters(dG + dGk);
     ws = over_quarters(ws);
     if (h == 0) {
       s_dG[tok] = dG;
