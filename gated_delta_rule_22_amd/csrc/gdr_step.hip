@@ -25,6 +25,9 @@ __device__ __forceinline__ void put(__hip_bfloat16 *p, float x) { *p = __float2b
 // first reduction.  slots[n] names the row's state.  A slot outside the pool
 // marks a padded row, and so does one that an earlier row has named: the
 // pool's states are written by one row each, whatever the slots hold.
+// 256 rows of 16 heads of 128 x 128 (537 MB of state traffic): 108 us in a pool
+// larger than the caches (5.0 TB/s; a copy reaches 5.16), 79 us where a part of
+// it is still there; 5 rows of 16 heads 5.3 us.
 template <typename TIn, int DK, int DV>
 __global__ __launch_bounds__(kThreads) void gdr_step_kernel(
     const TIn *__restrict__ q, const TIn *__restrict__ k, const TIn *__restrict__ v,
