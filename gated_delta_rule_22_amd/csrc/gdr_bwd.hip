@@ -45,7 +45,7 @@ __device__ __forceinline__ bool chain_block(int nblk, int pairs, int &pair, int 
 //
 // 8 x 4096 tokens of 16 heads of 128 x 128: 303 us for the 1.43 GB that it reads
 // and writes (4.7 TB/s, 277 at a copy's rate); where few sequences leave memory
-// idle, a chunk takes 3.8 us, the chain's latency (406 us on the layer without
+// idle, a chunk takes 3.1 us, the chain's latency (406 us on the layer without
 // helper waves, 325 with them, 303 with reads in batches and no conflicts).
 template <int DK> struct ReverseLds {
   static constexpr int kWave = (4 + DK / 16) * 1024;   // a wave's tiles
@@ -337,7 +337,7 @@ __global__ __launch_bounds__(2 * kThreads, 2) void reverse_kernel(
 // loaded while the one before it is used.  So two workgroups fit a compute
 // unit, and one computes while the other waits for memory, which is the bound
 // (2.5 GB on the layer of 8 x 4096 tokens and 16 heads of 128 x 128: 608 us,
-// 4.1 TB/s, with the vector units busy half of that time); and a wave keeps only
+// 4.1 TB/s, with the vector units active 63% of that time); and a wave keeps only
 // 64 columns of its own rows in registers.  Eight waves with all of a chunk in
 // 150 KB took 746 us: one workgroup a compute unit waits where two overlap.
 template <int DK, int DV> struct GradLds {

@@ -25,9 +25,9 @@ namespace {
 // 64 x 64 unit lower triangular inverse is taken in fp32: its 16 x 16 diagonal
 // blocks by substitution, what is below them by matrix products (substitution
 // over all 64 rows takes 2016 steps a wave and as many LDS broadcasts: 127 us
-// where this takes 94).  8 x 4096 tokens, 16 heads, 128 channels: 94 us for the
-// 520 MB that it reads and writes (5.5 TB/s with what stays in the caches), 108
-// us for the backward's records, so memory bounds it.
+// where this takes 94).  8 x 4096 tokens, 16 heads, 128 channels: 94 us for 448 MB
+// read and written (4.8 TB/s), 108 us for 508 MB with the backward's records, so
+// memory bounds it.
 constexpr int kMStride = C + 4;          // floats; keeps rows 16-byte aligned
 
 template <int DK, bool BWD>
@@ -268,7 +268,7 @@ __device__ __forceinline__ bool chain_block(int nblk, int pairs, int &pair, int 
 // cycles), T X (1000), U's terms and the barrier (700), K^T U (1600) and the
 // next state's terms (1100), each of which waits for the one before; 1400 of
 // the 5800 are matrix instructions.  8 x 4096 tokens of 16 heads of 128 x 128:
-// 203 to 209 us for 790 MB (3.8 TB/s); STORE 240 us for 1.24 GB (5.2 TB/s, a
+// 203 to 209 us for 714 MB (3.5 TB/s); STORE 240 us for 1.24 GB (5.2 TB/s, a
 // copy's rate).  Tried and slower: operands a whole chunk ahead (255 us, too
 // many registers), half of the products with the state behind barrier B with
 // K and Q twice in LDS (217), rows padded instead of the swizzle (+15%).
