@@ -158,3 +158,45 @@ def test_frequencies_give_the_plain_rotation():
     u, w = x.double()[..., :32], x.double()[..., 32:]
     assert rel(y, torch.cat([u * c - w * s, w * c + u * s], -1)) < TOL[F32]
     assert math.isclose(scale, 1.0)
+
+
+@pytest.mark.parametrize("tokens", [1023, 1024, 1025, 1031])
+def test_where_tiles_of_tokens_begin(tokens):
+    """One token a workgroup below 1024 tokens, tiles of eight from there on, the last one partial."""
+    q, k, pos, freqs, wq, wk = data(tokens, tokens, 3, 1, 64, 48, BF, packed=False)
+    a, b = ck.qk_norm_rotary(q.cuda(), k.cuda(), pos.cuda(), freqs.cuda(), q_weight=wq.cuda(),
+                             k_weight=wk.cuda())
+    assert rel(a, rotate(norm(q, "rms", wq), pos, freqs, "half")) < TOL[BF]
+    assert rel(b, rotate(norm(k, "rms", wk), pos, freqs, "half")) < TOL[BF]
+    x = ck.rotary(q.cuda(), pos.cuda(), freqs.cuda())
+    assert rel(x, rotate(q.double(), pos, freqs, "half")) < TOL[BF]
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("kind", ["rms", "l2"])
+def test_gradients_against_differences(kind, layout):
+    """Along a random direction u of all inputs, central differences of the fp32
+    operator.  With steps h u of 2^-7 of a row's length the third-order term is
+    within 2^-14 of the scale |g| |u| and the rounding of outputs (2^-23, over
+    2 h) within 2^-16; the bound is 2^-11 of that scale, where the derivative
+    itself is about 2^-3 of it."""
+    tokens, d, rd = 2, 16, 12
+    q, k, pos, freqs, wq, wk = data(31, tokens, 2, 1, d, rd, F32, packed=False)
+    r = NO().manual_seed(32)
+    leaves = [q, k, wq, wk]
+    step = [torch.randn(t.shape, generator=r) for t in leaves]
+    out = [torch.randn(q.shape, generator=r), torch.randn(k.shape, generator=r)]
+    opts = dict(norm=kind, layout=layout, q_scale=0.5, rotary_scale=1.5)
+    h = 2.0 ** -7
+
+    def loss(s):
+        q, k, wq, wk = (t.double().add(u.double(), alpha=s).float().cuda() for t, u in zip(leaves, step))
+        a, b = ck.qk_norm_rotary(q, k, pos.cuda(), freqs.cuda(), q_weight=wq, k_weight=wk, **opts)
+        return float((a.cpu().double() * out[0].double()).sum() + (b.cpu().double() * out[1].double()).sum())
+
+    got = ck.qk_norm_rotary_backward(out[0].cuda(), out[1].cuda(), q.cuda(), k.cuda(), pos.cuda(),
+                                     freqs.cuda(), q_weight=wq.cuda(), k_weight=wk.cuda(), **opts)
+    dot = sum(float((g.cpu().double() * u.double()).sum()) for g, u in zip(got, step))
+    scale = math.sqrt(sum(float(g.double().square().sum()) for g in got)
+                      * sum(float(u.double().square().sum()) for u in step))
+    assert abs((loss(h) - loss(-h)) / (2 * h) - dot) < 2.0 ** -11 * scale
