@@ -47,26 +47,28 @@ __device__ __forceinline__ bool chain_block(int nblk, int pairs, int &pair, int 
 // and writes (4.7 TB/s, 277 at a copy's rate); where few sequences leave memory
 // idle, a chunk takes 3.1 us, the chain's latency (406 us on the layer without
 // helper waves, 325 with them, 303 with reads in batches and no conflicts).
-template <int DK> struct ReverseLds {
+template <int DK, int BV> struct ReverseLds {
   static constexpr int kWave = (4 + DK / 16) * 1024;   // a wave's tiles
   static constexpr int kK = 0, kT = kTile<DK>, kQ = kT + 2 * kTri, kD = kQ + kTile<DK>;
-  static constexpr int kP = kD + kTile<64>, kGam = kP + 2 * kTri;
-  static constexpr int kTiles = kGam + 2 * C * 4, kBytes = kTiles + 4 * kWave;
+  static constexpr int kP = kD + kTile<BV>, kGam = kP + 2 * kTri;
+  static constexpr int kTiles = kGam + 2 * C * 4, kBytes = kTiles + BV / 16 * kWave;
 };
 
-template <int DK, int DV>
-__global__ __launch_bounds__(2 * kThreads, 2) void reverse_kernel(
+template <int DK, int DV, int BV>
+__global__ __launch_bounds__(4 * BV + kThreads, 2) void reverse_kernel(
     const __hip_bfloat16 *__restrict__ q, const __hip_bfloat16 *__restrict__ k,
     const __hip_bfloat16 *__restrict__ d_o, const float *__restrict__ dS_T, Seqs seqs, int N,
     int Hk, int Hv, const char *__restrict__ rec_base, char *__restrict__ dS_keep,
     char *__restrict__ F_keep, float *__restrict__ dS0) {
-  using L = ReverseLds<DK>;
-  constexpr int KS = DK / 32, MT = DK / 16, BV = 64;
+  using L = ReverseLds<DK, BV>;
+  constexpr int KS = DK / 32, MT = DK / 16, kChain = 4 * BV;   // threads of the chain
   extern __shared__ __attribute__((aligned(16))) char lds[];
   int pair, blk;
   if (!chain_block(DV / BV, N * Hv, pair, blk)) return;
   const int seq = seqs.order(pair / Hv), hv = pair % Hv, hk = hv / (Hv / Hk);
-  const int wave = (threadIdx.x >> 6) & 3, lane = threadIdx.x & 63, m = lane & 15, h = lane >> 4;
+  const bool helper = threadIdx.x >= kChain;
+  const int wave = (threadIdx.x - (helper ? kChain : 0)) >> 6;
+  const int lane = threadIdx.x & 63, m = lane & 15, h = lane >> 4;
   const int len = seqs.len(seq), chunks = (len + C - 1) / C;
   const size_t row0 = seqs.start(seq);
   const size_t c0 = seqs.first_chunk(seq);
@@ -74,8 +76,10 @@ __global__ __launch_bounds__(2 * kThreads, 2) void reverse_kernel(
   const char *K = lds + L::kK, *T = lds + L::kT;
   char *tiles = lds + L::kTiles + wave * L::kWave + lane * 16;
 
-  if (threadIdx.x >= kThreads) {         // helper waves
-    const int t = threadIdx.x - kThreads;
+  if (helper) {
+    const int t = threadIdx.x - kChain;
+    // one helper per chain wave computes; all four load
+    const bool ahead_too = BV == 64 || __builtin_amdgcn_readfirstlane(wave) < BV / 16;
     const char *Q = lds + L::kQ, *D = lds + L::kD, *P = lds + L::kP;
     const float *s_gam = reinterpret_cast<const float *>(lds + L::kGam);
     Stage<DK> gk, gq;
@@ -101,7 +105,7 @@ __global__ __launch_bounds__(2 * kThreads, 2) void reverse_kernel(
       gd.load(d_o + (row * Hv + hv) * DV + blk * BV, (size_t)Hv * DV, valid, t);
       // P hi and P lo: two matrices, not next to each other in the record
 #pragma unroll
-      for (int i = 0; i < 3; ++i) {
+      for (int i = 0; i < gp.kPasses; ++i) {
         const int at = (t + i * kThreads) * 16;
         gp.r[i] = load16(rec + (at < kTri ? kRecPh + at : kRecPl + at - kTri), true);
       }
@@ -178,8 +182,10 @@ __global__ __launch_bounds__(2 * kThreads, 2) void reverse_kernel(
     lds_barrier();                       // the helpers' operands of the last chunk
     if (chunks > 0) {
       fetch_own(max(last - 1, 0));
-      ahead();
-      put_tiles();
+      if (ahead_too) {
+        ahead();
+        put_tiles();
+      }
     }
     lds_barrier();                       // all helpers have read them
     if (chunks > 0) put_own(max(last - 1, 0));
@@ -188,9 +194,9 @@ __global__ __launch_bounds__(2 * kThreads, 2) void reverse_kernel(
       const int c1 = max(c - 1, 0), c2 = max(c - 2, 0);
       fetch_chain(c1);
       fetch_own(c2);
-      ahead();
+      if (ahead_too) ahead();
       lds_barrier();                     // B
-      put_tiles();
+      if (ahead_too) put_tiles();
       put_chain(c1);
       put_own(c2);
     }
@@ -728,6 +734,23 @@ __global__ __launch_bounds__(kThreads, 2) void grad_kernel(
   }
 }
 
+template <int DK, int DV, int BV>
+hipError_t launch_reverse(const GdrBwdArgs &a, const char *rec, char *dS, char *F, hipStream_t st) {
+  const GdrArgs &f = a.fwd;
+  constexpr int lds = ReverseLds<DK, BV>::kBytes;
+  auto *rev = reverse_kernel<DK, DV, BV>;
+  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(rev),
+                                     hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  if (e != hipSuccess) return e;
+  const unsigned pairs = (unsigned)((f.N * f.Hv + 7) / 8 * 8);
+  hipLaunchKernelGGL(rev, dim3(pairs * (DV / BV)), dim3(4 * BV + kThreads), lds, st,
+                     static_cast<const __hip_bfloat16 *>(f.q),
+                     static_cast<const __hip_bfloat16 *>(f.k),
+                     static_cast<const __hip_bfloat16 *>(a.d_o), a.dS_T, f.seqs, f.N, f.Hk, f.Hv,
+                     rec, dS, F, a.dS0);
+  return hipGetLastError();
+}
+
 template <int DK, int DV> hipError_t backward_typed(const GdrBwdArgs &a, hipStream_t st) {
   const GdrArgs &f = a.fwd;
   const auto *q = static_cast<const __hip_bfloat16 *>(f.q);
@@ -736,16 +759,12 @@ template <int DK, int DV> hipError_t backward_typed(const GdrBwdArgs &a, hipStre
   char *rec = static_cast<char *>(a.rec), *S = static_cast<char *>(a.S);
   char *U = static_cast<char *>(a.U), *dS = static_cast<char *>(a.dS);
   char *F = static_cast<char *>(a.F);
-  if (hipError_t e = launch_gdr_keep(f, rec, S, U, st); e != hipSuccess) return e;
-  constexpr int lds = ReverseLds<DK>::kBytes;
-  auto *rev = reverse_kernel<DK, DV>;
-  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(rev),
-                                     hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  hipError_t e = launch_gdr_keep(f, rec, S, U, st);
   if (e != hipSuccess) return e;
-  const unsigned pairs = (unsigned)((f.N * f.Hv + 7) / 8 * 8);
-  hipLaunchKernelGGL(rev, dim3(pairs * (DV / 64)), dim3(2 * kThreads), lds, st, q, k, d_o, a.dS_T,
-                     f.seqs, f.N, f.Hk, f.Hv, rec, dS, F, a.dS0);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
+  e = chain_columns(f.N * f.Hv, DV) == 64
+                     ? launch_reverse<DK, DV, 64>(a, rec, dS, F, st)
+                     : launch_reverse<DK, DV, 32>(a, rec, dS, F, st);
+  if (e != hipSuccess) return e;
   if (f.n_chunks_ub == 0) return hipSuccess;
   auto *gr = grad_kernel<DK, DV>;
   constexpr int gl = GradLds<DK, DV>::kBytes;

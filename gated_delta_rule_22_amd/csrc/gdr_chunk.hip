@@ -549,17 +549,6 @@ hipError_t launch_chain(const GdrArgs &a, char *rec, char *S, char *U, hipStream
   return hipGetLastError();
 }
 
-// Columns of a workgroup of STORE; without it, 64.  64 load a chunk's operands once for twice the
-// columns, and leave the helpers twice the threads: with an output they have so
-// much to do that 32 columns lose at any size (a layer of 128 heads 368 against
-// 203 us, one sequence of 16 heads 223 against 175).  Without one, 32 halve the
-// LDS traffic of a compute unit and win where half the chip would stand idle
-// (56 heads of 64 columns 74 against 86 us), and lose where it would not (a
-// layer 300 against 240).
-int chain_columns(int pairs, int dv) {
-  return (size_t)pairs * (dv / 64) <= 128 ? 32 : 64;
-}
-
 // prepare, then the chain; with STORE it keeps S and U and makes no output.
 template <int DK, int DV, bool STORE>
 hipError_t forward_typed(const GdrArgs &a, char *rec, char *S, char *U, hipStream_t st) {
