@@ -38,6 +38,8 @@ struct SeqTable {
     int32_t *chunk_off;
     int32_t *order;
 };
+// Sequences are ordered by length up to this many (the ranking is quadratic).
+constexpr int kRankedSeqs = 1024;
 
 // The sequences of a call: the table, or for uniform rows of T tokens (T >= 0)
 // plain arithmetic, which spares the table's launch.

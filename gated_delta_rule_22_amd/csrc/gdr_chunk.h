@@ -267,15 +267,16 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_wave_barrier();
 }
 
-// Columns of a workgroup of STORE; without it, 64.  64 load a chunk's operands once for twice the
-// columns, and leave the helpers twice the threads: with an output they have so
-// much to do that 32 columns lose at any size (a layer of 128 heads 368 against
-// 203 us, one sequence of 16 heads 223 against 175).  Without one, 32 halve the
-// LDS traffic of a compute unit and win where half the chip would stand idle
-// (56 heads of 64 columns 74 against 86 us), and lose where it would not (a
-// layer 300 against 240).
+// Value columns of a workgroup of a chain.  64 load a chunk's operands once for
+// twice the columns; 32 halve the LDS traffic of a compute unit and give each
+// chain wave two helpers, and win where compute units would stand idle, which is
+// up to this many blocks of 64 columns: forward of 1 x 4096 tokens, 16 heads of
+// 128 x 128 (32 blocks) 156 against 186 us, 4 x 2048 (128) 104 against 117, but 6 x
+// 2048 (192) 184 against 138 and the layer (256) 390 against 303; reverse chain of
+// 56 blocks of 64 90 against 123.
+constexpr size_t kFewBlocks = 128;
 inline int chain_columns(int pairs, int dv) {
-  return (size_t)pairs * (dv / 64) <= 128 ? 32 : 64;
+  return (size_t)pairs * (dv / 64) <= kFewBlocks ? 32 : 64;
 }
 
 }  // namespace gdr

@@ -255,8 +255,8 @@ __device__ __forceinline__ bool chain_block(int nblk, int pairs, int &pair, int 
 // its chunks.  Its chain waves own 16 columns each for the whole sequence, so
 // the chain S -> K S -> U -> S of a column never leaves its wave: S is 4 DK /
 // 16 accumulator registers, and each product's result tiles are the next one's
-// operand.  As many helper waves do what the chain does not wait for: they
-// load the next chunk and make the output of this one.  Two barriers a chunk:
+// operand.  Four helper waves do what the chain does not wait for: they load
+// the next chunk and make the output of this one.  Two barriers a chunk:
 // A, when the chunk's operands and S's terms are in LDS, and B, when the chain
 // has read all of them into registers and has written U; the next chunk's
 // operands take their places between B and the next A.
@@ -281,19 +281,27 @@ template <int DK, int BV, bool STORE> struct ChainLds {
 };
 
 template <int DK, int DV, int BV, bool STORE>
-__global__ __launch_bounds__(8 * BV, 2) void chain_kernel(
+__global__ __launch_bounds__(4 * BV + kThreads, 2) void chain_kernel(
     const __hip_bfloat16 *__restrict__ q, const __hip_bfloat16 *__restrict__ k,
     const __hip_bfloat16 *__restrict__ v, const float *__restrict__ S0, Seqs seqs, int N,
     int Hk, int Hv, const char *__restrict__ rec_base, __hip_bfloat16 *__restrict__ o,
-    float *__restrict__ S_T, char *__restrict__ S_keep, char *__restrict__ U_keep) {
+    float *__restrict__ S_T, char *__restrict__ S_keep, char *__restrict__ U_keep,
+    bool by_lengths) {
   using L = ChainLds<DK, BV, STORE>;
-  constexpr int KS = DK / 32, MT = DK / 16, kWaves = BV / 16, kHelp = 64 * kWaves;
+  constexpr int KS = DK / 32, MT = DK / 16, kWaves = BV / 16;
   constexpr int kRec = STORE ? kRecBwd : kRecFwd;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   int pair, blk;
   if (!chain_block(DV / BV, N * Hv, pair, blk)) return;
+  if (!STORE && by_lengths) {            // as many pairs as the longest one's time has room for
+    const size_t longest = (seqs.len(seqs.order(0)) + C - 1) / C;
+    const bool few = (size_t)seqs.first_chunk(N) * Hv * (DV / 64) <= kFewBlocks * longest;
+    if (few != (BV == 32)) return;
+  }
   const int seq = seqs.order(pair / Hv), hv = pair % Hv, hk = hv / (Hv / Hk);
-  const int wave = (threadIdx.x >> 6) % kWaves, lane = threadIdx.x & 63, m = lane & 15, h = lane >> 4;
+  const bool helper = threadIdx.x >= 64 * kWaves;
+  const int wave = (threadIdx.x >> 6) % kWaves;   // its columns
+  const int lane = threadIdx.x & 63, m = lane & 15, h = lane >> 4;
   const int len = seqs.len(seq), chunks = (len + C - 1) / C;
   const size_t row0 = seqs.start(seq);
   const size_t c0 = seqs.first_chunk(seq);
@@ -303,11 +311,15 @@ __global__ __launch_bounds__(8 * BV, 2) void chain_kernel(
   char *s_S = lds + L::kS + wave * L::kSWave + lane * 16;
   char *s_U = lds + L::kU + wave * 4 * kFrag + lane * 16;
 
-  if (threadIdx.x >= kHelp) {            // helper waves
-    const int t = threadIdx.x - kHelp;
-    Stage<DK, kHelp> gk, gq;
-    Stage<BV, kHelp> gv;
-    Linear<kRecFwd, kHelp> gr;
+  if (helper) {
+    const int t = threadIdx.x - 64 * kWaves;
+    // A helper's 16-token tiles of the output: all four, or half where two
+    // helpers share 16 columns.
+    constexpr int kIt = kWaves;
+    const int it0 = kIt == 4 ? 0 : __builtin_amdgcn_readfirstlane(t / 64 / kWaves) * kIt;
+    Stage<DK> gk, gq;
+    Stage<BV> gv;
+    Linear<kRecFwd> gr;
     auto fetch = [&](int c) {
       const int valid = min(C, len - c * C);
       const size_t row = row0 + (size_t)c * C;
@@ -331,35 +343,35 @@ __global__ __launch_bounds__(8 * BV, 2) void chain_kernel(
       lds_barrier();                     // A
       const int next = min(c + 1, chunks - 1);   // the last one again: read by nobody
       fetch(next);
-      f4 a[4];
-      bf8 p[6];
+      f4 a[kIt];
+      bf8 p[kIt][2];
       if (!STORE) {
         // O, transposed: lane = token, 4 columns a lane.
         Split s[KS];
-        bf8 qf[KS][4];
+        bf8 qf[KS][kIt];
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
           s[ks] = {*reinterpret_cast<const bf8 *>(s_S + ks * kFrag),
                    *reinterpret_cast<const bf8 *>(s_S + (KS + ks) * kFrag)};
 #pragma unroll
-          for (int it = 0; it < 4; ++it) qf[ks][it] = rows_frag<DK>(Q, 16 * it, 32 * ks, lane);
+          for (int i = 0; i < kIt; ++i)
+            qf[ks][i] = rows_frag<DK>(Q, 16 * (it0 + i), 32 * ks, lane);
         }
         fence_schedule();
 #pragma unroll
-        for (int it = 0; it < 4; ++it) a[it] = 0.f;
+        for (int i = 0; i < kIt; ++i) a[i] = 0.f;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
 #pragma unroll
-          for (int it = 0; it < 4; ++it) a[it] = mfma(s[ks].hi, qf[ks][it], a[it]);
+          for (int i = 0; i < kIt; ++i) a[i] = mfma(s[ks].hi, qf[ks][i], a[i]);
 #pragma unroll
-          for (int it = 0; it < 4; ++it) a[it] = mfma(s[ks].lo, qf[ks][it], a[it]);
+          for (int i = 0; i < kIt; ++i) a[i] = mfma(s[ks].lo, qf[ks][i], a[i]);
         }
 #pragma unroll
-        for (int it = 0; it < 4; ++it) {
-          a[it] *= gate[kGam * C + 16 * it + m];
-#pragma unroll
-          for (int ks = 0; ks <= it / 2; ++ks)
-            p[frag_at(it, ks) / kFrag] = tri_frag(R + kRecPh, it, ks, lane);
+        for (int i = 0; i < kIt; ++i) {
+          a[i] *= gate[kGam * C + 16 * (it0 + i) + m];
+          p[i][0] = tri_frag(R + kRecPh, it0 + i, 0, lane);
+          p[i][1] = it0 + i < 2 ? p[i][0] : tri_frag(R + kRecPh, it0 + i, 1, lane);
         }
       }
       lds_barrier();                     // B
@@ -372,14 +384,16 @@ __global__ __launch_bounds__(8 * BV, 2) void chain_kernel(
         const Split u1 = {*reinterpret_cast<const bf8 *>(s_U + kFrag),
                           *reinterpret_cast<const bf8 *>(s_U + 3 * kFrag)};
 #pragma unroll
-        for (int it = 0; it < 4; ++it) {
+        for (int i = 0; i < kIt; ++i) a[i] = dot2(u0, p[i][0], a[i]);
+        if (kIt == 4 || it0 > 0)
 #pragma unroll
-          for (int ks = 0; ks <= it / 2; ++ks)
-            a[it] = dot2(ks ? u1 : u0, p[frag_at(it, ks) / kFrag], a[it]);
-          const int tok = c * C + 16 * it + m;
+          for (int i = kIt == 4 ? 2 : 0; i < kIt; ++i) a[i] = dot2(u1, p[i][1], a[i]);
+#pragma unroll
+        for (int i = 0; i < kIt; ++i) {
+          const int tok = c * C + 16 * (it0 + i) + m;
           if (tok < len)
             *reinterpret_cast<bf4 *>(o + ((row0 + tok) * Hv + hv) * DV + col + 4 * h) =
-                round4(a[it]);
+                round4(a[i]);
         }
       }
     }
@@ -537,15 +551,16 @@ template <typename F> hipError_t allow_lds(F *f, int bytes) {
 }
 
 template <int DK, int DV, int BV, bool STORE>
-hipError_t launch_chain(const GdrArgs &a, char *rec, char *S, char *U, hipStream_t st) {
+hipError_t launch_chain(const GdrArgs &a, char *rec, char *S, char *U, bool by_lengths,
+                        hipStream_t st) {
   constexpr int lds = ChainLds<DK, BV, STORE>::kBytes;
   auto *kernel = chain_kernel<DK, DV, BV, STORE>;
   if (hipError_t e = allow_lds(kernel, lds); e != hipSuccess) return e;
-  hipLaunchKernelGGL(kernel, dim3(chain_grid(a.N * a.Hv, DV / BV)), dim3(8 * BV), lds, st,
+  hipLaunchKernelGGL(kernel, dim3(chain_grid(a.N * a.Hv, DV / BV)), dim3(4 * BV + kThreads), lds, st,
                      static_cast<const __hip_bfloat16 *>(a.q),
                      static_cast<const __hip_bfloat16 *>(a.k),
                      static_cast<const __hip_bfloat16 *>(a.v), a.S0, a.seqs, a.N, a.Hk, a.Hv, rec,
-                     static_cast<__hip_bfloat16 *>(a.o), a.S_T, S, U);
+                     static_cast<__hip_bfloat16 *>(a.o), a.S_T, S, U, by_lengths);
   return hipGetLastError();
 }
 
@@ -560,10 +575,16 @@ hipError_t forward_typed(const GdrArgs &a, char *rec, char *S, char *U, hipStrea
                        q, k, a.g, a.beta, a.seqs, a.N, a.Hk, a.Hv, rec);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }
-  if constexpr (STORE)
-    if (chain_columns(a.N * a.Hv, DV) == 32)
-      return launch_chain<DK, DV, 32, STORE>(a, rec, S, U, st);
-  return launch_chain<DK, DV, 64, STORE>(a, rec, S, U, st);
+  const bool few = chain_columns(a.N * a.Hv, DV) == 32;
+  // Packed sequences that are many, but of which a few may be long: the lengths
+  // say on the device which of the two kernels runs, and the other one ends at
+  // once.  (Both are launched where their order by length is known.)
+  const bool by_lengths = !STORE && !few && a.seqs.T < 0 && a.N <= kRankedSeqs;
+  if (few || by_lengths) {
+    const hipError_t e = launch_chain<DK, DV, 32, STORE>(a, rec, S, U, by_lengths, st);
+    if (e != hipSuccess || few) return e;
+  }
+  return launch_chain<DK, DV, 64, STORE>(a, rec, S, U, by_lengths, st);
 }
 
 template <bool STORE>

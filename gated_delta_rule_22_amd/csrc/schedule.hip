@@ -17,7 +17,6 @@ namespace ckda {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRankMax = 1024;   // rank-sort sequences only up to this many
 
 // Inclusive scan of s_part[1 .. kThreads] over the workgroup (s_part[0] stays).
 template <typename F> __device__ __forceinline__ void scan(int32_t *s_part, int t, F op) {
@@ -76,7 +75,7 @@ __global__ __launch_bounds__(kThreads) void seq_table_kernel(const int32_t *__re
   if (t == kThreads - 1) tab.chunk_off[N] = s_part[kThreads];
 
   // order: longest first.
-  const bool rank = cu != nullptr && N <= kRankMax;
+  const bool rank = cu != nullptr && N <= kRankedSeqs;
   for (int i = t; i < N; i += kThreads) {
     if (!rank) {
       tab.order[i] = i;

@@ -200,3 +200,18 @@ def test_prefill_then_steps(dtype):
     for t in range(80, 90):
         out.append(ck.gdr_decode_step(*(d[n][t:t + 1] for n in ("q", "k", "v", "g", "beta")), S))
     assert rel(torch.cat(out), ro) < TOL[dtype][0] and rel(S, rS) < TOL[dtype][1]
+
+
+@pytest.mark.parametrize("lens", [[900, 3, 0, 70, 64, 1, 33, 200, 65], [130] * 9, [2000] + [1] * 8])
+def test_packed_batches_long_and_even(lens):
+    """More than 128 blocks of 64 columns: how even the lengths are decides how a head's
+    columns are cut, and results are the sequences' own either way."""
+    hk, hv = 4, 16
+    x = inputs(41, lens, hk, hv, 64, 64, BF)
+    check(x, lens, BF)
+    o, S = run(x, lens)
+    at, n = sum(lens[:3]), lens[3]
+    one = {m: x[m][at:at + n] for m in ("q", "k", "v", "g", "beta")}
+    one["S0"] = x["S0"][3:4]
+    oo, SS = run(one, [n])
+    assert torch.equal(o[at:at + n], oo) and torch.equal(S[3:4], SS)
