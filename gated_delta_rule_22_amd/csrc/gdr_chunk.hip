@@ -263,15 +263,16 @@ __device__ __forceinline__ bool chain_block(int nblk, int pairs, int &pair, int 
 // STORE: for the backward, keeps the state before each chunk and U (two bf16
 // terms each) and makes no output.
 //
-// A chunk takes 2.6 to 3.1 us (5800 cycles) whatever runs beside it, and 2.3
-// without any helper work: the chain's own latency bounds it, K S (1300
+// A chunk takes 2.6 to 3.1 us (5800 cycles) on 64 columns, and 2.26 on 32, where
+// two helpers share a chain wave's output: the chain's own latency, K S (1300
 // cycles), T X (1000), U's terms and the barrier (700), K^T U (1600) and the
-// next state's terms (1100), each of which waits for the one before; 1400 of
-// the 5800 are matrix instructions.  8 x 4096 tokens of 16 heads of 128 x 128:
-// 203 to 209 us for 714 MB (3.5 TB/s); STORE 240 us for 1.24 GB (5.2 TB/s, a
-// copy's rate).  Tried and slower: operands a whole chunk ahead (255 us, too
-// many registers), half of the products with the state behind barrier B with
-// K and Q twice in LDS (217), rows padded instead of the swizzle (+15%).
+// next state's terms (1000), each of which waits for the one before; 1400 of
+// them are matrix instructions.  8 x 4096 tokens of 16 heads of 128 x 128: 203 to
+// 212 us for 714 MB (3.5 TB/s); STORE 240 us for 1.24 GB (5.2 TB/s, a copy's
+// rate).  Tried and slower: operands a whole chunk ahead (255 us, too many
+// registers), half of the products with the state behind barrier B with K and Q
+// twice in LDS (217), U's terms and barrier B behind the products of the next
+// state (238: the helpers wait), rows padded instead of the swizzle (+15%).
 template <int DK, int BV, bool STORE> struct ChainLds {
   static constexpr int kK = 0, kV = gdr::kTile<DK>, kRec = kV + gdr::kTile<BV>;
   static constexpr int kQ = kRec + kRecFwd;                      // the rest: !STORE
@@ -578,8 +579,12 @@ hipError_t forward_typed(const GdrArgs &a, char *rec, char *S, char *U, hipStrea
   const bool few = chain_columns(a.N * a.Hv, DV) == 32;
   // Packed sequences that are many, but of which a few may be long: the lengths
   // say on the device which of the two kernels runs, and the other one ends at
-  // once.  (Both are launched where their order by length is known.)
-  const bool by_lengths = !STORE && !few && a.seqs.T < 0 && a.N <= kRankedSeqs;
+  // once (ten sequences, the longest 8192 tokens, of 16 heads of 128 x 128: 289
+  // against 336 us).  Both are launched where the order by length is known, and
+  // where the longest can have so many chunks that their 0.35 us each pay for the
+  // 4 us of the other launch: 64 chunks in all.
+  const bool by_lengths = !STORE && !few && a.seqs.T < 0 && a.N <= kRankedSeqs &&
+                          a.n_chunks_ub >= 64 + (size_t)a.N;
   if (few || by_lengths) {
     const hipError_t e = launch_chain<DK, DV, 32, STORE>(a, rec, S, U, by_lengths, st);
     if (e != hipSuccess || few) return e;

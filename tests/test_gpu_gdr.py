@@ -202,10 +202,11 @@ def test_prefill_then_steps(dtype):
     assert rel(torch.cat(out), ro) < TOL[dtype][0] and rel(S, rS) < TOL[dtype][1]
 
 
-@pytest.mark.parametrize("lens", [[900, 3, 0, 70, 64, 1, 33, 200, 65], [130] * 9, [2000] + [1] * 8])
+@pytest.mark.parametrize("lens", [[900, 3, 0, 70, 64, 1, 33, 200, 65], [130] * 9, [2000] + [1] * 8,
+                                  [3900, 3, 0, 170, 64, 1, 33, 200, 65], [470] * 9])
 def test_packed_batches_long_and_even(lens):
-    """More than 128 blocks of 64 columns: how even the lengths are decides how a head's
-    columns are cut, and results are the sequences' own either way."""
+    """More than 128 blocks of 64 columns: from 64 chunks on, how even the lengths are decides
+    how a head's columns are cut, and results are the sequences' own either way."""
     hk, hv = 4, 16
     x = inputs(41, lens, hk, hv, 64, 64, BF)
     check(x, lens, BF)
