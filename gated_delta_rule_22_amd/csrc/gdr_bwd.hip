@@ -22,18 +22,11 @@
 // backwards (dS', F), each serial in the chunks of a (sequence, head), and the
 // gradients, parallel over chunks.  Everything that feeds an fp32 gradient
 // (dg, dbeta, dS0) runs in two bf16 terms, as in the forward.
-#include "gdr_chunk.h"
+#include "gdr_chain.h"
 
 namespace ckda {
 using namespace gdr;
 namespace {
-
-__device__ __forceinline__ bool chain_block(int nblk, int pairs, int &pair, int &blk) {
-  const int b = blockIdx.x;              // as in the forward: a head's blocks share an XCD
-  blk = (b / 8) % nblk;
-  pair = (b / 8 / nblk) * 8 + b % 8;
-  return pair < pairs;
-}
 
 // The chain of dS, last chunk first.  As in the forward's chain four waves own
 // 16 of the DV columns each, so dS -> dU -> F -> dS stays in their registers,
@@ -55,16 +48,15 @@ template <int DK, int BV> struct ReverseLds {
 };
 
 template <int DK, int DV, int BV>
-__global__ __launch_bounds__(4 * BV + kThreads, 2) void reverse_kernel(
-    const __hip_bfloat16 *__restrict__ q, const __hip_bfloat16 *__restrict__ k,
+__device__ __forceinline__ void reverse_body(
+    int block, char *lds, const __hip_bfloat16 *__restrict__ q, const __hip_bfloat16 *__restrict__ k,
     const __hip_bfloat16 *__restrict__ d_o, const float *__restrict__ dS_T, Seqs seqs, int N,
     int Hk, int Hv, const char *__restrict__ rec_base, char *__restrict__ dS_keep,
     char *__restrict__ F_keep, float *__restrict__ dS0) {
   using L = ReverseLds<DK, BV>;
   constexpr int KS = DK / 32, MT = DK / 16, kChain = 4 * BV;   // threads of the chain
-  extern __shared__ __attribute__((aligned(16))) char lds[];
   int pair, blk;
-  if (!chain_block(DV / BV, N * Hv, pair, blk)) return;
+  if (!chain_block(block, DV / BV, N * Hv, pair, blk)) return;
   const int seq = seqs.order(pair / Hv), hv = pair % Hv, hk = hv / (Hv / Hk);
   const bool helper = threadIdx.x >= kChain;
   const int wave = (threadIdx.x - (helper ? kChain : 0)) >> 6;
@@ -329,6 +321,37 @@ __global__ __launch_bounds__(4 * BV + kThreads, 2) void reverse_kernel(
 #pragma unroll
       for (int r = 0; r < 4; ++r)
         dS0[sbase + (size_t)(16 * i + 4 * h + r) * DV] = S[i][r];
+}
+
+template <int DK, int DV>
+__global__ __launch_bounds__(2 * kThreads, 2) void reverse_kernel(
+    const __hip_bfloat16 *__restrict__ q, const __hip_bfloat16 *__restrict__ k,
+    const __hip_bfloat16 *__restrict__ d_o, const float *__restrict__ dS_T, Seqs seqs, int N,
+    int Hk, int Hv, const char *__restrict__ rec_base, char *__restrict__ dS_keep,
+    char *__restrict__ F_keep, float *__restrict__ dS0) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  reverse_body<DK, DV, 64>(blockIdx.x, lds, q, k, d_o, dS_T, seqs, N, Hk, Hv, rec_base, dS_keep,
+                           F_keep, dS0);
+}
+
+// Neither chain needs anything of the other: where few pairs leave compute units
+// idle one launch runs both, the longer reverse chains first, on 32 columns each
+// (seven packed sequences of 8 heads, the longest 2500 tokens: MEASURED).
+template <int DK, int DV>
+__global__ __launch_bounds__(128 + kThreads, 2) void chains_kernel(
+    const __hip_bfloat16 *__restrict__ q, const __hip_bfloat16 *__restrict__ k,
+    const __hip_bfloat16 *__restrict__ v, const __hip_bfloat16 *__restrict__ d_o,
+    const float *__restrict__ S0, const float *__restrict__ dS_T, Seqs seqs, int N, int Hk, int Hv,
+    const char *__restrict__ rec_base, char *__restrict__ S_keep, char *__restrict__ U_keep,
+    char *__restrict__ dS_keep, char *__restrict__ F_keep, float *__restrict__ dS0) {
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  const int half = gridDim.x / 2, b = blockIdx.x;
+  if (b < half)
+    reverse_body<DK, DV, 32>(b, lds, q, k, d_o, dS_T, seqs, N, Hk, Hv, rec_base, dS_keep, F_keep,
+                             dS0);
+  else
+    chain_body<DK, DV, 32, true>(b - half, lds, q, k, v, S0, seqs, N, Hk, Hv, rec_base, nullptr,
+                                 nullptr, S_keep, U_keep, false);
 }
 
 // ---------------------------------------------------------------- gradients
@@ -734,43 +757,42 @@ __global__ __launch_bounds__(kThreads, 2) void grad_kernel(
   }
 }
 
-template <int DK, int DV, int BV>
-hipError_t launch_reverse(const GdrBwdArgs &a, const char *rec, char *dS, char *F, hipStream_t st) {
-  const GdrArgs &f = a.fwd;
-  constexpr int lds = ReverseLds<DK, BV>::kBytes;
-  auto *rev = reverse_kernel<DK, DV, BV>;
-  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(rev),
-                                     hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-  if (e != hipSuccess) return e;
-  const unsigned pairs = (unsigned)((f.N * f.Hv + 7) / 8 * 8);
-  hipLaunchKernelGGL(rev, dim3(pairs * (DV / BV)), dim3(4 * BV + kThreads), lds, st,
-                     static_cast<const __hip_bfloat16 *>(f.q),
-                     static_cast<const __hip_bfloat16 *>(f.k),
-                     static_cast<const __hip_bfloat16 *>(a.d_o), a.dS_T, f.seqs, f.N, f.Hk, f.Hv,
-                     rec, dS, F, a.dS0);
-  return hipGetLastError();
-}
-
 template <int DK, int DV> hipError_t backward_typed(const GdrBwdArgs &a, hipStream_t st) {
   const GdrArgs &f = a.fwd;
   const auto *q = static_cast<const __hip_bfloat16 *>(f.q);
   const auto *k = static_cast<const __hip_bfloat16 *>(f.k);
+  const auto *v = static_cast<const __hip_bfloat16 *>(f.v);
   const auto *d_o = static_cast<const __hip_bfloat16 *>(a.d_o);
   char *rec = static_cast<char *>(a.rec), *S = static_cast<char *>(a.S);
   char *U = static_cast<char *>(a.U), *dS = static_cast<char *>(a.dS);
   char *F = static_cast<char *>(a.F);
   hipError_t e = launch_gdr_keep(f, rec, S, U, st);
   if (e != hipSuccess) return e;
-  e = chain_columns(f.N * f.Hv, DV) == 64
-                     ? launch_reverse<DK, DV, 64>(a, rec, dS, F, st)
-                     : launch_reverse<DK, DV, 32>(a, rec, dS, F, st);
-  if (e != hipSuccess) return e;
+  auto lds_of = [](auto *kernel, int bytes) {
+    return hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                               hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  };
+  const int pairs = f.N * f.Hv;
+  if (chain_columns(pairs, DV) == 64) {
+    constexpr int lds = ReverseLds<DK, 64>::kBytes;
+    auto *kernel = reverse_kernel<DK, DV>;
+    if ((e = lds_of(kernel, lds)) != hipSuccess) return e;
+    hipLaunchKernelGGL(kernel, dim3(chain_grid(pairs, DV / 64)), dim3(2 * kThreads), lds, st, q, k,
+                       d_o, a.dS_T, f.seqs, f.N, f.Hk, f.Hv, rec, dS, F, a.dS0);
+  } else {
+    constexpr int r = ReverseLds<DK, 32>::kBytes, c = ChainLds<DK, 32, true>::kBytes;
+    constexpr int lds = r > c ? r : c;
+    auto *kernel = chains_kernel<DK, DV>;
+    if ((e = lds_of(kernel, lds)) != hipSuccess) return e;
+    hipLaunchKernelGGL(kernel, dim3(2 * chain_grid(pairs, DV / 32)), dim3(128 + kThreads), lds, st,
+                       q, k, v, d_o, f.S0, a.dS_T, f.seqs, f.N, f.Hk, f.Hv, rec, S, U, dS, F,
+                       a.dS0);
+  }
+  if ((e = hipGetLastError()) != hipSuccess) return e;
   if (f.n_chunks_ub == 0) return hipSuccess;
   auto *gr = grad_kernel<DK, DV>;
   constexpr int gl = GradLds<DK, DV>::kBytes;
-  e = hipFuncSetAttribute(reinterpret_cast<const void *>(gr),
-                          hipFuncAttributeMaxDynamicSharedMemorySize, gl);
-  if (e != hipSuccess) return e;
+  if ((e = lds_of(gr, gl)) != hipSuccess) return e;
   hipLaunchKernelGGL(gr, dim3((unsigned)(f.n_chunks_ub * f.Hk)), dim3(kThreads), gl, st, q, k, f.g,
                      f.beta, d_o, f.seqs, f.N, f.Hk, f.Hv, rec, S, U, dS, F,
                      static_cast<__hip_bfloat16 *>(a.dq), static_cast<__hip_bfloat16 *>(a.dk),

@@ -1,0 +1,314 @@
+// The chain of the chunkwise gated delta rule: what a workgroup does with some
+// columns of one (sequence, head), for the forward's kernel and the backward's.
+#pragma once
+
+#include "gdr_chunk.h"
+
+namespace ckda {
+namespace gdr {
+
+// Workgroups of one (sequence, head) -- its column blocks -- share an XCD's
+// L2: consecutive workgroups go round the 8 XCDs.
+__device__ __forceinline__ bool chain_block(int b, int nblk, int pairs, int &pair, int &blk) {
+  blk = (b / 8) % nblk;
+  pair = (b / 8 / nblk) * 8 + b % 8;
+  return pair < pairs;
+}
+
+// -------------------------------------------------------------------- chain
+// A workgroup runs BV of the state's DV columns of one (sequence, head) over
+// its chunks.  Its chain waves own 16 columns each for the whole sequence, so
+// the chain S -> K S -> U -> S of a column never leaves its wave: S is 4 DK /
+// 16 accumulator registers, and each product's result tiles are the next one's
+// operand.  Four helper waves do what the chain does not wait for: they load
+// the next chunk and make the output of this one.  Two barriers a chunk:
+// A, when the chunk's operands and S's terms are in LDS, and B, when the chain
+// has read all of them into registers and has written U; the next chunk's
+// operands take their places between B and the next A.
+// STORE: for the backward, keeps the state before each chunk and U (two bf16
+// terms each) and makes no output.
+//
+// A chunk takes 2.6 to 3.1 us (5800 cycles) on 64 columns, and 2.26 on 32, where
+// two helpers share a chain wave's output: the chain's own latency, K S (1300
+// cycles), T X (1000), U's terms and the barrier (700), K^T U (1600) and the
+// next state's terms (1000), each of which waits for the one before; 1400 of
+// them are matrix instructions.  8 x 4096 tokens of 16 heads of 128 x 128: 203 to
+// 212 us for 714 MB (3.5 TB/s); STORE 240 us for 1.24 GB (5.2 TB/s, a copy's
+// rate).  Tried and slower: operands a whole chunk ahead (255 us, too many
+// registers), half of the products with the state behind barrier B with K and Q
+// twice in LDS (217), U's terms and barrier B behind the products of the next
+// state (238: the helpers wait), rows padded instead of the swizzle (+15%).
+template <int DK, int BV, bool STORE> struct ChainLds {
+  static constexpr int kK = 0, kV = gdr::kTile<DK>, kRec = kV + gdr::kTile<BV>;
+  static constexpr int kQ = kRec + kRecFwd;                      // the rest: !STORE
+  static constexpr int kS = kQ + gdr::kTile<DK>, kSWave = 2 * (DK / 32) * kFrag;
+  static constexpr int kU = kS + BV / 16 * kSWave;
+  static constexpr int kBytes = STORE ? kQ : kU + BV / 16 * 4 * kFrag;
+};
+
+template <int DK, int DV, int BV, bool STORE>
+__device__ __forceinline__ void chain_body(
+    int block, char *lds, const __hip_bfloat16 *__restrict__ q, const __hip_bfloat16 *__restrict__ k,
+    const __hip_bfloat16 *__restrict__ v, const float *__restrict__ S0, Seqs seqs, int N,
+    int Hk, int Hv, const char *__restrict__ rec_base, __hip_bfloat16 *__restrict__ o,
+    float *__restrict__ S_T, char *__restrict__ S_keep, char *__restrict__ U_keep,
+    bool by_lengths) {
+  using L = ChainLds<DK, BV, STORE>;
+  constexpr int KS = DK / 32, MT = DK / 16, kWaves = BV / 16;
+  constexpr int kRec = STORE ? kRecBwd : kRecFwd;
+  int pair, blk;
+  if (!chain_block(block, DV / BV, N * Hv, pair, blk)) return;
+  if (!STORE && by_lengths) {            // as many pairs as the longest one's time has room for
+    const size_t longest = (seqs.len(seqs.order(0)) + C - 1) / C;
+    const bool few = (size_t)seqs.first_chunk(N) * Hv * (DV / 64) <= kFewBlocks * longest;
+    if (few != (BV == 32)) return;
+  }
+  const int seq = seqs.order(pair / Hv), hv = pair % Hv, hk = hv / (Hv / Hk);
+  const bool helper = threadIdx.x >= 64 * kWaves;
+  const int wave = (threadIdx.x >> 6) % kWaves;   // its columns
+  const int lane = threadIdx.x & 63, m = lane & 15, h = lane >> 4;
+  const int len = seqs.len(seq), chunks = (len + C - 1) / C;
+  const size_t row0 = seqs.start(seq);
+  const size_t c0 = seqs.first_chunk(seq);
+  const int col = blk * BV + 16 * wave;  // of the head's DV
+  const char *K = lds + L::kK, *V = lds + L::kV, *R = lds + L::kRec, *Q = lds + L::kQ;
+  const float *gate = reinterpret_cast<const float *>(R + kRecGate);
+  char *s_S = lds + L::kS + wave * L::kSWave + lane * 16;
+  char *s_U = lds + L::kU + wave * 4 * kFrag + lane * 16;
+
+  if (helper) {
+    const int t = threadIdx.x - 64 * kWaves;
+    // A helper's 16-token tiles of the output: all four, or half where two
+    // helpers share 16 columns.
+    constexpr int kIt = kWaves;
+    const int it0 = kIt == 4 ? 0 : __builtin_amdgcn_readfirstlane(t / 64 / kWaves) * kIt;
+    Stage<DK> gk, gq;
+    Stage<BV> gv;
+    Linear<kRecFwd> gr;
+    auto fetch = [&](int c) {
+      const int valid = min(C, len - c * C);
+      const size_t row = row0 + (size_t)c * C;
+      gk.load(k + (row * Hk + hk) * DK, (size_t)Hk * DK, valid, t);
+      if (!STORE) gq.load(q + (row * Hk + hk) * DK, (size_t)Hk * DK, valid, t);
+      gv.load(v + (row * Hv + hv) * DV + blk * BV, (size_t)Hv * DV, valid, t);
+      gr.load(rec_base + ((c0 + c) * Hv + hv) * kRec, t);
+    };
+    auto put = [&](int c) {
+      const int valid = min(C, len - c * C);
+      gk.store(lds + L::kK, valid, t);
+      if (!STORE) gq.store(lds + L::kQ, valid, t);
+      gv.store(lds + L::kV, valid, t);
+      gr.store(lds + L::kRec, t);
+    };
+    if (chunks > 0) {
+      fetch(0);
+      put(0);
+    }
+    for (int c = 0; c < chunks; ++c) {
+      lds_barrier();                     // A
+      const int next = min(c + 1, chunks - 1);   // the last one again: read by nobody
+      fetch(next);
+      f4 a[kIt];
+      bf8 p[kIt][2];
+      if (!STORE) {
+        // O, transposed: lane = token, 4 columns a lane.
+        Split s[KS];
+        bf8 qf[KS][kIt];
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          s[ks] = {*reinterpret_cast<const bf8 *>(s_S + ks * kFrag),
+                   *reinterpret_cast<const bf8 *>(s_S + (KS + ks) * kFrag)};
+#pragma unroll
+          for (int i = 0; i < kIt; ++i)
+            qf[ks][i] = rows_frag<DK>(Q, 16 * (it0 + i), 32 * ks, lane);
+        }
+        fence_schedule();
+#pragma unroll
+        for (int i = 0; i < kIt; ++i) a[i] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+#pragma unroll
+          for (int i = 0; i < kIt; ++i) a[i] = mfma(s[ks].hi, qf[ks][i], a[i]);
+#pragma unroll
+          for (int i = 0; i < kIt; ++i) a[i] = mfma(s[ks].lo, qf[ks][i], a[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < kIt; ++i) {
+          a[i] *= gate[kGam * C + 16 * (it0 + i) + m];
+          p[i][0] = tri_frag(R + kRecPh, it0 + i, 0, lane);
+          p[i][1] = it0 + i < 2 ? p[i][0] : tri_frag(R + kRecPh, it0 + i, 1, lane);
+        }
+      }
+      lds_barrier();                     // B
+      put(next);                         // before the stores, which loads' waits count too
+      if (!STORE) {
+        // One term of P: it is within 2^-9 of its value, and so is the bf16
+        // output itself.
+        const Split u0 = {*reinterpret_cast<const bf8 *>(s_U),
+                          *reinterpret_cast<const bf8 *>(s_U + 2 * kFrag)};
+        const Split u1 = {*reinterpret_cast<const bf8 *>(s_U + kFrag),
+                          *reinterpret_cast<const bf8 *>(s_U + 3 * kFrag)};
+#pragma unroll
+        for (int i = 0; i < kIt; ++i) a[i] = dot2(u0, p[i][0], a[i]);
+        if (kIt == 4 || it0 > 0)
+#pragma unroll
+          for (int i = kIt == 4 ? 2 : 0; i < kIt; ++i) a[i] = dot2(u1, p[i][1], a[i]);
+#pragma unroll
+        for (int i = 0; i < kIt; ++i) {
+          const int tok = c * C + 16 * (it0 + i) + m;
+          if (tok < len)
+            *reinterpret_cast<bf4 *>(o + ((row0 + tok) * Hv + hv) * DV + col + 4 * h) =
+                round4(a[i]);
+        }
+      }
+    }
+    return;
+  }
+
+  f4 S[MT];
+  const size_t sbase = ((size_t)seq * Hv + hv) * DK * DV + col + m;
+#pragma unroll
+  for (int i = 0; i < MT; ++i) S[i] = 0.f;
+  if (S0)
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) S[i][r] = S0[sbase + (size_t)(16 * i + 4 * h + r) * DV];
+
+  // The gate factors of a lane's tokens come from memory a chunk ahead: read
+  // from LDS they would be 9 cycles of its time each for 64 bytes.
+  f4 gam[4], last[4], bet[4];
+  float gn = 0.f;
+  auto fetch_gates = [&](int c) {
+    const float *g = reinterpret_cast<const float *>(rec_base + ((c0 + c) * Hv + hv) * kRec +
+                                                     kRecGate);
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      gam[it] = *reinterpret_cast<const f4 *>(g + kGam * C + 16 * it + 4 * h);
+      last[it] = *reinterpret_cast<const f4 *>(g + kLast * C + 16 * it + 4 * h);
+      bet[it] = *reinterpret_cast<const f4 *>(g + kBeta * C + 16 * it + 4 * h);
+    }
+    gn = g[kGam * C + C - 1];
+  };
+  if (chunks > 0) fetch_gates(0);
+  __builtin_amdgcn_s_setprio(2);         // the chain before the helper on its SIMD
+  for (int c = 0; c < chunks; ++c) {
+    Split sf[KS];
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      sf[ks] = split8(S[2 * ks], S[2 * ks + 1]);
+      if (!STORE) {
+        *reinterpret_cast<bf8 *>(s_S + ks * kFrag) = sf[ks].hi;
+        *reinterpret_cast<bf8 *>(s_S + (KS + ks) * kFrag) = sf[ks].lo;
+      }
+    }
+    lds_barrier();                       // A
+    if (STORE) {
+      char *p = S_keep + (((c0 + c) * Hv + hv) * (2 * KS * (DV / 16)) + col / 16) * kFrag +
+                lane * 16;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        *reinterpret_cast<bf8 *>(p + ks * (DV / 16) * kFrag) = sf[ks].hi;
+        *reinterpret_cast<bf8 *>(p + (KS + ks) * (DV / 16) * kFrag) = sf[ks].lo;
+      }
+    }
+    // X = V - gam K S, as the operand of T' X
+    bf8 kf[KS][4];
+    f4 X[4];
+    auto read_k = [&](int ks) {
+#pragma unroll
+      for (int it = 0; it < 4; ++it) kf[ks][it] = rows_frag<DK>(K, 16 * it, 32 * ks, lane);
+    };
+    auto times_s = [&](int ks) {
+#pragma unroll
+      for (int it = 0; it < 4; ++it) X[it] = mfma(kf[ks][it], sf[ks].hi, ks ? X[it] : f4(0.f));
+#pragma unroll
+      for (int it = 0; it < 4; ++it) X[it] = mfma(kf[ks][it], sf[ks].lo, X[it]);
+    };
+    read_k(0);
+    read_k(1);
+    fence_schedule();
+    if (KS > 2) {
+      read_k(KS - 2);
+      read_k(KS - 1);
+    }
+    times_s(0);
+    fence_schedule();
+    bf4 vq[4];
+    Split T[6];
+#pragma unroll
+    for (int it = 0; it < 4; ++it) vq[it] = cols_quad<BV>(V, 16 * it, 16 * wave, lane);
+#pragma unroll
+    for (int f = 0; f < 6; ++f)
+      T[f] = {*reinterpret_cast<const bf8 *>(R + kRecTh + f * kFrag + lane * 16),
+              *reinterpret_cast<const bf8 *>(R + kRecTl + f * kFrag + lane * 16)};
+#pragma unroll
+    for (int ks = 1; ks < KS; ++ks) times_s(ks);
+    fence_schedule();
+    bf8 kt[2][MT];                       // K^T for the update, read meanwhile
+#pragma unroll
+    for (int i = 0; i < MT; ++i) kt[0][i] = cols_frag<DK>(K, 0, 16 * i, lane);
+#pragma unroll
+    for (int it = 0; it < 4; ++it) X[it] = widen4(vq[it]) - gam[it] * X[it];
+    const Split x0 = split8(X[0], X[1]), x1 = split8(X[2], X[3]);
+    fence_schedule();
+    f4 U[4];
+#pragma unroll
+    for (int it = 0; it < 4; ++it) U[it] = X[it];
+    // the four tiles' products turn by turn: each waits for its own last one
+#pragma unroll
+    for (int term = 0; term < 4; ++term)
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int it = 2 * ks; it < 4; ++it) {
+          const Split &t = T[frag_at(it, ks) / kFrag];
+          const Split &x = ks ? x1 : x0;
+          U[it] = mfma(term & 2 ? t.lo : t.hi, term & 1 ? x.lo : x.hi, U[it]);
+        }
+#pragma unroll
+    for (int i = 0; i < MT; ++i) S[i] *= gn;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) kt[1][i] = cols_frag<DK>(K, 32, 16 * i, lane);
+#pragma unroll
+    for (int it = 0; it < 4; ++it) U[it] *= bet[it];
+    {
+      const Split u0 = split8(U[0], U[1]), u1 = split8(U[2], U[3]);
+      char *p = STORE ? U_keep + (((c0 + c) * Hv + hv) * (4 * (DV / 16)) + col / 16) * kFrag +
+                            lane * 16
+                      : s_U;
+      constexpr int step = STORE ? (DV / 16) * kFrag : kFrag;
+      *reinterpret_cast<bf8 *>(p) = u0.hi;
+      *reinterpret_cast<bf8 *>(p + step) = u1.hi;
+      *reinterpret_cast<bf8 *>(p + 2 * step) = u0.lo;
+      *reinterpret_cast<bf8 *>(p + 3 * step) = u1.lo;
+    }
+    fence_schedule();
+    lds_barrier();                       // B
+    fence_schedule();
+#pragma unroll
+    for (int it = 0; it < 4; ++it) U[it] *= last[it];
+    fetch_gates(min(c + 1, chunks - 1));
+    const Split w0 = split8(U[0], U[1]), w1 = split8(U[2], U[3]);
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+      for (int term = 0; term < 2; ++term)
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          const Split &w = ks ? w1 : w0;
+          S[i] = mfma(kt[ks][i], term ? w.lo : w.hi, S[i]);
+        }
+  }
+  if (S_T)
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        S_T[sbase + (size_t)(16 * i + 4 * h + r) * DV] = S[i][r];
+}
+
+inline unsigned chain_grid(int pairs, int nblk) { return (unsigned)((pairs + 7) / 8 * 8) * nblk; }
+
+}  // namespace gdr
+}  // namespace ckda
