@@ -148,9 +148,8 @@ hipError_t launch_gdr_token(const GdrArgs &a, hipStream_t stream);
 // gdr_forward_rec_bytes() for every chunk and value head.
 size_t gdr_forward_rec_bytes();
 hipError_t launch_gdr_forward(const GdrArgs &a, void *rec, hipStream_t stream);
-// The same chain for the backward: keeps the state before every chunk and U
-// (two bf16 terms each, in result-tile order) and makes no output.
-hipError_t launch_gdr_keep(const GdrArgs &a, void *rec, void *S, void *U, hipStream_t stream);
+// The backward's records, which hold P's second term too.
+hipError_t launch_gdr_prepare_backward(const GdrArgs &a, void *rec, hipStream_t stream);
 struct GdrBwdArgs {
     GdrArgs fwd;                         // fwd.S_T is NULL
     const void *d_o;

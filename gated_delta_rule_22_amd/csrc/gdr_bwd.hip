@@ -18,9 +18,9 @@
 // each, and beta is kept off zero by kBetaFloor, so F.U / beta^2 holds at
 // beta = 0 too.)
 //
-// Three passes: the forward's chain kept per chunk (S, U), the chain of dS
-// backwards (dS', F), each serial in the chunks of a (sequence, head), and the
-// gradients, parallel over chunks.  Everything that feeds an fp32 gradient
+// Three parts: the forward's chain kept per chunk (S, U) and, beside it, the
+// chain of dS backwards (dS', F), each serial in the chunks of a (sequence,
+// head), then the gradients, parallel over chunks.  Everything that feeds an fp32 gradient
 // (dg, dbeta, dS0) runs in two bf16 terms, as in the forward.
 #include "gdr_chain.h"
 
@@ -36,10 +36,11 @@ namespace {
 // Barrier A: the chunk's operands and those tiles are in LDS; barrier B: the
 // chain has read all of them into registers.
 //
-// 8 x 4096 tokens of 16 heads of 128 x 128: 303 us for the 1.43 GB that it reads
-// and writes (4.7 TB/s, 277 at a copy's rate); where few sequences leave memory
-// idle, a chunk takes 3.1 us, the chain's latency (406 us on the layer without
-// helper waves, 325 with them, 303 with reads in batches and no conflicts).
+// 8 x 4096 tokens of 16 heads of 128 x 128: 303 us alone for the 1.43 GB that it
+// reads and writes (4.7 TB/s, 277 at a copy's rate); a chunk takes the chain's
+// latency otherwise, 3.1 us on 64 columns and 2.3 on 32.  (406 us on the layer
+// without helper waves, 325 with them, 303 with reads in batches and without
+// bank conflicts.)
 template <int DK, int BV> struct ReverseLds {
   static constexpr int kWave = (4 + DK / 16) * 1024;   // a wave's tiles
   static constexpr int kK = 0, kT = kTile<DK>, kQ = kT + 2 * kTri, kD = kQ + kTile<DK>;
@@ -323,22 +324,14 @@ __device__ __forceinline__ void reverse_body(
         dS0[sbase + (size_t)(16 * i + 4 * h + r) * DV] = S[i][r];
 }
 
-template <int DK, int DV>
-__global__ __launch_bounds__(2 * kThreads, 2) void reverse_kernel(
-    const __hip_bfloat16 *__restrict__ q, const __hip_bfloat16 *__restrict__ k,
-    const __hip_bfloat16 *__restrict__ d_o, const float *__restrict__ dS_T, Seqs seqs, int N,
-    int Hk, int Hv, const char *__restrict__ rec_base, char *__restrict__ dS_keep,
-    char *__restrict__ F_keep, float *__restrict__ dS0) {
-  extern __shared__ __attribute__((aligned(16))) char lds[];
-  reverse_body<DK, DV, 64>(blockIdx.x, lds, q, k, d_o, dS_T, seqs, N, Hk, Hv, rec_base, dS_keep,
-                           F_keep, dS0);
-}
-
-// Neither chain needs anything of the other: where few pairs leave compute units
-// idle one launch runs both, the longer reverse chains first, on 32 columns each
-// (seven packed sequences of 8 heads, the longest 2500 tokens: MEASURED).
-template <int DK, int DV>
-__global__ __launch_bounds__(128 + kThreads, 2) void chains_kernel(
+// Neither chain needs anything of the other, so one launch runs both, the longer
+// reverse chains first: compute units that few pairs or a few long sequences
+// leave idle take the other chain's.  Seven packed sequences of 8 heads, the
+// longest 2500 tokens, 92 us (81 + 91 one after the other); ten of 16 heads, the
+// longest 8192, 950 us a backward against 1220; the layer of 8 x 4096 tokens and
+// 16 heads, which fills the card, 546 us (240 + 303) for 2.7 GB (4.9 TB/s).
+template <int DK, int DV, int BV>
+__global__ __launch_bounds__(4 * BV + kThreads, 2) void chains_kernel(
     const __hip_bfloat16 *__restrict__ q, const __hip_bfloat16 *__restrict__ k,
     const __hip_bfloat16 *__restrict__ v, const __hip_bfloat16 *__restrict__ d_o,
     const float *__restrict__ S0, const float *__restrict__ dS_T, Seqs seqs, int N, int Hk, int Hv,
@@ -347,10 +340,10 @@ __global__ __launch_bounds__(128 + kThreads, 2) void chains_kernel(
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const int half = gridDim.x / 2, b = blockIdx.x;
   if (b < half)
-    reverse_body<DK, DV, 32>(b, lds, q, k, d_o, dS_T, seqs, N, Hk, Hv, rec_base, dS_keep, F_keep,
+    reverse_body<DK, DV, BV>(b, lds, q, k, d_o, dS_T, seqs, N, Hk, Hv, rec_base, dS_keep, F_keep,
                              dS0);
   else
-    chain_body<DK, DV, 32, true>(b - half, lds, q, k, v, S0, seqs, N, Hk, Hv, rec_base, nullptr,
+    chain_body<DK, DV, BV, true>(b - half, lds, q, k, v, S0, seqs, N, Hk, Hv, rec_base, nullptr,
                                  nullptr, S_keep, U_keep, false);
 }
 
@@ -757,42 +750,45 @@ __global__ __launch_bounds__(kThreads, 2) void grad_kernel(
   }
 }
 
+template <typename F> hipError_t allow_lds(F *f, int bytes) {
+  return hipFuncSetAttribute(reinterpret_cast<const void *>(f),
+                             hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+template <int DK, int DV, int BV>
+hipError_t launch_chains(const GdrBwdArgs &a, const char *rec, char *S, char *U, char *dS, char *F,
+                         hipStream_t st) {
+  const GdrArgs &f = a.fwd;
+  constexpr int r = ReverseLds<DK, BV>::kBytes, c = ChainLds<DK, BV, true>::kBytes;
+  constexpr int lds = r > c ? r : c;
+  auto *kernel = chains_kernel<DK, DV, BV>;
+  if (hipError_t e = allow_lds(kernel, lds); e != hipSuccess) return e;
+  hipLaunchKernelGGL(kernel, dim3(2 * chain_grid(f.N * f.Hv, DV / BV)), dim3(4 * BV + kThreads),
+                     lds, st, static_cast<const __hip_bfloat16 *>(f.q),
+                     static_cast<const __hip_bfloat16 *>(f.k),
+                     static_cast<const __hip_bfloat16 *>(f.v),
+                     static_cast<const __hip_bfloat16 *>(a.d_o), f.S0, a.dS_T, f.seqs, f.N, f.Hk,
+                     f.Hv, rec, S, U, dS, F, a.dS0);
+  return hipGetLastError();
+}
+
 template <int DK, int DV> hipError_t backward_typed(const GdrBwdArgs &a, hipStream_t st) {
   const GdrArgs &f = a.fwd;
   const auto *q = static_cast<const __hip_bfloat16 *>(f.q);
   const auto *k = static_cast<const __hip_bfloat16 *>(f.k);
-  const auto *v = static_cast<const __hip_bfloat16 *>(f.v);
   const auto *d_o = static_cast<const __hip_bfloat16 *>(a.d_o);
   char *rec = static_cast<char *>(a.rec), *S = static_cast<char *>(a.S);
   char *U = static_cast<char *>(a.U), *dS = static_cast<char *>(a.dS);
   char *F = static_cast<char *>(a.F);
-  hipError_t e = launch_gdr_keep(f, rec, S, U, st);
+  hipError_t e = launch_gdr_prepare_backward(f, rec, st);
   if (e != hipSuccess) return e;
-  auto lds_of = [](auto *kernel, int bytes) {
-    return hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
-                               hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  };
-  const int pairs = f.N * f.Hv;
-  if (chain_columns(pairs, DV) == 64) {
-    constexpr int lds = ReverseLds<DK, 64>::kBytes;
-    auto *kernel = reverse_kernel<DK, DV>;
-    if ((e = lds_of(kernel, lds)) != hipSuccess) return e;
-    hipLaunchKernelGGL(kernel, dim3(chain_grid(pairs, DV / 64)), dim3(2 * kThreads), lds, st, q, k,
-                       d_o, a.dS_T, f.seqs, f.N, f.Hk, f.Hv, rec, dS, F, a.dS0);
-  } else {
-    constexpr int r = ReverseLds<DK, 32>::kBytes, c = ChainLds<DK, 32, true>::kBytes;
-    constexpr int lds = r > c ? r : c;
-    auto *kernel = chains_kernel<DK, DV>;
-    if ((e = lds_of(kernel, lds)) != hipSuccess) return e;
-    hipLaunchKernelGGL(kernel, dim3(2 * chain_grid(pairs, DV / 32)), dim3(128 + kThreads), lds, st,
-                       q, k, v, d_o, f.S0, a.dS_T, f.seqs, f.N, f.Hk, f.Hv, rec, S, U, dS, F,
-                       a.dS0);
-  }
-  if ((e = hipGetLastError()) != hipSuccess) return e;
+  e = chain_columns(f.N * f.Hv, DV) == 64 ? launch_chains<DK, DV, 64>(a, rec, S, U, dS, F, st)
+                                          : launch_chains<DK, DV, 32>(a, rec, S, U, dS, F, st);
+  if (e != hipSuccess) return e;
   if (f.n_chunks_ub == 0) return hipSuccess;
   auto *gr = grad_kernel<DK, DV>;
   constexpr int gl = GradLds<DK, DV>::kBytes;
-  if ((e = lds_of(gr, gl)) != hipSuccess) return e;
+  if ((e = allow_lds(gr, gl)) != hipSuccess) return e;
   hipLaunchKernelGGL(gr, dim3((unsigned)(f.n_chunks_ub * f.Hk)), dim3(kThreads), gl, st, q, k, f.g,
                      f.beta, d_o, f.seqs, f.N, f.Hk, f.Hv, rec, S, U, dS, F,
                      static_cast<__hip_bfloat16 *>(a.dq), static_cast<__hip_bfloat16 *>(a.dk),

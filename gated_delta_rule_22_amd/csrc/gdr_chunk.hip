@@ -241,75 +241,59 @@ __global__ __launch_bounds__(kThreads) void prepare_kernel(
     }
 }
 
-template <int DK, int DV, int BV, bool STORE>
+template <int DK, int DV, int BV>
 __global__ __launch_bounds__(4 * BV + kThreads, 2) void chain_kernel(
     const __hip_bfloat16 *__restrict__ q, const __hip_bfloat16 *__restrict__ k,
     const __hip_bfloat16 *__restrict__ v, const float *__restrict__ S0, Seqs seqs, int N,
     int Hk, int Hv, const char *__restrict__ rec_base, __hip_bfloat16 *__restrict__ o,
-    float *__restrict__ S_T, char *__restrict__ S_keep, char *__restrict__ U_keep,
-    bool by_lengths) {
+    float *__restrict__ S_T, bool by_lengths) {
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  chain_body<DK, DV, BV, STORE>(blockIdx.x, lds, q, k, v, S0, seqs, N, Hk, Hv, rec_base, o, S_T,
-                                S_keep, U_keep, by_lengths);
+  chain_body<DK, DV, BV, false>(blockIdx.x, lds, q, k, v, S0, seqs, N, Hk, Hv, rec_base, o, S_T,
+                                nullptr, nullptr, by_lengths);
 }
 
-template <typename F> hipError_t allow_lds(F *f, int bytes) {
-  return hipFuncSetAttribute(reinterpret_cast<const void *>(f),
-                             hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-}
-
-template <int DK, int DV, int BV, bool STORE>
-hipError_t launch_chain(const GdrArgs &a, char *rec, char *S, char *U, bool by_lengths,
-                        hipStream_t st) {
-  constexpr int lds = ChainLds<DK, BV, STORE>::kBytes;
-  auto *kernel = chain_kernel<DK, DV, BV, STORE>;
-  if (hipError_t e = allow_lds(kernel, lds); e != hipSuccess) return e;
+template <int DK, int DV, int BV>
+hipError_t launch_chain(const GdrArgs &a, const char *rec, bool by_lengths, hipStream_t st) {
+  constexpr int lds = ChainLds<DK, BV, false>::kBytes;
+  auto *kernel = chain_kernel<DK, DV, BV>;
+  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  if (e != hipSuccess) return e;
   hipLaunchKernelGGL(kernel, dim3(chain_grid(a.N * a.Hv, DV / BV)), dim3(4 * BV + kThreads), lds, st,
                      static_cast<const __hip_bfloat16 *>(a.q),
                      static_cast<const __hip_bfloat16 *>(a.k),
                      static_cast<const __hip_bfloat16 *>(a.v), a.S0, a.seqs, a.N, a.Hk, a.Hv, rec,
-                     static_cast<__hip_bfloat16 *>(a.o), a.S_T, S, U, by_lengths);
+                     static_cast<__hip_bfloat16 *>(a.o), a.S_T, by_lengths);
   return hipGetLastError();
 }
 
-// prepare, then the chain; with STORE it keeps S and U and makes no output, and
-// the chain on 32 columns is the caller's.
-template <int DK, int DV, bool STORE>
-hipError_t forward_typed(const GdrArgs &a, char *rec, char *S, char *U, hipStream_t st) {
-  const auto *q = static_cast<const __hip_bfloat16 *>(a.q);
-  const auto *k = static_cast<const __hip_bfloat16 *>(a.k);
-  if (a.n_chunks_ub > 0) {
-    hipLaunchKernelGGL((prepare_kernel<DK, STORE>),
-                       dim3((unsigned)(a.n_chunks_ub * ((a.Hv + 3) / 4))), dim3(kThreads), 0, st,
-                       q, k, a.g, a.beta, a.seqs, a.N, a.Hk, a.Hv, rec);
-    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-  }
+template <int DK, bool BWD> hipError_t prepare(const GdrArgs &a, char *rec, hipStream_t st) {
+  if (a.n_chunks_ub == 0) return hipSuccess;
+  hipLaunchKernelGGL((prepare_kernel<DK, BWD>),
+                     dim3((unsigned)(a.n_chunks_ub * ((a.Hv + 3) / 4))), dim3(kThreads), 0, st,
+                     static_cast<const __hip_bfloat16 *>(a.q),
+                     static_cast<const __hip_bfloat16 *>(a.k), a.g, a.beta, a.seqs, a.N, a.Hk, a.Hv,
+                     rec);
+  return hipGetLastError();
+}
+
+template <int DK, int DV>
+hipError_t forward_typed(const GdrArgs &a, char *rec, hipStream_t st) {
+  if (hipError_t e = prepare<DK, false>(a, rec, st); e != hipSuccess) return e;
   const bool few = chain_columns(a.N * a.Hv, DV) == 32;
   // Packed sequences that are many, but of which a few may be long: the lengths
   // say on the device which of the two kernels runs, and the other one ends at
-  // once (ten sequences, the longest 8192 tokens, of 16 heads of 128 x 128: 289
+  // once (ten sequences, the longest 8192 tokens, of 16 heads of 128 x 128: 280
   // against 336 us).  Both are launched where the order by length is known, and
   // where the longest can have so many chunks that their 0.35 us each pay for the
   // 4 us of the other launch: 64 chunks in all.
-  const bool by_lengths = !STORE && !few && a.seqs.T < 0 && a.N <= kRankedSeqs &&
+  const bool by_lengths = !few && a.seqs.T < 0 && a.N <= kRankedSeqs &&
                           a.n_chunks_ub >= 64 + (size_t)a.N;
-  if constexpr (STORE) {
-    if (few) return hipSuccess;
-  } else if (few || by_lengths) {
-    const hipError_t e = launch_chain<DK, DV, 32, STORE>(a, rec, S, U, by_lengths, st);
+  if (few || by_lengths) {
+    const hipError_t e = launch_chain<DK, DV, 32>(a, rec, by_lengths, st);
     if (e != hipSuccess || few) return e;
   }
-  return launch_chain<DK, DV, 64, STORE>(a, rec, S, U, by_lengths, st);
-}
-
-template <bool STORE>
-hipError_t forward_any(const GdrArgs &a, void *rec, void *S, void *E, hipStream_t st) {
-  char *r = static_cast<char *>(rec), *s = static_cast<char *>(S), *e = static_cast<char *>(E);
-  if (a.dk == 64)
-    return a.dv == 64 ? forward_typed<64, 64, STORE>(a, r, s, e, st)
-                      : forward_typed<64, 128, STORE>(a, r, s, e, st);
-  return a.dv == 64 ? forward_typed<128, 64, STORE>(a, r, s, e, st)
-                    : forward_typed<128, 128, STORE>(a, r, s, e, st);
+  return launch_chain<DK, DV, 64>(a, rec, by_lengths, st);
 }
 
 }  // namespace
@@ -317,10 +301,14 @@ hipError_t forward_any(const GdrArgs &a, void *rec, void *S, void *E, hipStream_
 size_t gdr_forward_rec_bytes() { return kRecFwd; }
 
 hipError_t launch_gdr_forward(const GdrArgs &a, void *rec, hipStream_t stream) {
-  return forward_any<false>(a, rec, nullptr, nullptr, stream);
+  char *r = static_cast<char *>(rec);
+  if (a.dk == 64)
+    return a.dv == 64 ? forward_typed<64, 64>(a, r, stream) : forward_typed<64, 128>(a, r, stream);
+  return a.dv == 64 ? forward_typed<128, 64>(a, r, stream) : forward_typed<128, 128>(a, r, stream);
 }
-hipError_t launch_gdr_keep(const GdrArgs &a, void *rec, void *S, void *E, hipStream_t stream) {
-  return forward_any<true>(a, rec, S, E, stream);
+hipError_t launch_gdr_prepare_backward(const GdrArgs &a, void *rec, hipStream_t stream) {
+  char *r = static_cast<char *>(rec);
+  return a.dk == 64 ? prepare<64, true>(a, r, stream) : prepare<128, true>(a, r, stream);
 }
 
 }  // namespace ckda
