@@ -296,16 +296,12 @@ __device__ __forceinline__ void reverse_body(
     fence_schedule();
     lds_barrier();                       // B
     fence_schedule();
-    p = F_keep + (((c0 + c) * Hv + hv) * (4 * (DV / 16)) + col / 16) * kFrag + lane * 16;
-    const Split f0 = split8(F[0], F[1]), f1 = split8(F[2], F[3]);
-    *reinterpret_cast<bf8 *>(p) = f0.hi;
-    *reinterpret_cast<bf8 *>(p + (DV / 16) * kFrag) = f1.hi;
-    *reinterpret_cast<bf8 *>(p + 2 * (DV / 16) * kFrag) = f0.lo;
-    *reinterpret_cast<bf8 *>(p + 3 * (DV / 16) * kFrag) = f1.lo;
+    f4 W[4];
 #pragma unroll
-    for (int jt = 0; jt < 4; ++jt) F[jt] *= -gam[jt];
+    for (int jt = 0; jt < 4; ++jt) W[jt] = F[jt] * -gam[jt];
     fetch_gates(max(c - 1, 0));
-    const Split w0 = split8(F[0], F[1]), w1 = split8(F[2], F[3]);
+    const Split w0 = split8(W[0], W[1]), w1 = split8(W[2], W[3]);
+    fence_schedule();
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
@@ -315,6 +311,13 @@ __device__ __forceinline__ void reverse_body(
           const Split &w = ks ? w1 : w0;
           S[i] = mfma(kt[ks][i], term ? w.lo : w.hi, S[i]);
         }
+    // F's terms, while the products run
+    p = F_keep + (((c0 + c) * Hv + hv) * (4 * (DV / 16)) + col / 16) * kFrag + lane * 16;
+    const Split f0 = split8(F[0], F[1]), f1 = split8(F[2], F[3]);
+    *reinterpret_cast<bf8 *>(p) = f0.hi;
+    *reinterpret_cast<bf8 *>(p + (DV / 16) * kFrag) = f1.hi;
+    *reinterpret_cast<bf8 *>(p + 2 * (DV / 16) * kFrag) = f0.lo;
+    *reinterpret_cast<bf8 *>(p + 3 * (DV / 16) * kFrag) = f1.lo;
   }
   if (dS0)
 #pragma unroll
@@ -327,7 +330,7 @@ __device__ __forceinline__ void reverse_body(
 // Neither chain needs anything of the other, so one launch runs both, the longer
 // reverse chains first: compute units that few pairs or a few long sequences
 // leave idle take the other chain's.  Seven packed sequences of 8 heads, the
-// longest 2500 tokens, 92 us (81 + 91 one after the other); ten of 16 heads, the
+// longest 2500 tokens, 89 us (81 + 91 one after the other); ten of 16 heads, the
 // longest 8192, 950 us a backward against 1220; the layer of 8 x 4096 tokens and
 // 16 heads, which fills the card, 546 us (240 + 303) for 2.7 GB (4.9 TB/s).
 template <int DK, int DV, int BV>

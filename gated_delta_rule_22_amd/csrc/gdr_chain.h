@@ -272,7 +272,7 @@ __device__ __forceinline__ void chain_body(
     for (int i = 0; i < MT; ++i) kt[1][i] = cols_frag<DK>(K, 32, 16 * i, lane);
 #pragma unroll
     for (int it = 0; it < 4; ++it) U[it] *= bet[it];
-    {
+    auto put_u = [&]() {                 // U's terms, for the helpers or for the backward
       const Split u0 = split8(U[0], U[1]), u1 = split8(U[2], U[3]);
       char *p = STORE ? U_keep + (((c0 + c) * Hv + hv) * (4 * (DV / 16)) + col / 16) * kFrag +
                             lane * 16
@@ -282,14 +282,17 @@ __device__ __forceinline__ void chain_body(
       *reinterpret_cast<bf8 *>(p + step) = u1.hi;
       *reinterpret_cast<bf8 *>(p + 2 * step) = u0.lo;
       *reinterpret_cast<bf8 *>(p + 3 * step) = u1.lo;
-    }
+    };
+    if (!STORE) put_u();
     fence_schedule();
     lds_barrier();                       // B
     fence_schedule();
+    f4 W[4];
 #pragma unroll
-    for (int it = 0; it < 4; ++it) U[it] *= last[it];
+    for (int it = 0; it < 4; ++it) W[it] = U[it] * last[it];
     fetch_gates(min(c + 1, chunks - 1));
-    const Split w0 = split8(U[0], U[1]), w1 = split8(U[2], U[3]);
+    const Split w0 = split8(W[0], W[1]), w1 = split8(W[2], W[3]);
+    fence_schedule();
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
@@ -299,6 +302,7 @@ __device__ __forceinline__ void chain_body(
           const Split &w = ks ? w1 : w0;
           S[i] = mfma(kt[ks][i], term ? w.lo : w.hi, S[i]);
         }
+    if (STORE) put_u();                  // while the products run
   }
   if (S_T)
 #pragma unroll
