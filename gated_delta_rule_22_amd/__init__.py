@@ -9,8 +9,8 @@ from . import workloads  # noqa: F401  (seeded input generators; no GPU needed)
 
 _BINDING = ("forward", "kda_forward", "backward", "decode_step", "forward_workspace_bytes",
             "backward_workspace_bytes", "gdr_forward", "gdr_backward", "gdr_decode_step",
-            "gdr_forward_workspace_bytes", "gdr_backward_workspace_bytes", "qk_norm_rotary", "qk_norm_rotary_backward", "rotary",
-            "rotary_frequencies", "library", "CkdaError")
+            "gdr_forward_workspace_bytes", "gdr_backward_workspace_bytes", "qk_norm_rotary",
+            "qk_norm_rotary_backward", "rotary", "rotary_frequencies", "library", "CkdaError")
 
 __all__ = [*_BINDING, "workloads"]
 

@@ -122,6 +122,33 @@ def test_replays_are_the_eager_call(name, dtype):
         torch.cuda.synchronize()
 
 
+def test_replays_with_other_lengths():
+    """The offsets are read on the device: a captured call serves even and uneven batches, which
+    take their columns differently, and empty ones."""
+    n, T = 9, 4608
+    x = seq(21, BF, lens=[512] * n, hk=4, hv=16, dk=64)
+    five = [x[m] for m in ("q", "k", "v", "g", "beta")]
+    cu = torch.zeros(n + 1, dtype=torch.int32, device="cuda")
+    batches = [[512] * n, [4500] + [1] * 8, [0] * 8 + [T], [0] * n, [700, 3, 0, 64, 1000, 1, 900, 65, 1875]]
+
+    def fill(lens):
+        cu.copy_(torch.tensor([0] + lens).cumsum(0).to(torch.int32))
+
+    def call(_):
+        o = torch.zeros_like(x["v"])     # rows outside every sequence stay as they are
+        return ck.gdr_forward(*five, S0=x["S0"], cu_seqlens=cu, out=o)
+
+    fill(batches[0])
+    graph, got = capture(call, None)
+    for lens in batches + batches[:1]:
+        fill(lens)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        same(tuple(outputs(got)), call(None), lens)
+        torch.cuda.synchronize()
+
+
 @pytest.mark.parametrize("name", ["forward", "backward", "prepare_back"])
 def test_two_graphs_at_once(name):
     """Two captured graphs of one call, each with its own workspace, replayed on two streams."""
