@@ -37,7 +37,9 @@ __device__ __forceinline__ bool chain_block(int b, int nblk, int pairs, int &pai
 // rate).  Tried and slower: operands a whole chunk ahead (255 us, too many
 // registers), half of the products with the state behind barrier B with K and Q
 // twice in LDS (217), U's terms and barrier B behind the products of the next
-// state (238: the helpers wait), rows padded instead of the swizzle (+15%).
+// state (238: the helpers wait), barrier B before U and the output behind the
+// next A on 32 columns (296 against 281 on ten packed sequences), rows padded
+// instead of the swizzle (+15%).
 template <int DK, int BV, bool STORE> struct ChainLds {
   static constexpr int kK = 0, kV = gdr::kTile<DK>, kRec = kV + gdr::kTile<BV>;
   static constexpr int kQ = kRec + kRecFwd;                      // the rest: !STORE
